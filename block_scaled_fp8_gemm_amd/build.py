@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8bg.so")
-SOURCES = ["fp8bg_api.hip", "fp8bg_kernels.hip", "fp8bg_quant.hip", "fp8bg_plan.cpp"]
+SOURCES = ["fp8bg_api.hip", "fp8bg_kernels.hip", "fp8bg_quant.hip", "fp8bg_int8.hip", "fp8bg_rows.hip",
+           "fp8bg_plan.cpp"]
 PROBE_LIB = os.path.join(PKG, "libfp8bg_probe.so")
 PROBE_SOURCES = ["fp8bg_probe.hip"]
 ARCH = "gfx950"

@@ -378,3 +378,177 @@ extern "C" int fp8_block_gemm_grouped(const void* A, const float* a_s, const voi
                                                          (int)E);
   return e == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }
+
+// ---------------------------------------------------------------------------
+// 8-bit integers, and the row operators that feed them.
+// ---------------------------------------------------------------------------
+namespace {
+
+// int32 sums of products of int8 codes, -128 included: 2^14 * K < 2^31.
+constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 1;
+
+// Bytes from the first element of `rows` rows of `cols` elements, `ld` apart,
+// to the end of the last one; false if that overflows.
+bool extent(int64_t rows, int64_t cols, int64_t ld, int64_t size, int64_t* bytes) {
+  *bytes = 0;
+  if (rows <= 0 || cols <= 0) return true;
+  int64_t n = 0;
+  return !__builtin_mul_overflow(rows - 1, ld, &n) && !__builtin_add_overflow(n, cols, &n) &&
+         !__builtin_mul_overflow(n, size, bytes);
+}
+
+bool known_dtype(int d) { return d == FBG_OUT_BF16 || d == FBG_OUT_FP16 || d == FBG_OUT_FP32; }
+
+int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb, const float* b_s,
+              const float* bias, void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N,
+              int64_t K, int out_dtype, bool grouped, void* stream) {
+  if (E < 0 || M < 0 || N < 0 || K < 0 || !known_dtype(out_dtype)) return FBG_ERROR_INVALID_VALUE;
+  if (M > INT32_MAX || N > INT32_MAX || K > kMaxInt8K || E > INT32_MAX - 1) return FBG_ERROR_UNSUPPORTED;
+  const bool many_b = N > 1 || (grouped && E > 1);
+  if ((M > 1 && lda < K) || (many_b && ldb < K) || (M > 1 && ldc < N)) return FBG_ERROR_INVALID_VALUE;
+  if (M <= 1) lda = K, ldc = N;  // the pitch of a single row says nothing
+  if (!many_b) ldb = K;
+  if (lda > kMaxK || ldb > kMaxK) return FBG_ERROR_UNSUPPORTED;  // 32-bit offsets inside a tile's rows
+  const int64_t es = elem_size(out_dtype);
+  int64_t rows_b = 0, bytesA = 0, bytesB = 0, bytesC = 0, bytesBs = 0;
+  if (__builtin_mul_overflow(E, N, &rows_b) || !extent(M, K, lda, 1, &bytesA) || !extent(rows_b, K, ldb, 1, &bytesB) ||
+      !extent(M, N, ldc, es, &bytesC) || __builtin_mul_overflow(rows_b, (int64_t)4, &bytesBs))
+    return FBG_ERROR_UNSUPPORTED;
+  const int64_t bytesAs = M * 4, bytesOff = grouped ? (E + 1) * 4 : 0;
+  if (M == 0 || N == 0) return FBG_SUCCESS;
+  if ((bytesA > 0 && !A) || (bytesB > 0 && !B) || !a_s || (bytesBs > 0 && !b_s) || !C || (grouped && E > 0 && !offsets))
+    return FBG_ERROR_INVALID_VALUE;
+  if (overlaps(C, bytesC, A, bytesA) || overlaps(C, bytesC, B, bytesB) || overlaps(C, bytesC, a_s, bytesAs) ||
+      overlaps(C, bytesC, b_s, bytesBs) || overlaps(C, bytesC, bias, N * 4) || overlaps(C, bytesC, offsets, bytesOff))
+    return FBG_ERROR_INVALID_VALUE;
+  if (!aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(bias, 4) || !aligned(offsets, 4) || !aligned(C, (uintptr_t)es))
+    return FBG_ERROR_UNSUPPORTED;
+
+  fbg::I8Args args;
+  args.A = static_cast<const uint8_t*>(A);
+  args.a_s = a_s;
+  args.B = static_cast<const uint8_t*>(B);
+  args.b_s = b_s;
+  args.bias = bias;
+  args.C = C;
+  args.offsets = grouped ? offsets : nullptr;
+  args.lda = lda;
+  args.ldb = ldb;
+  args.ldc = ldc;
+  args.M = (int)M;
+  args.N = (int)N;
+  args.K = grouped && E == 0 ? 0 : (int)K;
+  args.E = (int)E;
+  args.out = out_dtype;
+  args.vec = (ldc % 4 == 0) && aligned(C, (uintptr_t)(4 * es));
+  if (args.vec && (ldc * es) % 16 == 0 && aligned(C, 16)) args.vec |= 2;  // 16-byte rows
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_i8(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}
+
+}  // namespace
+
+extern "C" int fbg_int8_gemm(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb,
+                             const float* b_s, const float* bias, void* C, int64_t ldc, int64_t M, int64_t N,
+                             int64_t K, int out_dtype, void* stream) {
+  return int8_call(A, lda, a_s, B, ldb, b_s, bias, C, ldc, nullptr, 1, M, N, K, out_dtype, false, stream);
+}
+
+extern "C" int fbg_int8_grouped_gemm(const void* A, int64_t lda, const float* a_s, const void* B, const float* b_s,
+                                     void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N,
+                                     int64_t K, int out_dtype, void* stream) {
+  return int8_call(A, lda, a_s, B, K, b_s, nullptr, C, ldc, offsets, E, M, N, K, out_dtype, true, stream);
+}
+
+extern "C" int fbg_quantize_tokens(const void* x, int64_t ldx, int in_dtype, int64_t M, int64_t K, void* q,
+                                   int64_t ldq, float* scale, void* stream) {
+  if (M < 0 || K < 0 || !known_dtype(in_dtype)) return FBG_ERROR_INVALID_VALUE;
+  if (M > INT32_MAX || K > INT32_MAX) return FBG_ERROR_UNSUPPORTED;
+  if (M > 1 && (ldx < K || ldq < K)) return FBG_ERROR_INVALID_VALUE;
+  if (M <= 1) ldx = K, ldq = K;
+  const int64_t es = elem_size(in_dtype);
+  int64_t bytesX = 0, bytesQ = 0;
+  if (!extent(M, K, ldx, es, &bytesX) || !extent(M, K, ldq, 1, &bytesQ)) return FBG_ERROR_UNSUPPORTED;
+  if (M == 0) return FBG_SUCCESS;
+  if ((bytesX > 0 && !x) || (bytesQ > 0 && !q) || !scale) return FBG_ERROR_INVALID_VALUE;
+  if (overlaps(q, bytesQ, x, bytesX) || overlaps(scale, M * 4, x, bytesX) || overlaps(scale, M * 4, q, bytesQ))
+    return FBG_ERROR_INVALID_VALUE;
+  if (!aligned(x, (uintptr_t)es) || !aligned(scale, 4)) return FBG_ERROR_UNSUPPORTED;
+  fbg::QuantArgs args;
+  args.x = x;
+  args.q = static_cast<int8_t*>(q);
+  args.scale = scale;
+  args.ldx = ldx;
+  args.ldq = ldq;
+  args.M = (int)M;
+  args.K = (int)K;
+  args.dtype = in_dtype;
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_quantize_tokens(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}
+
+extern "C" int fbg_block_norm(const void* h, int64_t ldh, const void* x, int64_t ldx, const void* gate,
+                              int64_t gate_row, int64_t gate_col, const void* post, const void* pre, int dtype,
+                              int weight_dtype, int64_t M, int64_t D, float residual_scale, float eps,
+                              float weight_offset, void* r, int64_t ldr, void* y, int64_t ldy, float* y_scale,
+                              int quantize, void* stream) {
+  if (M < 0 || D < 0 || gate_row < 0 || gate_col < 0 || !known_dtype(dtype) ||
+      (weight_dtype != dtype && weight_dtype != FBG_OUT_FP32) || quantize < FBG_QUANT_NONE || quantize > FBG_QUANT_FP8)
+    return FBG_ERROR_INVALID_VALUE;
+  if (M > INT32_MAX || D > INT32_MAX) return FBG_ERROR_UNSUPPORTED;
+  if (pre && quantize == FBG_QUANT_FP8 && D % 128 != 0) return FBG_ERROR_UNSUPPORTED;
+  if (M > 1 && (ldh < D || (x && ldx < D) || ldr < D || (pre && ldy < D))) return FBG_ERROR_INVALID_VALUE;
+  if (M <= 1) ldh = ldx = ldr = ldy = D;
+  if (M == 0 || D == 0) return FBG_SUCCESS;
+  const int64_t es = elem_size(dtype), ws = elem_size(weight_dtype), ys = quantize == FBG_QUANT_NONE ? es : 1;
+  const int64_t bytesS = quantize == FBG_QUANT_NONE ? 0 : quantize == FBG_QUANT_INT8 ? M * 4 : M * (D / 128) * 4;
+  int64_t bytesH = 0, bytesX = 0, bytesR = 0, bytesY = 0, bytesG = 0, g0 = 0, g1 = 0;
+  if (!extent(M, D, ldh, es, &bytesH) || !extent(M, D, ldx, es, &bytesX) || !extent(M, D, ldr, es, &bytesR) ||
+      !extent(M, D, ldy, ys, &bytesY) || __builtin_mul_overflow(M - 1, gate_row, &g0) ||
+      __builtin_mul_overflow(D - 1, gate_col, &g1) || __builtin_add_overflow(g0, g1, &g0) ||
+      __builtin_add_overflow(g0, (int64_t)1, &g0) || __builtin_mul_overflow(g0, es, &bytesG))
+    return FBG_ERROR_UNSUPPORTED;
+  if (!h || !r || (pre && !y) || (pre && bytesS > 0 && !y_scale)) return FBG_ERROR_INVALID_VALUE;
+  if (!pre) y = nullptr, y_scale = nullptr;
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  const Range in[] = {{h, bytesH}, {x, bytesX}, {gate, bytesG}, {post, D * ws}, {pre, D * ws}};
+  const Range out[] = {{r, bytesR}, {y, bytesY}, {y_scale, bytesS}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& b : in)
+      if (overlaps(out[i].p, out[i].bytes, b.p, b.bytes)) return FBG_ERROR_INVALID_VALUE;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return FBG_ERROR_INVALID_VALUE;
+  }
+  const uintptr_t ea = (uintptr_t)es;
+  if (!aligned(h, ea) || !aligned(x, ea) || !aligned(gate, ea) || !aligned(r, ea) || !aligned(y, (uintptr_t)ys) ||
+      !aligned(post, (uintptr_t)ws) || !aligned(pre, (uintptr_t)ws) || !aligned(y_scale, 4))
+    return FBG_ERROR_UNSUPPORTED;
+  fbg::NormArgs args;
+  args.h = h;
+  args.x = x;
+  args.gate = gate;
+  args.post = post;
+  args.pre = pre;
+  args.r = r;
+  args.y = y;
+  args.y_scale = y_scale;
+  args.ldh = ldh;
+  args.ldx = ldx;
+  args.ldr = ldr;
+  args.ldy = ldy;
+  args.gate_row = gate_row;
+  args.gate_col = gate_col;
+  args.M = (int)M;
+  args.D = (int)D;
+  args.dtype = dtype;
+  args.wdtype = weight_dtype;
+  args.quant = quantize;
+  args.residual_scale = residual_scale;
+  args.eps = eps;
+  args.weight_offset = weight_offset;
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_block_norm(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}

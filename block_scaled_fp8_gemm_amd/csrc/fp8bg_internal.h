@@ -55,6 +55,54 @@ hipError_t launch_grouped(const GemmArgs& a, int cfg, int64_t grid, const int* o
 hipError_t launch_generic_grouped(const GemmArgs& a, int cfg, int64_t grid, const int* offsets, int E);
 hipError_t launch_quantize_rows(const uint16_t* x, uint8_t* q, float* a_s, int64_t groups, hipStream_t stream);
 hipError_t launch_quantize_blocks(const uint16_t* w, uint8_t* q, float* b_s, int N, int K, hipStream_t stream);
+
+// The int8 products (fp8bg_int8.hip): rows of A, B and C lda, ldb, ldc
+// elements apart.  offsets: the grouped form (B [E,N,ldb], b_s [E,N]), else null.
+struct I8Args {
+  const uint8_t* A;
+  const float* a_s;
+  const uint8_t* B;
+  const float* b_s;
+  const float* bias;  // [N], or null
+  void* C;
+  const int* offsets;
+  int64_t lda, ldb, ldc;
+  int M, N, K, E;
+  int out;
+  int vec;  // as GemmArgs::vec, with ldc for the row pitch
+  hipStream_t stream;
+};
+hipError_t launch_i8(const I8Args& a);
+
+// One row per token (fp8bg_rows.hip).  dtype: the FBG_OUT_* code of x, h,
+// gate and r; rows ld* elements apart.
+struct QuantArgs {
+  const void* x;
+  int8_t* q;
+  float* scale;
+  int64_t ldx, ldq;
+  int M, K;
+  int dtype;
+  hipStream_t stream;
+};
+hipError_t launch_quantize_tokens(const QuantArgs& a);
+
+struct NormArgs {
+  const void* h;
+  const void* x;     // null: no residual
+  const void* gate;  // null: no gate; else element (m, d) at m * gate_row + d * gate_col
+  const void* post;  // null: no norm of h
+  const void* pre;   // null: no second output
+  void* r;
+  void* y;
+  float* y_scale;
+  int64_t ldh, ldx, ldr, ldy, gate_row, gate_col;
+  int M, D;
+  int dtype, wdtype, quant;
+  float residual_scale, eps, weight_offset;
+  hipStream_t stream;
+};
+hipError_t launch_block_norm(const NormArgs& a);
 #endif
 
 }  // namespace fbg

@@ -258,6 +258,102 @@ int fp8_block_gemm_quantize_rows(const void *x, int64_t M, int64_t K, void *A, f
  */
 int fp8_block_gemm_quantize_blocks(const void *w, int64_t N, int64_t K, void *B, float *b_s, void *stream);
 
+/* ===========================================================================
+ * 8-bit integers with one scale per token and one per output channel: the
+ * products, the quantiser that makes their activation operand, and the norms
+ * between two blocks that can quantise on the way out.
+ *
+ * Tensors here are row-major with unit column stride and a row pitch `ld*` in
+ * ELEMENTS (at least the row's length where there is more than one row), so
+ * a slice of the columns of a wider buffer is passed as it is.  Sizes may be
+ * any number >= 0, odd ones included.  Statuses, ownership, streams and
+ * determinism are those of the functions above; no function allocates or
+ * keeps anything, and each may be captured in a HIP graph.
+ * ======================================================================== */
+
+/*
+ * fbg_int8_gemm -- C[m,n] = a_s[m] * b_s[n] * sum_k A[m,k] * B[n,k] (+ bias[n]).
+ *
+ * A [M,K] and B [N,K] int8, a_s [M] and b_s [N] fp32, bias [N] fp32 or NULL,
+ * C [M,N] of out_dtype.  The integer sum is exact; the epilogue is fp32,
+ * fl(fl(a_s*b_s) * fl(sum)) + bias, then one rounding to nearest even.  A and
+ * B may start at any byte and have any pitch; rows that start on 16-byte
+ * boundaries (base and pitch) take the faster loads.  a_s, b_s and bias 4-byte
+ * aligned, C aligned to its element size.  M == 0 or N == 0: nothing launched;
+ * K == 0: C is the bias, or zero.  K > 131071 (the int32 sum could overflow),
+ * M or N above INT32_MAX, or a pitch above 2^24 - 128 for A or B ->
+ * UNSUPPORTED; a pitch below the row's length, a null pointer with a
+ * non-empty extent, an unknown out_dtype or C overlapping an input ->
+ * INVALID_VALUE.
+ */
+int fbg_int8_gemm(const void *A, int64_t lda, const float *a_s, const void *B, int64_t ldb, const float *b_s,
+                  const float *bias, void *C, int64_t ldc, int64_t M, int64_t N, int64_t K, int out_dtype,
+                  void *stream);
+
+/*
+ * fbg_int8_grouped_gemm -- the grouped (mixture-of-experts) form: rows
+ * offsets[e] .. offsets[e+1]-1 of A use expert e's weight and scales:
+ *
+ *     C[m,n] = a_s[m] * b_s[e,n] * sum_k A[m,k] * B[e,n,k]
+ *
+ * B [E,N,K] int8 and b_s [E,N] fp32, contiguous; A, a_s and C as above.
+ * offsets: DEVICE pointer to E+1 int32, as for fp8_block_gemm_grouped: read
+ * by the kernels alone, clamped into [0, M] (malformed offsets leave rows
+ * unwritten or written twice, never address outside the operands), rows of no
+ * expert are not written.  K == 0 or E == 0: C is filled with zeros.
+ */
+int fbg_int8_grouped_gemm(const void *A, int64_t lda, const float *a_s, const void *B, const float *b_s, void *C,
+                          int64_t ldc, const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                          int out_dtype, void *stream);
+
+/*
+ * fbg_quantize_tokens -- per-row symmetric int8 quantisation of x [M,K]
+ * (in_dtype: an FBG_OUT_* code) into q [M,K] int8 and scale [M] fp32:
+ *
+ *     scale[m] = max(max_k |x[m,k]|, 1e-12f) / 127
+ *     q[m,k]   = round to nearest even of clamp(x[m,k] / scale[m], -127, 127)
+ *
+ * with correctly rounded fp32 divisions.  Makes A and a_s from activations,
+ * and B and b_s from weights [N,K].  A row that holds a NaN or an infinity
+ * gets a scale that is one, and code 0 where x / scale is NaN: the products of
+ * that row are NaN.  x aligned to its element size, q at any byte, scale 4-byte aligned.
+ * K == 0: every scale is 1e-12f / 127.
+ */
+int fbg_quantize_tokens(const void *x, int64_t ldx, int in_dtype, int64_t M, int64_t K, void *q, int64_t ldq,
+                        float *scale, void *stream);
+
+/* What fbg_block_norm does with its second output. */
+enum {
+    FBG_QUANT_NONE = 0, /* y in the type of x */
+    FBG_QUANT_INT8 = 1, /* int8, one scale per row: A and a_s of fbg_int8_gemm */
+    FBG_QUANT_FP8 = 2   /* E4M3, one scale per 128 columns: A and a_s of fp8_block_gemm */
+};
+
+/*
+ * fbg_block_norm -- what stands between two blocks of a network, in one pass:
+ * the norm after a block, its gate, the scaled residual, and the norm before
+ * the next block.  With rms(v) = v / sqrt(mean(v^2) + eps) over a row:
+ *
+ *     u = rms(h) * (post + weight_offset)         (u = h where post is NULL)
+ *     r = residual_scale * x + gate * u           (no x term where x is NULL; gate 1 where NULL)
+ *     y = rms(r) * (pre + weight_offset)          (not computed where pre is NULL)
+ *
+ * h, x, gate and r of `dtype` (FBG_OUT_*), post and pre [D] of `weight_dtype`
+ * (`dtype` or fp32).  gate element (m, d) sits at m * gate_row + d * gate_col
+ * elements, so strides of 0 broadcast it: (0,1) per channel, (1,0) per token,
+ * (pitch,1) one value for every element.  All arithmetic in fp32; r is rounded
+ * once, and y is formed from r before that rounding.  y [M,D] by `quantize`:
+ * `dtype`; int8 codes with y_scale [M] by the rule of fbg_quantize_tokens; or
+ * E4M3 codes with y_scale [M, D/128] (contiguous) by the rule of
+ * fp8_block_gemm_quantize_rows (D % 128 == 0, else UNSUPPORTED), both taken
+ * from the fp32 values.  r and y must not overlap an input or each other.
+ * M == 0 or D == 0: nothing launched (int8 with D == 0 leaves y_scale alone).
+ */
+int fbg_block_norm(const void *h, int64_t ldh, const void *x, int64_t ldx, const void *gate, int64_t gate_row,
+                   int64_t gate_col, const void *post, const void *pre, int dtype, int weight_dtype, int64_t M,
+                   int64_t D, float residual_scale, float eps, float weight_offset, void *r, int64_t ldr, void *y,
+                   int64_t ldy, float *y_scale, int quantize, void *stream);
+
 /* fp8_block_gemm_status_string -- static text for a status code. */
 const char *fp8_block_gemm_status_string(int status);
 
