@@ -18,6 +18,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8bg.so")
 SOURCES = ["fp8bg_api.hip", "fp8bg_kernels.hip", "fp8bg_quant.hip", "fp8bg_int8.hip", "fp8bg_rows.hip",
            "fp8bg_plan.cpp"]
+# The FP8 kernels fold every MFMA's result in the vector ALU, so theirs stay in
+# vector registers; the int8 kernels accumulate in the MFMA's own registers.
+MFMA_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+NO_VGPR_FORM = {"fp8bg_int8.hip"}
 PROBE_LIB = os.path.join(PKG, "libfp8bg_probe.so")
 PROBE_SOURCES = ["fp8bg_probe.hip"]
 ARCH = "gfx950"
@@ -33,7 +37,7 @@ def hipcc() -> str:
 def flags():
     return ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-            "-ffp-contract=off", "-mllvm", "-amdgpu-mfma-vgpr-form", "-Wall", "-Wno-unused-function",
+            "-ffp-contract=off", "-Wall", "-Wno-unused-function",
             f"-I{INCLUDE}", f"-I{CSRC}"]
 
 
@@ -51,7 +55,8 @@ def _build_lib(sources, out, verbose: bool, jobs: int) -> str:
     for src in sources:
         obj = os.path.join(objdir, src + ".o")
         lang = ["-x", "hip"] if src.endswith(".cpp") else []
-        cmd = [cc, *flags(), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+        form = [] if src in NO_VGPR_FORM else MFMA_IN_VGPRS
+        cmd = [cc, *flags(), *form, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((subprocess.Popen(cmd), src))

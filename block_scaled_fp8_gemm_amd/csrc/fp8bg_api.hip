@@ -443,7 +443,10 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
   args.vec = (ldc % 4 == 0) && aligned(C, (uintptr_t)(4 * es));
   if (args.vec && (ldc * es) % 16 == 0 && aligned(C, 16)) args.vec |= 2;  // 16-byte rows
   args.stream = static_cast<hipStream_t>(stream);
-  return fbg::launch_i8(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+  const int force = forced_config();
+  const hipError_t err = fbg::launch_i8(args, force);
+  if (err == hipErrorInvalidValue && force >= 0) return FBG_ERROR_UNSUPPORTED;
+  return err == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }
 
 }  // namespace

@@ -16,6 +16,8 @@
 //
 // The grouped (mixture-of-experts) form gives rows offsets[e] ..
 // offsets[e+1]-1 of A the weight B[e]; see expert_of_slot.
+#include <type_traits>
+
 #include "fp8bg_device.hpp"
 #include "fp8bg_internal.h"
 
@@ -37,10 +39,10 @@ __device__ __forceinline__ v4i mfma_i8(const v4i& x, const v4i& y, const v4i& ac
 // at once instead of a prefix sum over tile counts.  Slots past an expert's
 // last tile exit.  There are floor(M / BM) + E slots.
 // Returns whether slot `t` holds rows; all threads of the workgroup call it.
+// `found`: three words of LDS, free again afterwards.
 template <int BM>
 __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, int E, int M, int t, int& e_out,
-                                               int& m0, int& m_end) {
-  __shared__ int found[3];
+                                               int& m0, int& m_end, int* found) {
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -58,6 +60,7 @@ __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, 
   e_out = found[0];
   m0 = found[1];
   m_end = found[2];
+  __syncthreads();
   return e_out >= 0;
 }
 
@@ -107,7 +110,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
   const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
   int m0, n0, m_end = a.M, e = 0;
   if constexpr (GRP) {
-    if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end)) return;
+    if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(smem))) return;
     n0 = (lid % tiles_n) * BN;
   } else {
     int tm, tn;
@@ -190,6 +193,310 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
   }
 }
 
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+// Scales a wave's IB x JB blocks of 32 x 32 sums and stores them.  Block
+// (i, j), element 4q + r of lane l: row m = 32i + (l & 31), column
+// n = 32j + 8q + 4(l >> 5) + r.  Where C's rows are 16-byte aligned and the
+// columns are all there, 32 rows at a time go through the wave's own padded
+// slab of LDS and out as whole row segments, 16 bytes per lane (C is written
+// once and not read back: non-temporal); else 4 outputs per lane.
+//
+// as_t, bs_t, bi_t: the wave's row scales, column scales and bias in LDS
+// (loaded before the K loop: read from memory here, their latency would add
+// to every tile's end).
+template <int OUT, int IB, int JB>
+__device__ __forceinline__ void store_tile(const I8Args& a, const v16i (&acc)[IB][JB], uint8_t* slab,
+                                           const float* as_t, const float* bs_t, const float* bi_t, int lane, int m0,
+                                           int m_end, int n0) {
+  typedef typename Out<OUT>::T T;
+  constexpr int ES = (int)sizeof(T), ROWB = 32 * JB * ES, ROWP = ROWB + 16, PER_ROW = ROWB / 16;
+  const int h = lane >> 5;
+  const bool whole = (a.vec & 2) && n0 + 32 * JB <= a.N;
+#pragma unroll
+  for (int i = 0; i < IB; ++i) {
+    const int m = m0 + 32 * i + (lane & 31);
+    const float as = as_t[32 * i + (lane & 31)];
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = 32 * j + 8 * q + 4 * h;
+        const v4f bs = *reinterpret_cast<const v4f*>(bs_t + col);
+        v4f c;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c[r] = (as * bs[r]) * (float)acc[i][j][4 * q + r];
+        if (a.bias) {
+          const v4f bi = *reinterpret_cast<const v4f*>(bi_t + col);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) c[r] = c[r] + bi[r];
+        }
+        if (whole) {
+          store4<OUT>(slab + (lane & 31) * ROWP, col, c, 4, true);
+        } else {
+          const int cnt = a.N - (n0 + col) < 4 ? a.N - (n0 + col) : 4;
+          if (m < m_end && cnt > 0) store4<OUT>(a.C, (int64_t)m * a.ldc + n0 + col, c, cnt, a.vec & 1);
+        }
+      }
+    if (whole) {
+#pragma unroll
+      for (int t = 0; t < 32 * PER_ROW / 64; ++t) {
+        const int q = t * 64 + lane, row = q / PER_ROW, cb = (q % PER_ROW) * 16;
+        const int mm = m0 + 32 * i + row;
+        if (mm < m_end)
+          __builtin_nontemporal_store(*reinterpret_cast<const v4i*>(slab + row * ROWP + cb),
+                                      reinterpret_cast<v4i*>(reinterpret_cast<uint8_t*>(a.C) +
+                                                             ((int64_t)mm * a.ldc + n0) * ES + cb));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The tile kernel: BM x BN outputs per workgroup, WAVES_M x WAVES_N waves, a
+// STAGES-deep ring of 128-byte K steps in LDS filled by direct-to-LDS loads
+// (16 bytes per lane, so rows start on 16-byte boundaries and K is a multiple
+// of 16).
+//
+// The accumulators stay in the MFMA's own registers for all of K, so a wave
+// can hold 128 x 128 outputs (256 accumulator registers, one wave per SIMD),
+// which halves the LDS reads per product against the 128 x 64 of the FP8
+// kernel: 128 KB of fragments and 64 KB of fills per 2048 MFMA cycles, three
+// quarters of what LDS delivers.
+//
+// A step is 4 slices of 32 K bytes: slice s of a row block is chunk 2s + h of
+// its 32 rows (h = lane >> 5), one 16-byte read per lane.  The fragments of
+// slice s + 1 are read while slice s is multiplied; at the start of the last
+// slice the wave has read all of the step, so that is where it waits for the
+// next step's loads, meets the others, refills the slot with the step STAGES
+// ahead and reads the next step's first fragments.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WAVES_M, int WAVES_N, int BK, int STAGES, int SPREAD, int GRP>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 72 * 1024 ? 2 : 1) void k_i8_tile(I8Args a) {
+  constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
+  constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, IB = WM / 32, JB = WN / 32;
+  constexpr int CH = BK / 16, RI = 64 / CH, SL = BK / 32;           // chunks per row, rows per load image, slices
+  constexpr int AP = BM * CH / NT, BP = BN * CH / NT, LPS = AP + BP;  // loads per thread per step
+  constexpr int A_BYTES = BM * BK, SLOT = (BM + BN) * BK;
+  static_assert(BK == 64 || BK == 128, "");
+  static_assert(BM * CH % NT == 0 && BN * CH % NT == 0, "whole load images per wave");
+  static_assert((NW * RI) % 16 == 0, "a lane's chunk is the same in all its images");
+  static_assert((STAGES - 1) * LPS < 64, "vmcnt counts at most 63 outstanding loads");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[STAGES * SLOT + (BM + 2 * BN) * 4];
+  float* const as_t = reinterpret_cast<float*>(smem + STAGES * SLOT);  // row scales, column scales, bias
+  float* const bs_t = as_t + BM;
+  float* const bi_t = bs_t + BN;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  const int tiles_n = (a.N + BN - 1) / BN;
+  int m0, n0, m_end = a.M, e = 0;
+  {
+    const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+    if constexpr (GRP) {
+      if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(smem))) return;
+      n0 = (lid % tiles_n) * BN;
+    } else {
+      int tm, tn;
+      raster(lid, (a.M + BM - 1) / BM, tiles_n, 8, tm, tn);
+      m0 = tm * BM;
+      n0 = tn * BN;
+    }
+  }
+  // Uniform over the workgroup: in scalar registers, as the buffer resources
+  // have to be.
+  m0 = __builtin_amdgcn_readfirstlane(m0);
+  n0 = __builtin_amdgcn_readfirstlane(n0);
+  m_end = __builtin_amdgcn_readfirstlane(m_end);
+  e = __builtin_amdgcn_readfirstlane(e);
+  const uint8_t* Bt = a.B + (int64_t)e * a.N * a.ldb + (int64_t)n0 * a.ldb;
+  const buf_rsrc rA = make_rsrc(a.A + (int64_t)m0 * a.lda), rB = make_rsrc(Bt);
+  const int nk = (a.K + BK - 1) / BK;
+
+  // Load image q (q = i*NW + wave) fills RI LDS rows of a tile; lane l writes
+  // row q*RI + l / CH, slot l % CH, so it reads the row's chunk
+  // (l % CH) ^ swz(row).  Rows past the matrix are clamped to its last row:
+  // they feed outputs that are never stored.
+  auto swz = [](int r) { return BK == 128 ? swz_row(r) : (r >> 2) & 3; };
+  uint32_t aoff[AP], boff[BP];
+  const int chunk = (lane % CH) ^ swz(RI * wave + lane / CH);
+#pragma unroll
+  for (int i = 0; i < AP; ++i) {
+    const int r = RI * (i * NW + wave) + lane / CH;
+    aoff[i] = (uint32_t)(m0 + r < m_end ? r : m_end - 1 - m0) * (uint32_t)a.lda + 16u * (uint32_t)chunk;
+  }
+#pragma unroll
+  for (int i = 0; i < BP; ++i) {
+    const int r = RI * (i * NW + wave) + lane / CH;
+    boff[i] = (uint32_t)(n0 + r < a.N ? r : a.N - 1 - n0) * (uint32_t)a.ldb + 16u * (uint32_t)chunk;
+  }
+  // In the last step, lanes whose chunk lies past K read the step's first
+  // chunk instead (K % 16 == 0: a chunk is wholly in or out); the fragments'
+  // mask keeps it out of the sums.
+  const uint32_t tail = (nk - 1) * BK + 16 * chunk >= a.K ? 16u * (uint32_t)chunk : 0u;
+  lds_u8* const lds = (lds_u8*)smem;
+  auto load_one = [&](int k, int slot, int i, uint32_t sub) {
+    lds_u8* base = lds + slot * SLOT;
+    if (i < AP) lds_dma16(rA, aoff[i < AP ? i : 0] - sub, k * BK, base + 1024 * (i * NW + wave));
+    else lds_dma16(rB, boff[i < AP ? 0 : i - AP] - sub, k * BK, base + A_BYTES + 1024 * ((i - AP) * NW + wave));
+  };
+
+  // Slice s of row block b: this lane's 16 bytes.
+  const int frow = lane & 31, fh = lane >> 5, fsw = swz(frow);
+  auto frag = [&](int slot, int off, int row0, int s) {
+    return *reinterpret_cast<const v4i*>(smem + slot * SLOT + off + BK * (row0 + frow) + 16 * ((2 * s + fh) ^ fsw));
+  };
+
+  v16i acc[IB][JB];
+#pragma unroll
+  for (int i = 0; i < IB; ++i)
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+  // The scales, loaded ahead of the tiles and put into LDS behind them.
+  constexpr int SA = (BM + NT - 1) / NT, SB = (BN + NT - 1) / NT;
+  float sa[SA], sb[SB], si[SB];
+#pragma unroll
+  for (int i = 0; i < SA; ++i) {
+    const int m = m0 + i * NT + tid;
+    sa[i] = a.a_s[m < m_end ? m : m_end - 1];
+  }
+#pragma unroll
+  for (int i = 0; i < SB; ++i) {
+    const int n = n0 + i * NT + tid < a.N ? n0 + i * NT + tid : a.N - 1;
+    sb[i] = a.b_s[(int64_t)e * a.N + n];
+    si[i] = a.bias ? a.bias[n] : 0.0f;
+  }
+
+  // A step's refill is spread over SPREAD slices, the last one of the step
+  // that frees the slot and the first ones of the step after it: load q goes
+  // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
+  // belong to the first part.
+  constexpr int NM = IB * JB;
+  constexpr int LPS0 = (LPS + SPREAD - 1) / SPREAD;
+#pragma unroll
+  for (int p = 0; p < STAGES; ++p)
+    if (p < nk) {
+      const uint32_t sub = p == nk - 1 ? tail : 0u;
+#pragma unroll
+      for (int i = 0; i < (p < STAGES - 1 ? LPS : LPS0); ++i) load_one(p, p, i, sub);
+    }
+#pragma unroll
+  for (int i = 0; i < SA; ++i)
+    if (i * NT + tid < BM) as_t[i * NT + tid] = sa[i];
+#pragma unroll
+  for (int i = 0; i < SB; ++i)
+    if (i * NT + tid < BN) {
+      bs_t[i * NT + tid] = sb[i];
+      bi_t[i * NT + tid] = si[i];
+    }
+  if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS + LPS0));
+  else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+  __builtin_amdgcn_s_barrier();
+  v4i fa[2][IB], fb[2][JB];
+#pragma unroll
+  for (int i = 0; i < IB; ++i) fa[0][i] = frag(0, 0, wm * WM + 32 * i, 0);
+#pragma unroll
+  for (int j = 0; j < JB; ++j) fb[0][j] = frag(0, A_BYTES, wn * WN + 32 * j, 0);
+
+  // One step.  kPrev: the rest of the refill that the step before began;
+  // kRefill: the first part of this slot's, with the step STAGES ahead; kNext:
+  // another step follows (the last one masks its tail instead).  The order of
+  // MFMAs, fragment reads and loads is pinned, a read or load behind an MFMA,
+  // so that none of them holds up the MFMA after it for long.
+  auto step = [&](int k, int slot, auto prev, auto refill, auto more) {
+    constexpr bool kPrev = decltype(prev)::value, kRefill = decltype(refill)::value, kNext = decltype(more)::value;
+    const int next = slot + 1 == STAGES ? 0 : slot + 1, before = slot == 0 ? STAGES - 1 : slot - 1;
+    uint32_t sub = 0, sub_prev = 0;
+    if constexpr (kRefill) sub = k + STAGES == nk - 1 ? tail : 0u;
+    if constexpr (kPrev) sub_prev = k - 1 + STAGES == nk - 1 ? tail : 0u;
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      const int cur = s & 1, nxt = cur ^ 1;
+      if (s == SL - 1 && kNext) {
+        // Every LDS read of this step has been issued: past the barrier the
+        // slot is free and the next step's tile is visible.
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(kPrev ? (STAGES - 2) * LPS : 0) & ~(15 << 8));
+        __builtin_amdgcn_s_barrier();
+      }
+      if constexpr (!kNext) {
+        if (a.K % BK != 0) {
+          const bool in = k * BK + 16 * (2 * s + fh) < a.K;
+#pragma unroll
+          for (int i = 0; i < IB; ++i) fa[cur][i] = in ? fa[cur][i] : v4i{0, 0, 0, 0};
+        }
+      }
+      const int rs = s == SL - 1 ? next : slot, ss = (s + 1) % SL;
+      const bool reads = s < SL - 1 || kNext;
+#pragma unroll
+      for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+          const int t = i * JB + j;
+          __builtin_amdgcn_sched_barrier(0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if (reads) {  // A 0, B 0 .., A 1 ..: the order the next slice needs them in
+            constexpr int R = (IB + JB + NM - 1) / NM;
+#pragma unroll
+            for (int q = t * R; q < t * R + R && q < IB + JB; ++q) {
+              if (q == 0) fa[nxt][0] = frag(rs, 0, wm * WM, ss);
+              else if (q <= JB) fb[nxt][q - 1 < JB ? q - 1 : 0] = frag(rs, A_BYTES, wn * WN + 32 * (q - 1), ss);
+              else fa[nxt][q - JB < IB ? q - JB : 0] = frag(rs, 0, wm * WM + 32 * (q - JB), ss);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < LPS; ++q) {
+            const int at = q < LPS0 ? q * NM / LPS0 : NM + (q - LPS0) * ((SPREAD - 1) * NM) / (LPS - LPS0 > 0 ? LPS - LPS0 : 1);
+            if (kRefill && s == SL - 1 && at == t) load_one(k + STAGES, slot, q, sub);
+            if (kPrev && s < SL - 1 && at == (s + 1) * NM + t) load_one(k - 1 + STAGES, before, q, sub_prev);
+          }
+        }
+    }
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  int slot = 0, k = 0;
+  auto advance = [&] {
+    ++k;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+  };
+  while (k + STAGES < nk) {
+    step(k, slot, yes, yes, yes);
+    advance();
+  }
+  if (k + STAGES == nk) {
+    step(k, slot, yes, no, yes);
+    advance();
+  }
+  if constexpr (STAGES > 2) {
+    while (k + 1 < nk) {
+      step(k, slot, no, no, yes);
+      advance();
+    }
+  }
+  step(k, slot, no, no, no);
+  __syncthreads();
+  const float *as_w = as_t + wm * WM, *bs_w = bs_t + wn * WN, *bi_w = bi_t + wn * WN;
+  const int mw = m0 + wm * WM, nw = n0 + wn * WN;
+  constexpr int SLAB2 = 32 * (32 * JB * 2 + 16), SLAB4 = 32 * (32 * JB * 4 + 16);  // 2- and 4-byte outputs
+  static_assert(NW * SLAB4 <= STAGES * SLOT, "the slabs fit in the ring");
+  switch (a.out) {
+    case kOutBF16: store_tile<kOutBF16, IB, JB>(a, acc, smem + wave * SLAB2, as_w, bs_w, bi_w, lane, mw, m_end, nw); break;
+    case kOutFP16: store_tile<kOutFP16, IB, JB>(a, acc, smem + wave * SLAB2, as_w, bs_w, bi_w, lane, mw, m_end, nw); break;
+    default: store_tile<kOutFP32, IB, JB>(a, acc, smem + wave * SLAB4, as_w, bs_w, bi_w, lane, mw, m_end, nw); break;
+  }
+}
+
+// Whether every row of A and B starts on a 16-byte boundary and holds whole
+// 16-byte chunks, as the direct-to-LDS loads want it.
+inline bool fast_rows(const I8Args& a) {
+  return ((uintptr_t)a.A | (uintptr_t)a.B | (uintptr_t)a.lda | (uintptr_t)a.ldb | (uintptr_t)a.K) % 16 == 0;
+}
+
 // The empty sum: every output is its column's bias, or zero.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_i8_no_k(I8Args a) {
@@ -199,23 +506,52 @@ __global__ __launch_bounds__(256) void k_i8_no_k(I8Args a) {
   store1<OUT>(a.C, m * a.ldc + n, a.bias ? a.bias[n] : 0.0f);
 }
 
+// Kernel configurations: X(index, kernel, its sizes).
+#define FBG_I8_CFGS(X)                \
+  X(0, ANY, 64, 64)                   \
+  X(1, TILE, 256, 256, 2, 2, 128, 2, 2) \
+  X(2, TILE, 256, 128, 2, 2, 128, 3, 2) \
+  X(3, TILE, 128, 256, 2, 2, 128, 3, 2) \
+  X(4, TILE, 128, 128, 2, 2, 128, 4, 2) \
+  X(5, TILE, 128, 128, 2, 2, 128, 2, 2) \
+  X(6, TILE, 64, 128, 2, 2, 128, 3, 2)  \
+  X(7, TILE, 128, 64, 2, 2, 128, 3, 2)  \
+  X(8, TILE, 64, 64, 2, 2, 128, 4, 2)
+
 template <int BM, int BN, int GRP>
-hipError_t launch_any(const I8Args& a, int64_t grid) {
-  const dim3 g((unsigned)grid), b(256);
+void start_any(const I8Args& a, dim3 g) {
   switch (a.out) {
-    case kOutBF16: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutBF16, GRP>), g, b, 0, a.stream, a); break;
-    case kOutFP16: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutFP16, GRP>), g, b, 0, a.stream, a); break;
-    case kOutFP32: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutFP32, GRP>), g, b, 0, a.stream, a); break;
-    default: return hipErrorInvalidValue;
+    case kOutBF16: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutBF16, GRP>), g, dim3(256), 0, a.stream, a); break;
+    case kOutFP16: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutFP16, GRP>), g, dim3(256), 0, a.stream, a); break;
+    default: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutFP32, GRP>), g, dim3(256), 0, a.stream, a); break;
   }
+}
+
+template <int BM, int BN>
+hipError_t launch_ANY(const I8Args& a) {
+  const int64_t tn = (a.N + BN - 1) / BN, tm = a.offsets ? (int64_t)a.M / BM + a.E : ((int64_t)a.M + BM - 1) / BM;
+  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 g((unsigned)(tm * tn));
+  if (a.offsets) start_any<BM, BN, 1>(a, g);
+  else start_any<BM, BN, 0>(a, g);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WM_, int WN_, int BK, int ST, int SP>
+hipError_t launch_TILE(const I8Args& a) {
+  if (!fast_rows(a)) return hipErrorInvalidValue;
+  const int64_t tn = (a.N + BN - 1) / BN, tm = a.offsets ? (int64_t)a.M / BM + a.E : ((int64_t)a.M + BM - 1) / BM;
+  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 g((unsigned)(tm * tn)), b(64 * WM_ * WN_);
+  if (a.offsets) hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 1>), g, b, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 0>), g, b, 0, a.stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_i8(const I8Args& a) {
-  const bool grouped = a.offsets != nullptr;
-  if (a.K == 0 || (grouped && a.E == 0)) {
+hipError_t launch_i8(const I8Args& a, int force_cfg) {
+  if (a.K == 0) {
     const int64_t grid = ((int64_t)a.M * a.N + 255) / 256;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     const dim3 g((unsigned)grid), b(256);
@@ -226,10 +562,24 @@ hipError_t launch_i8(const I8Args& a) {
     }
     return hipGetLastError();
   }
-  const int64_t tiles_n = (a.N + 63) / 64;
-  const int64_t grid = (grouped ? (int64_t)a.M / 64 + a.E : ((int64_t)a.M + 63) / 64) * tiles_n;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return grouped ? launch_any<64, 64, 1>(a, grid) : launch_any<64, 64, 0>(a, grid);
+  int cfg = force_cfg;
+  if (cfg < 0) {
+    // The largest tile that still gives every compute unit one.
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+    if (!fast_rows(a)) cfg = 0;
+    else if (tiles(256, 256) >= 192) cfg = 1;
+    else if (tiles(256, 128) >= 192) cfg = 2;
+    else if (tiles(128, 128) >= 256) cfg = 5;
+    else if (tiles(64, 128) >= 256) cfg = 6;
+    else cfg = 8;
+  }
+  switch (cfg) {
+#define X(id, kind, ...) \
+  case id: return launch_##kind<__VA_ARGS__>(a);
+    FBG_I8_CFGS(X)
+#undef X
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace fbg

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import _int8 as T
+from tests._gpu import forced_config
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -229,3 +230,42 @@ def test_graph_replays(gpu):
         torch.cuda.synchronize()
         got = [o.clone() for o in outs]
         assert all(torch.equal(a, b) for a, b in zip(got, chain())), i
+
+
+# ---------------------------------------------------------------------------
+# Every kernel configuration, forced
+# ---------------------------------------------------------------------------
+CONFIGS = range(0, 9)
+
+
+@pytest.mark.parametrize("cfg", CONFIGS)
+@pytest.mark.parametrize("M,N,K,out", [(1, 1, 16, "fp32"), (1, 700, 128, "bf16"), (64, 64, 240, "fp16"), (70, 300, 384, "fp32"),
+                                       (257, 264, 512, "bf16"), (300, 520, 656, "fp32"), (513, 257, 2048, "bf16"),
+                                       (129, 640, 144, "fp16"), (600, 40, 1008, "bf16")])
+def test_forced_configuration(gpu, cfg, M, N, K, out):
+    d = T.make_gemm(M, N, K, seed=cfg + M, bias=cfg % 2 == 0)
+    with forced_config(cfg):
+        C = _gemm(gpu, d, out)
+    T.assert_gemm(C, d, out, f"configuration {cfg}, {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("cfg", CONFIGS)
+@pytest.mark.parametrize("name", ["decode", "ragged", "empty_ends", "big"])
+def test_forced_configuration_grouped(gpu, cfg, name):
+    counts = GROUPS[name]
+    d = T.make_gemm(sum(counts), 200, 336, seed=cfg, experts=len(counts))
+    with forced_config(cfg):
+        C = _grouped(gpu, d, counts, "bf16")
+    lo = 0
+    for e, n in enumerate(counts):
+        if n:
+            T.assert_gemm(C[lo:lo + n], _expert(d, e, lo, lo + n), "bf16", f"configuration {cfg}, {name} expert {e}")
+        lo += n
+
+
+def test_forced_configuration_that_does_not_take_the_operands(gpu):
+    d = T.make_gemm(5, 7, 9, seed=1)
+    for cfg in (1, 99):
+        with forced_config(cfg), pytest.raises(gpu.FP8BGError) as e:
+            _gemm(gpu, d, "bf16")
+        assert e.value.status == gpu.UNSUPPORTED
