@@ -193,6 +193,130 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The skinny kernel: few rows, so the weights' bytes and the launch's latency
+// are what counts.  A workgroup takes 16*NB columns and ROWS rows; its KW
+// waves split K, each loading its own fragments straight into registers in
+// groups of U slices of 64 K bytes (wave w takes groups w, w + KW, ..), the
+// next group's loads in flight while this one is multiplied; the waves' sums
+// meet in LDS.  ROWS = 8 halves a 16-row tile's activation bytes: the upper
+// eight rows of the MFMA repeat the last one and are not stored.
+//
+// FAST: rows of whole 16-byte chunks on 16-byte boundaries; else chunks are
+// assembled at any alignment.
+//
+// Grouped: one workgroup per (expert, column tile), walking the expert's rows
+// ROWS at a time (the weights of a second pass come from L2).
+// ---------------------------------------------------------------------------
+template <int NB, int ROWS, int KW, int U, bool FAST, int GRP>
+__global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
+  constexpr int MB = (ROWS + 15) / 16, BLOCKS = NB * MB;
+  __shared__ v4i red[KW][BLOCKS][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
+  const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+  int e = 0, m_lo, m_end, tn;
+  if constexpr (GRP) {
+    e = lid / tiles_n;
+    tn = lid - e * tiles_n;
+    int lo = a.offsets[e], hi = a.offsets[e + 1];
+    lo = lo < 0 ? 0 : (lo > a.M ? a.M : lo);  // malformed offsets never lead outside the operands
+    hi = hi < lo ? lo : (hi > a.M ? a.M : hi);
+    m_lo = lo;
+    m_end = hi;
+  } else {
+    const int tiles_m = (a.M + ROWS - 1) / ROWS;
+    tn = lid / tiles_m;
+    m_lo = (lid - tn * tiles_m) * ROWS;
+    m_end = m_lo + ROWS < a.M ? m_lo + ROWS : a.M;
+  }
+  const int n0 = tn * 16 * NB, r = lane & 15, h = lane >> 4;
+  const uint8_t* brow[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int n = n0 + 16 * j + r < a.N ? n0 + 16 * j + r : a.N - 1;
+    brow[j] = a.B + ((int64_t)e * a.N + n) * a.ldb;
+  }
+  const int groups = (a.K + 64 * U - 1) / (64 * U);
+  for (int m0 = m_lo; m0 < m_end; m0 += ROWS) {
+    const uint8_t* arow[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int last = m0 + ROWS < m_end ? m0 + ROWS - 1 : m_end - 1;
+      const int m = m0 + 16 * i + r < last ? m0 + 16 * i + r : last;
+      arow[i] = a.A + (int64_t)m * a.lda;
+    }
+    v4i acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    v4i fa[U][MB], fb[U][NB];
+    auto load = [&](int g) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (g * U + u) * 64 + 16 * h;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          if constexpr (FAST && GRP) fb[u][j] = *reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0));
+          else if constexpr (FAST) fb[u][j] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0)));
+          else fb[u][j] = load_chunk(brow[j], k, a.K);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (g * U + u) * 64 + 16 * h;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          if constexpr (FAST) fa[u][i] = *reinterpret_cast<const v4i*>(arow[i] + (k < a.K ? k : 0));
+          else fa[u][i] = load_chunk(arow[i], k, a.K);
+        }
+      }
+    };
+    auto multiply = [&](int g) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = (g * U + u) * 64 + 16 * h < a.K;  // chunks past K were read from the row's start
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          const v4i f = !FAST || in ? fa[u][i] : v4i{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[i][j] = mfma_i8(fb[u][j], f, acc[i][j]);
+        }
+      }
+    };
+    for (int g = wave; g < groups; g += KW) {
+      load(g);
+      __builtin_amdgcn_sched_barrier(0);  // every load of the group in flight before the first product
+      multiply(g);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) red[wave][i * NB + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int b = wave; b < BLOCKS; b += KW) {
+      const int i = b / NB, j = b % NB, m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * h;
+      const int stop = m0 + ROWS < m_end ? m0 + ROWS : m_end;
+      v4i s = red[0][b][lane];
+#pragma unroll
+      for (int w = 1; w < KW; ++w) s += red[w][b][lane];
+      const int cnt = a.N - n < 4 ? a.N - n : 4;
+      if (m < stop && cnt > 0) {
+        const v4f c = scale4(s, a.a_s[m], a.b_s + (int64_t)e * a.N, a.bias, n, a.N);
+        const int64_t at = (int64_t)m * a.ldc + n;
+        switch (a.out) {
+          case kOutBF16: store4<kOutBF16>(a.C, at, c, cnt, a.vec & 1); break;
+          case kOutFP16: store4<kOutFP16>(a.C, at, c, cnt, a.vec & 1); break;
+          default: store4<kOutFP32>(a.C, at, c, cnt, a.vec & 1); break;
+        }
+      }
+    }
+    if constexpr (GRP) __syncthreads();
+  }
+}
+
 typedef int v16i __attribute__((ext_vector_type(16)));
 
 // Scales a wave's IB x JB blocks of 32 x 32 sums and stores them.  Block
@@ -311,25 +435,31 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
   m_end = __builtin_amdgcn_readfirstlane(m_end);
   e = __builtin_amdgcn_readfirstlane(e);
   const uint8_t* Bt = a.B + (int64_t)e * a.N * a.ldb + (int64_t)n0 * a.ldb;
-  const buf_rsrc rA = make_rsrc(a.A + (int64_t)m0 * a.lda), rB = make_rsrc(Bt);
+  // The resources end with the last row that the tile may use: lanes of rows
+  // past it read zeros and touch no memory (their outputs are never stored).
+  auto bytes_to = [](int64_t rows, int64_t ld, int K) {
+    const int64_t b = (rows - 1) * ld + K;
+    return (uint32_t)(b < UINT32_MAX ? b : UINT32_MAX);
+  };
+  const buf_rsrc rA = make_rsrc_n(a.A + (int64_t)m0 * a.lda, bytes_to(m_end - m0, a.lda, a.K));
+  const buf_rsrc rB = make_rsrc_n(Bt, bytes_to(a.N - n0, a.ldb, a.K));
   const int nk = (a.K + BK - 1) / BK;
 
   // Load image q (q = i*NW + wave) fills RI LDS rows of a tile; lane l writes
   // row q*RI + l / CH, slot l % CH, so it reads the row's chunk
-  // (l % CH) ^ swz(row).  Rows past the matrix are clamped to its last row:
-  // they feed outputs that are never stored.
+  // (l % CH) ^ swz(row).
   auto swz = [](int r) { return BK == 128 ? swz_row(r) : (r >> 2) & 3; };
   uint32_t aoff[AP], boff[BP];
   const int chunk = (lane % CH) ^ swz(RI * wave + lane / CH);
 #pragma unroll
   for (int i = 0; i < AP; ++i) {
     const int r = RI * (i * NW + wave) + lane / CH;
-    aoff[i] = (uint32_t)(m0 + r < m_end ? r : m_end - 1 - m0) * (uint32_t)a.lda + 16u * (uint32_t)chunk;
+    aoff[i] = (uint32_t)r * (uint32_t)a.lda + 16u * (uint32_t)chunk;
   }
 #pragma unroll
   for (int i = 0; i < BP; ++i) {
     const int r = RI * (i * NW + wave) + lane / CH;
-    boff[i] = (uint32_t)(n0 + r < a.N ? r : a.N - 1 - n0) * (uint32_t)a.ldb + 16u * (uint32_t)chunk;
+    boff[i] = (uint32_t)r * (uint32_t)a.ldb + 16u * (uint32_t)chunk;
   }
   // In the last step, lanes whose chunk lies past K read the step's first
   // chunk instead (K % 16 == 0: a chunk is wholly in or out); the fragments'
@@ -371,114 +501,183 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
     si[i] = a.bias ? a.bias[n] : 0.0f;
   }
 
-  // A step's refill is spread over SPREAD slices, the last one of the step
-  // that frees the slot and the first ones of the step after it: load q goes
-  // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
-  // belong to the first part.
-  constexpr int NM = IB * JB;
-  constexpr int LPS0 = (LPS + SPREAD - 1) / SPREAD;
+  auto scales_to_lds = [&] {
 #pragma unroll
-  for (int p = 0; p < STAGES; ++p)
-    if (p < nk) {
-      const uint32_t sub = p == nk - 1 ? tail : 0u;
+    for (int i = 0; i < SA; ++i)
+      if (i * NT + tid < BM) as_t[i * NT + tid] = sa[i];
 #pragma unroll
-      for (int i = 0; i < (p < STAGES - 1 ? LPS : LPS0); ++i) load_one(p, p, i, sub);
-    }
-#pragma unroll
-  for (int i = 0; i < SA; ++i)
-    if (i * NT + tid < BM) as_t[i * NT + tid] = sa[i];
-#pragma unroll
-  for (int i = 0; i < SB; ++i)
-    if (i * NT + tid < BN) {
-      bs_t[i * NT + tid] = sb[i];
-      bi_t[i * NT + tid] = si[i];
-    }
-  if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS + LPS0));
-  else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
-  __builtin_amdgcn_s_barrier();
-  v4i fa[2][IB], fb[2][JB];
-#pragma unroll
-  for (int i = 0; i < IB; ++i) fa[0][i] = frag(0, 0, wm * WM + 32 * i, 0);
-#pragma unroll
-  for (int j = 0; j < JB; ++j) fb[0][j] = frag(0, A_BYTES, wn * WN + 32 * j, 0);
-
-  // One step.  kPrev: the rest of the refill that the step before began;
-  // kRefill: the first part of this slot's, with the step STAGES ahead; kNext:
-  // another step follows (the last one masks its tail instead).  The order of
-  // MFMAs, fragment reads and loads is pinned, a read or load behind an MFMA,
-  // so that none of them holds up the MFMA after it for long.
-  auto step = [&](int k, int slot, auto prev, auto refill, auto more) {
-    constexpr bool kPrev = decltype(prev)::value, kRefill = decltype(refill)::value, kNext = decltype(more)::value;
-    const int next = slot + 1 == STAGES ? 0 : slot + 1, before = slot == 0 ? STAGES - 1 : slot - 1;
-    uint32_t sub = 0, sub_prev = 0;
-    if constexpr (kRefill) sub = k + STAGES == nk - 1 ? tail : 0u;
-    if constexpr (kPrev) sub_prev = k - 1 + STAGES == nk - 1 ? tail : 0u;
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-      const int cur = s & 1, nxt = cur ^ 1;
-      if (s == SL - 1 && kNext) {
-        // Every LDS read of this step has been issued: past the barrier the
-        // slot is free and the next step's tile is visible.
-        __builtin_amdgcn_s_waitcnt(vmcnt_only(kPrev ? (STAGES - 2) * LPS : 0) & ~(15 << 8));
-        __builtin_amdgcn_s_barrier();
+    for (int i = 0; i < SB; ++i)
+      if (i * NT + tid < BN) {
+        bs_t[i * NT + tid] = sb[i];
+        bi_t[i * NT + tid] = si[i];
       }
-      if constexpr (!kNext) {
-        if (a.K % BK != 0) {
+  };
+  if constexpr (SPREAD == 0) {
+    // Whole steps: all of a step's fragments are read one step ahead, behind
+    // the barrier that makes it visible, so that with few MFMAs per slice the
+    // latency of an LDS read is paid once per step and not once per slice.
+#pragma unroll
+    for (int p = 0; p < STAGES; ++p)
+      if (p < nk) {
+        const uint32_t sub = p == nk - 1 ? tail : 0u;
+#pragma unroll
+        for (int i = 0; i < LPS; ++i) load_one(p, p, i, sub);
+      }
+    scales_to_lds();
+    if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 1) * LPS));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    __builtin_amdgcn_s_barrier();
+    v4i fa[2][SL][IB], fb[2][SL][JB];
+    auto fetch = [&](int slot, v4i (&A_)[SL][IB], v4i (&B_)[SL][JB]) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+#pragma unroll
+        for (int i = 0; i < IB; ++i) A_[s][i] = frag(slot, 0, wm * WM + 32 * i, s);
+#pragma unroll
+        for (int j = 0; j < JB; ++j) B_[s][j] = frag(slot, A_BYTES, wn * WN + 32 * j, s);
+      }
+    };
+    fetch(0, fa[0], fb[0]);
+    auto step = [&](int k, int slot, v4i (&A_)[SL][IB], v4i (&B_)[SL][JB], v4i (&An)[SL][IB], v4i (&Bn)[SL][JB]) {
+      // This step's fragments are in registers; past the barrier its slot is
+      // free and the next step's tile is visible.
+      if (k + STAGES - 1 < nk) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS) & ~(15 << 8));
+      else __builtin_amdgcn_s_waitcnt(vmcnt_only(0) & ~(15 << 8));
+      __builtin_amdgcn_s_barrier();
+      if (k + 1 < nk) fetch(slot + 1 == STAGES ? 0 : slot + 1, An, Bn);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + STAGES < nk) {
+        const uint32_t sub = k + STAGES == nk - 1 ? tail : 0u;
+#pragma unroll
+        for (int i = 0; i < LPS; ++i) load_one(k + STAGES, slot, i, sub);
+      }
+      if (k == nk - 1 && a.K % BK != 0) {
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
           const bool in = k * BK + 16 * (2 * s + fh) < a.K;
 #pragma unroll
-          for (int i = 0; i < IB; ++i) fa[cur][i] = in ? fa[cur][i] : v4i{0, 0, 0, 0};
+          for (int i = 0; i < IB; ++i) A_[s][i] = in ? A_[s][i] : v4i{0, 0, 0, 0};
         }
       }
-      const int rs = s == SL - 1 ? next : slot, ss = (s + 1) % SL;
-      const bool reads = s < SL - 1 || kNext;
 #pragma unroll
-      for (int i = 0; i < IB; ++i)
+      for (int s = 0; s < SL; ++s)
 #pragma unroll
-        for (int j = 0; j < JB; ++j) {
-          const int t = i * JB + j;
-          __builtin_amdgcn_sched_barrier(0);
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-          if (reads) {  // A 0, B 0 .., A 1 ..: the order the next slice needs them in
-            constexpr int R = (IB + JB + NM - 1) / NM;
+        for (int i = 0; i < IB; ++i)
 #pragma unroll
-            for (int q = t * R; q < t * R + R && q < IB + JB; ++q) {
-              if (q == 0) fa[nxt][0] = frag(rs, 0, wm * WM, ss);
-              else if (q <= JB) fb[nxt][q - 1 < JB ? q - 1 : 0] = frag(rs, A_BYTES, wn * WN + 32 * (q - 1), ss);
-              else fa[nxt][q - JB < IB ? q - JB : 0] = frag(rs, 0, wm * WM + 32 * (q - JB), ss);
-            }
-          }
+          for (int j = 0; j < JB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(B_[s][j], A_[s][i], acc[i][j], 0, 0, 0);
+    };
+    int slot = 0;
+    for (int k = 0; k < nk; k += 2) {
+      step(k, slot, fa[0], fb[0], fa[1], fb[1]);
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      if (k + 1 < nk) {
+        step(k + 1, slot, fa[1], fb[1], fa[0], fb[0]);
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+      }
+    }
+  } else {
+    // A step's refill is spread over SPREAD slices, the last one of the step
+    // that frees the slot and the first ones of the step after it: load q goes
+    // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
+    // belong to the first part.
+    constexpr int NM = IB * JB;
+    constexpr int LPS0 = (LPS + SPREAD - 1) / (SPREAD > 0 ? SPREAD : 1);
 #pragma unroll
-          for (int q = 0; q < LPS; ++q) {
-            const int at = q < LPS0 ? q * NM / LPS0 : NM + (q - LPS0) * ((SPREAD - 1) * NM) / (LPS - LPS0 > 0 ? LPS - LPS0 : 1);
-            if (kRefill && s == SL - 1 && at == t) load_one(k + STAGES, slot, q, sub);
-            if (kPrev && s < SL - 1 && at == (s + 1) * NM + t) load_one(k - 1 + STAGES, before, q, sub_prev);
+    for (int p = 0; p < STAGES; ++p)
+      if (p < nk) {
+        const uint32_t sub = p == nk - 1 ? tail : 0u;
+#pragma unroll
+        for (int i = 0; i < (p < STAGES - 1 ? LPS : LPS0); ++i) load_one(p, p, i, sub);
+      }
+    scales_to_lds();
+    if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS + LPS0));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    __builtin_amdgcn_s_barrier();
+    v4i fa[2][IB], fb[2][JB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i) fa[0][i] = frag(0, 0, wm * WM + 32 * i, 0);
+#pragma unroll
+    for (int j = 0; j < JB; ++j) fb[0][j] = frag(0, A_BYTES, wn * WN + 32 * j, 0);
+
+    // One step.  kPrev: the rest of the refill that the step before began;
+    // kRefill: the first part of this slot's, with the step STAGES ahead; kNext:
+    // another step follows (the last one masks its tail instead).  The order of
+    // MFMAs, fragment reads and loads is pinned, a read or load behind an MFMA,
+    // so that none of them holds up the MFMA after it for long.
+    auto step = [&](int k, int slot, auto prev, auto refill, auto more) {
+      constexpr bool kPrev = decltype(prev)::value, kRefill = decltype(refill)::value, kNext = decltype(more)::value;
+      const int next = slot + 1 == STAGES ? 0 : slot + 1, before = slot == 0 ? STAGES - 1 : slot - 1;
+      uint32_t sub = 0, sub_prev = 0;
+      if constexpr (kRefill) sub = k + STAGES == nk - 1 ? tail : 0u;
+      if constexpr (kPrev) sub_prev = k - 1 + STAGES == nk - 1 ? tail : 0u;
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        const int cur = s & 1, nxt = cur ^ 1;
+        if (s == SL - 1 && kNext) {
+          // Every LDS read of this step has been issued: past the barrier the
+          // slot is free and the next step's tile is visible.
+          __builtin_amdgcn_s_waitcnt(vmcnt_only(kPrev ? (STAGES - 2) * LPS : 0) & ~(15 << 8));
+          __builtin_amdgcn_s_barrier();
+        }
+        if constexpr (!kNext) {
+          if (a.K % BK != 0) {
+            const bool in = k * BK + 16 * (2 * s + fh) < a.K;
+#pragma unroll
+            for (int i = 0; i < IB; ++i) fa[cur][i] = in ? fa[cur][i] : v4i{0, 0, 0, 0};
           }
         }
-    }
-  };
-  constexpr std::true_type yes{};
-  constexpr std::false_type no{};
-  int slot = 0, k = 0;
-  auto advance = [&] {
-    ++k;
-    slot = slot + 1 == STAGES ? 0 : slot + 1;
-  };
-  while (k + STAGES < nk) {
-    step(k, slot, yes, yes, yes);
-    advance();
-  }
-  if (k + STAGES == nk) {
-    step(k, slot, yes, no, yes);
-    advance();
-  }
-  if constexpr (STAGES > 2) {
-    while (k + 1 < nk) {
-      step(k, slot, no, no, yes);
+        const int rs = s == SL - 1 ? next : slot, ss = (s + 1) % SL;
+        const bool reads = s < SL - 1 || kNext;
+#pragma unroll
+        for (int i = 0; i < IB; ++i)
+#pragma unroll
+          for (int j = 0; j < JB; ++j) {
+            const int t = i * JB + j;
+            __builtin_amdgcn_sched_barrier(0);
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (reads) {  // A 0, B 0 .., A 1 ..: the order the next slice needs them in
+              constexpr int R = (IB + JB + NM - 1) / NM;
+#pragma unroll
+              for (int q = t * R; q < t * R + R && q < IB + JB; ++q) {
+                if (q == 0) fa[nxt][0] = frag(rs, 0, wm * WM, ss);
+                else if (q <= JB) fb[nxt][q - 1 < JB ? q - 1 : 0] = frag(rs, A_BYTES, wn * WN + 32 * (q - 1), ss);
+                else fa[nxt][q - JB < IB ? q - JB : 0] = frag(rs, 0, wm * WM + 32 * (q - JB), ss);
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < LPS; ++q) {
+              const int at = q < LPS0 ? q * NM / LPS0 : NM + (q - LPS0) * ((SPREAD - 1) * NM) / (LPS - LPS0 > 0 ? LPS - LPS0 : 1);
+              if (kRefill && s == SL - 1 && at == t) load_one(k + STAGES, slot, q, sub);
+              if (kPrev && s < SL - 1 && at == (s + 1) * NM + t) load_one(k - 1 + STAGES, before, q, sub_prev);
+            }
+          }
+      }
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    int slot = 0, k = 0;
+    auto advance = [&] {
+      ++k;
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    };
+    while (k + STAGES < nk) {
+      step(k, slot, yes, yes, yes);
       advance();
     }
+    if (k + STAGES == nk) {
+      step(k, slot, yes, no, yes);
+      advance();
+    }
+    if constexpr (STAGES > 2) {
+      while (k + 1 < nk) {
+        step(k, slot, no, no, yes);
+        advance();
+      }
+    }
+    step(k, slot, no, no, no);
   }
-  step(k, slot, no, no, no);
   __syncthreads();
   const float *as_w = as_t + wm * WM, *bs_w = bs_t + wn * WN, *bi_w = bi_t + wn * WN;
   const int mw = m0 + wm * WM, nw = n0 + wn * WN;
@@ -512,11 +711,24 @@ __global__ __launch_bounds__(256) void k_i8_no_k(I8Args a) {
   X(1, TILE, 256, 256, 2, 2, 128, 2, 2) \
   X(2, TILE, 256, 128, 2, 2, 128, 3, 2) \
   X(3, TILE, 128, 256, 2, 2, 128, 3, 2) \
-  X(4, TILE, 128, 128, 2, 2, 128, 4, 2) \
+  X(4, TILE, 128, 128, 2, 2, 128, 4, 0) \
   X(5, TILE, 128, 128, 2, 2, 128, 2, 2) \
   X(6, TILE, 64, 128, 2, 2, 128, 3, 2)  \
-  X(7, TILE, 128, 64, 2, 2, 128, 3, 2)  \
-  X(8, TILE, 64, 64, 2, 2, 128, 4, 2)
+  X(7, TILE, 64, 128, 2, 2, 128, 3, 0)  \
+  X(8, TILE, 64, 64, 2, 2, 128, 4, 2)   \
+  X(9, SKINNY, 1, 8, 8, 8)              \
+  X(10, SKINNY, 1, 16, 8, 8)            \
+  X(11, TILE, 64, 64, 2, 2, 128, 4, 0)  \
+  X(12, SKINNY, 2, 16, 8, 4)            \
+  X(13, TILE, 32, 64, 1, 2, 128, 4, 0)  \
+  X(14, TILE, 64, 64, 2, 2, 128, 8, 0)  \
+  X(15, TILE, 32, 64, 1, 2, 128, 6, 0)  \
+  X(16, TILE, 32, 128, 1, 4, 128, 3, 0) \
+  X(17, TILE, 32, 128, 1, 4, 128, 7, 0) \
+  X(18, TILE, 128, 128, 2, 2, 128, 2, 0) \
+  X(19, TILE, 64, 128, 2, 2, 128, 6, 0) \
+  X(20, TILE, 32, 64, 1, 2, 128, 4, 2)  \
+  X(21, TILE, 64, 256, 1, 4, 128, 3, 0)
 
 template <int BM, int BN, int GRP>
 void start_any(const I8Args& a, dim3 g) {
@@ -545,6 +757,21 @@ hipError_t launch_TILE(const I8Args& a) {
   const dim3 g((unsigned)(tm * tn)), b(64 * WM_ * WN_);
   if (a.offsets) hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 1>), g, b, 0, a.stream, a);
   else hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 0>), g, b, 0, a.stream, a);
+  return hipGetLastError();
+}
+
+template <int NB, int ROWS, int KW, int U>
+hipError_t launch_SKINNY(const I8Args& a) {
+  const int64_t tn = (a.N + 16 * NB - 1) / (16 * NB), tm = a.offsets ? a.E : ((int64_t)a.M + ROWS - 1) / ROWS;
+  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 g((unsigned)(tm * tn)), b(64 * KW);
+  if (fast_rows(a)) {
+    if (a.offsets) hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 1>), g, b, 0, a.stream, a);
+    else hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 0>), g, b, 0, a.stream, a);
+  } else {
+    if (a.offsets) hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, false, 1>), g, b, 0, a.stream, a);
+    else hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, false, 0>), g, b, 0, a.stream, a);
+  }
   return hipGetLastError();
 }
 
