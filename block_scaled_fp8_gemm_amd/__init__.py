@@ -11,6 +11,7 @@ section "Description".)  If the library is not built, load() raises: there is
 no fallback of any kind.
 """
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -25,7 +26,6 @@ VARIANT_NAMES[5] = "grouped"          # reported by grouped_plan only
 OUT_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 OUT_DTYPES = {v: k for k, v in OUT_CODES.items()}
 FP8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
-QUANT_CODES = {None: 0, "int8": 1, "fp8": 2}
 
 
 class FP8BGError(RuntimeError):
@@ -316,37 +316,23 @@ def grouped_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: torch
 # ---------------------------------------------------------------------------
 # 8-bit integers: one scale per token and one per output channel.  Matrices
 # here may be slices of wider buffers: unit column stride, any row pitch.
+# The checks and the call are compiled (csrc/fp8bg_torch.cpp).
 # ---------------------------------------------------------------------------
-def _pitch(t, name, dtype, shape, device):
-    """Checks a matrix and returns its row pitch in elements."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    ld, unit = t.stride()
-    if unit != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return ld
+_native = None
 
 
-def _vector(t, name, dtype, shape, device):
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
-    return t.data_ptr()
-
-
-def _cuda_matrix(t, name):
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return t.shape
-
-
-def _stream_ptr(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+def _load_native():
+    """The compiled binding (built in-tree with the library); raises if absent."""
+    global _native
+    load()
+    if not os.path.exists(os.path.join(_HERE, "_fp8bg_torch.so")):
+        raise RuntimeError(f"{_HERE}/_fp8bg_torch.so is not built: run `python -c 'import __graft_entry__ as g; g.build()'`")
+    spec = importlib.util.spec_from_file_location("_fp8bg_torch", os.path.join(_HERE, "_fp8bg_torch.so"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.set_error(FP8BGError)
+    _native = mod
+    return mod
 
 
 def int8_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: torch.Tensor, bias: torch.Tensor = None,
@@ -358,23 +344,7 @@ def int8_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: torch.Te
     GPU; rows of A, B and `out` may be any distance apart.  The sum over k is
     exact, so the result does not depend on the kernel that is chosen.  See
     fbg_int8_gemm in include/fp8bg.h."""
-    M, K = _cuda_matrix(A, "A")
-    N = _cuda_matrix(B, "B")[0]
-    dev = A.device
-    lda = _pitch(A, "A", torch.int8, (M, K), dev)
-    ldb = _pitch(B, "B", torch.int8, (N, K), dev)
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        ldc = N
-    else:
-        ldc = _pitch(out, "out", out_dtype, (M, N), dev)
-    st = load().fbg_int8_gemm(A.data_ptr(), lda, _vector(a_s, "a_s", torch.float32, (M,), dev), B.data_ptr(), ldb,
-                              _vector(b_s, "b_s", torch.float32, (N,), dev),
-                              None if bias is None else _vector(bias, "bias", torch.float32, (N,), dev),
-                              out.data_ptr(), ldc, M, N, K, _out_code(out_dtype), _stream_ptr(stream, dev))
-    if st != SUCCESS:
-        raise FP8BGError(st, "fbg_int8_gemm")
-    return out
+    return (_native or _load_native()).int8_gemm(A, a_s, B, b_s, bias, out_dtype, out, stream)
 
 
 def int8_grouped_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: torch.Tensor, offsets: torch.Tensor,
@@ -385,33 +355,7 @@ def int8_grouped_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: 
     a_s [M] float32, offsets int32 [E+1] on the same GPU (never read by the
     host).  Rows of no expert are left as they are in `out`.  See
     fbg_int8_grouped_gemm in include/fp8bg.h."""
-    M, K = _cuda_matrix(A, "A")
-    if B.dim() != 3 or B.dtype != torch.int8:
-        raise ValueError("B must be a 3-D int8 tensor [E, N, K]")
-    E, N = B.shape[0], B.shape[1]
-    dev = A.device
-    lda = _pitch(A, "A", torch.int8, (M, K), dev)
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        ldc = N
-    else:
-        ldc = _pitch(out, "out", out_dtype, (M, N), dev)
-    st = load().fbg_int8_grouped_gemm(A.data_ptr(), lda, _vector(a_s, "a_s", torch.float32, (M,), dev),
-                                      _vector(B, "B", torch.int8, (E, N, K), dev),
-                                      _vector(b_s, "b_s", torch.float32, (E, N), dev), out.data_ptr(), ldc,
-                                      _vector(offsets, "offsets", torch.int32, (E + 1,), dev), E, M, N, K,
-                                      _out_code(out_dtype), _stream_ptr(stream, dev))
-    if st != SUCCESS:
-        raise FP8BGError(st, "fbg_int8_grouped_gemm")
-    return out
-
-
-def _code_matrix(M: int, K: int, device) -> torch.Tensor:
-    """An int8 [M,K] matrix whose rows start 16 bytes apart or a multiple of
-    it, as the products' fast loads want them."""
-    ld = (K + 15) // 16 * 16
-    q = torch.empty((M, ld), dtype=torch.int8, device=device)
-    return q if ld == K else q[:, :K]
+    return (_native or _load_native()).int8_grouped_gemm(A, a_s, B, b_s, offsets, out_dtype, out, stream)
 
 
 def quantize_tokens(x: torch.Tensor, q: torch.Tensor = None, scale: torch.Tensor = None,
@@ -422,35 +366,7 @@ def quantize_tokens(x: torch.Tensor, q: torch.Tensor = None, scale: torch.Tensor
     the A and a_s (or, from weights, the B and b_s) of int8_gemm.  Where q is
     not given and K is not a multiple of 16, its rows are padded to one.  See
     fbg_quantize_tokens in include/fp8bg.h."""
-    M, K = _cuda_matrix(x, "x")
-    dev = x.device
-    if x.dtype not in OUT_CODES:
-        raise TypeError(f"x: dtype {x.dtype}, expected one of {tuple(OUT_CODES)}")
-    ldx = _pitch(x, "x", x.dtype, (M, K), dev)
-    if q is None:
-        q = _code_matrix(M, K, dev)
-    ldq = _pitch(q, "q", torch.int8, (M, K), dev)
-    if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
-    st = load().fbg_quantize_tokens(x.data_ptr(), ldx, OUT_CODES[x.dtype], M, K, q.data_ptr(), ldq,
-                                    _vector(scale, "scale", torch.float32, (M,), dev), _stream_ptr(stream, dev))
-    if st != SUCCESS:
-        raise FP8BGError(st, "fbg_quantize_tokens")
-    return q, scale
-
-
-def _gate_strides(gate, M, D, dtype, device):
-    """(row, column) element strides of a gate broadcast over [M,D]."""
-    if gate.dtype != dtype:
-        raise TypeError(f"gate: dtype {gate.dtype}, expected {dtype}")
-    if gate.device != device:
-        raise ValueError(f"gate is on {gate.device}, expected {device}")
-    shape, strides = gate.shape, gate.stride()
-    if len(shape) == 1:
-        shape, strides = (1, shape[0]), (0, strides[0])
-    if len(shape) != 2 or shape[0] not in (1, M) or shape[1] not in (1, D):
-        raise ValueError(f"gate: shape {tuple(gate.shape)} does not broadcast to {(M, D)}")
-    return (0 if shape[0] == 1 else strides[0]), (0 if shape[1] == 1 else strides[1])
+    return (_native or _load_native()).quantize_tokens(x, q, scale, stream)
 
 
 def block_norm(h: torch.Tensor, x: torch.Tensor = None, post_weight: torch.Tensor = None, gate: torch.Tensor = None,
@@ -467,41 +383,5 @@ def block_norm(h: torch.Tensor, x: torch.Tensor = None, post_weight: torch.Tenso
     quantize="int8" (r, q, scale [M]), the operands of int8_gemm; with
     quantize="fp8" (r, A, a_s [M, D/128]), those of gemm; without pre_weight
     (r, None).  See fbg_block_norm in include/fp8bg.h."""
-    M, D = _cuda_matrix(h, "h")
-    dev, dtype = h.device, h.dtype
-    if dtype not in OUT_CODES:
-        raise TypeError(f"h: dtype {dtype}, expected one of {tuple(OUT_CODES)}")
-    if quantize not in QUANT_CODES:
-        raise ValueError(f"quantize: {quantize!r}, expected one of {tuple(QUANT_CODES)}")
-    ldh = _pitch(h, "h", dtype, (M, D), dev)
-    ldx = 0 if x is None else _pitch(x, "x", dtype, (M, D), dev)
-    grow, gcol = (0, 0) if gate is None else _gate_strides(gate, M, D, dtype, dev)
-    weights = [w for w in (post_weight, pre_weight) if w is not None]
-    wtype = weights[0].dtype if weights else dtype
-    if wtype != dtype and wtype != torch.float32:
-        raise TypeError(f"weights: dtype {wtype}, expected {dtype} or torch.float32")
-    post = None if post_weight is None else _vector(post_weight, "post_weight", wtype, (D,), dev)
-    pre = None if pre_weight is None else _vector(pre_weight, "pre_weight", wtype, (D,), dev)
-    r = torch.empty((M, D), dtype=dtype, device=dev)
-    y = scale = None
-    ldy = D
-    if pre_weight is not None:
-        if quantize is None:
-            y = torch.empty((M, D), dtype=dtype, device=dev)
-        elif quantize == "int8":
-            y = _code_matrix(M, D, dev)
-            ldy = y.stride(0)
-            scale = torch.empty(M, dtype=torch.float32, device=dev)
-        else:
-            y = torch.empty((M, D), dtype=torch.float8_e4m3fn, device=dev)
-            scale = torch.empty((M, D // 128), dtype=torch.float32, device=dev)
-    elif quantize is not None:
-        raise ValueError("quantize needs pre_weight")
-    st = load().fbg_block_norm(h.data_ptr(), ldh, None if x is None else x.data_ptr(), ldx,
-                               None if gate is None else gate.data_ptr(), grow, gcol, post, pre, OUT_CODES[dtype],
-                               OUT_CODES[wtype], M, D, residual_scale, eps, weight_offset, r.data_ptr(), D,
-                               None if y is None else y.data_ptr(), ldy, None if scale is None else scale.data_ptr(),
-                               QUANT_CODES[quantize], _stream_ptr(stream, dev))
-    if st != SUCCESS:
-        raise FP8BGError(st, "fbg_block_norm")
-    return (r, y) if quantize is None else (r, y, scale)
+    return (_native or _load_native()).block_norm(h, x, post_weight, gate, pre_weight, residual_scale, eps,
+                                                  weight_offset, quantize, stream)

@@ -1,6 +1,7 @@
 """Builds the HIP library libfp8bg.so in-tree for gfx950 with hipcc, and
 beside it libfp8bg_probe.so, the load-path probe that the benchmark's
---probe-load mode runs (a measuring tool, not part of the GEMM library).
+--probe-load mode runs (a measuring tool, not part of the GEMM library), and
+_fp8bg_torch.so, the compiled part of the Python binding.
 
 Every HIP source is compiled for gfx950 only.  Flags:
   -Xclang -target-feature -Xclang -packed-fp32-ops   no packed-FP32 VALU ops
@@ -27,6 +28,10 @@ PROBE_SOURCES = ["fp8bg_probe.hip"]
 ARCH = "gfx950"
 
 
+TORCH_LIB = os.path.join(PKG, "_fp8bg_torch.so")
+TORCH_SOURCE = "fp8bg_torch.cpp"
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if cand and os.path.exists(cand):
@@ -41,10 +46,31 @@ def flags():
             f"-I{INCLUDE}", f"-I{CSRC}"]
 
 
-def build(verbose: bool = False, jobs: int = 3) -> str:
+def build(verbose: bool = False, jobs: int = 4) -> str:
     lib = _build_lib(SOURCES, LIB, verbose, jobs)
     _build_lib(PROBE_SOURCES, PROBE_LIB, verbose, jobs)
+    _build_torch(verbose)
     return lib
+
+
+def _build_torch(verbose: bool) -> None:
+    """The compiled part of the Python binding: host code only, against this
+    interpreter's torch, linked with the library beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include", INCLUDE]
+    libs = cpp_extension.library_paths()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for d in inc for f in ("-isystem" if d != INCLUDE else "-I", d)],
+           os.path.join(CSRC, TORCH_SOURCE), "-o", TORCH_LIB + ".tmp", "-L", PKG, "-lfp8bg", "-Wl,-rpath,$ORIGIN",
+           *[f"-L{d}" for d in libs], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
 
 
 def _build_lib(sources, out, verbose: bool, jobs: int) -> str:
