@@ -78,32 +78,44 @@ __device__ __forceinline__ v4f scale4(const v4i& acc, float as, const float* __r
   return c;
 }
 
-// 16 bytes of a row at byte k0, zeros from byte K on.  Rows start at any
-// address: a whole chunk is one unaligned 16-byte load.
-__device__ __forceinline__ v4i load_chunk(const uint8_t* __restrict__ row, int k0, int K) {
-  v4i v = {0, 0, 0, 0};
-  if (k0 + 16 <= K) {
-    __builtin_memcpy(&v, row + k0, 16);
-  } else if (k0 < K) {
-    uint32_t w[4] = {0, 0, 0, 0};
+// Rows that start anywhere and end anywhere (K >= 16).  The 16-byte chunk at
+// byte k0 is read at min(k0, K - 16), so that it never leaves the row and
+// needs no branch; both operands read the same window, and in the activations'
+// (keep_tail) the bytes before k0, which an earlier chunk holds, are zeroed.
+__device__ __forceinline__ v4i load_window(const uint8_t* __restrict__ row, int k0, int K) {
+  v4i v;
+  __builtin_memcpy(&v, row + (k0 < K - 16 ? k0 : K - 16), 16);
+  return v;
+}
+__device__ __forceinline__ v4i keep_tail(v4i v, int k0, int K) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k0 + i < K) w[i >> 2] |= (uint32_t)row[k0 + i] << (8 * (i & 3));
-    v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+  for (int i = 0; i < 4; ++i) {
+    const int drop = k0 - (K - 16) - 4 * i;  // leading bytes of dword i to zero
+    v[i] = drop <= 0 ? v[i] : drop >= 4 ? 0 : (int)((uint32_t)v[i] & (0xffffffffu << (8 * drop)));
   }
   return v;
 }
 
+// Every LDS access of the workgroup's waves before this is done after it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // ---------------------------------------------------------------------------
 // Any sizes and any alignment: BM x BN tiles, 2 x 2 waves, 128 bytes of K per
-// step through registers into swizzled LDS tiles (swz_row), the next step's
-// loads in flight while this one is multiplied.
+// step through registers into two swizzled LDS tiles (swz_row).  The chunks of
+// AHEAD steps are in flight in registers, since a step's arithmetic is far
+// shorter than a load's latency, and with two tiles a step needs one barrier.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int OUT, int GRP>
+template <int BM, int BN, int AHEAD, int OUT, int GRP>
 __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
   constexpr int WM = BM / 2, WN = BN / 2, IB = WM / 16, JB = WN / 16;
   constexpr int AP = BM * 8 / 256, BP = BN * 8 / 256;  // 16-byte chunks per thread
-  __shared__ __attribute__((aligned(16))) uint8_t smem[(BM + BN) * 128];
+  constexpr int TILE = (BM + BN) * 128;
+  static_assert(AHEAD % 2 == 0, "step k of an unrolled round uses tile k & 1");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * TILE];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const int tiles_n = (a.N + BN - 1) / BN;
@@ -140,42 +152,53 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
 #pragma unroll
     for (int j = 0; j < JB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
-  v4i ra[AP], rb[BP];
-  auto fetch = [&](int k) {
+  v4i ra[AHEAD][AP], rb[AHEAD][BP];
+  auto fetch = [&](int k, v4i (&fa)[AP], v4i (&fb)[BP]) {
     const int c = k + 16 * (tid & 7);
 #pragma unroll
-    for (int p = 0; p < AP; ++p) ra[p] = load_chunk(arow[p], c, a.K);
+    for (int p = 0; p < AP; ++p) fa[p] = load_window(arow[p], c, a.K);
 #pragma unroll
-    for (int p = 0; p < BP; ++p) rb[p] = load_chunk(brow[p], c, a.K);
+    for (int p = 0; p < BP; ++p) fb[p] = load_window(brow[p], c, a.K);
   };
-  fetch(0);
-  for (int k = 0; k < a.K; k += 128) {
-    __syncthreads();  // the previous step's reads are done
 #pragma unroll
-    for (int p = 0; p < AP; ++p) {
-      const int r = (p * 256 + tid) / 8;
-      *reinterpret_cast<v4i*>(smem + 128 * r + 16 * ((tid & 7) ^ swz_row(r))) = ra[p];
-    }
+  for (int s = 0; s < AHEAD; ++s) fetch(128 * s, ra[s], rb[s]);
+  for (int k0 = 0; k0 < a.K; k0 += 128 * AHEAD) {
 #pragma unroll
-    for (int p = 0; p < BP; ++p) {
-      const int r = (p * 256 + tid) / 8;
-      *reinterpret_cast<v4i*>(smem + BM * 128 + 128 * r + 16 * ((tid & 7) ^ swz_row(r))) = rb[p];
-    }
-    __syncthreads();
-    if (k + 128 < a.K) fetch(k + 128);
-    v8i bf[JB];
+    for (int s = 0; s < AHEAD; ++s) {
+      const int k = k0 + 128 * s;
+      if (k >= a.K) break;
+      uint8_t* tile = smem + (s & 1) * TILE;
+      if (k + 128 > a.K) {
 #pragma unroll
-    for (int j = 0; j < JB; ++j) bf[j] = load_frag_lds_sw(smem + BM * 128, wn * WN + 16 * j, lane);
+        for (int p = 0; p < AP; ++p) ra[s][p] = keep_tail(ra[s][p], k + 16 * (tid & 7), a.K);
+      }
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
-      const v8i af = load_frag_lds_sw(smem, wm * WM + 16 * i, lane);
-      const v4i alo = __builtin_shufflevector(af, af, 0, 1, 2, 3), ahi = __builtin_shufflevector(af, af, 4, 5, 6, 7);
+      for (int p = 0; p < AP; ++p) {
+        const int r = (p * 256 + tid) / 8;
+        *reinterpret_cast<v4i*>(tile + 128 * r + 16 * ((tid & 7) ^ swz_row(r))) = ra[s][p];
+      }
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        const v4i blo = __builtin_shufflevector(bf[j], bf[j], 0, 1, 2, 3);
-        const v4i bhi = __builtin_shufflevector(bf[j], bf[j], 4, 5, 6, 7);
-        acc[i][j] = mfma_i8(blo, alo, acc[i][j]);
-        acc[i][j] = mfma_i8(bhi, ahi, acc[i][j]);
+      for (int p = 0; p < BP; ++p) {
+        const int r = (p * 256 + tid) / 8;
+        *reinterpret_cast<v4i*>(tile + BM * 128 + 128 * r + 16 * ((tid & 7) ^ swz_row(r))) = rb[s][p];
+      }
+      // The chunk's registers are free again: the step AHEAD further on.
+      fetch(k + 128 * AHEAD, ra[s], rb[s]);
+      lds_barrier();  // the tile's last reads were two steps ago, before the previous barrier
+      v8i bf[JB];
+#pragma unroll
+      for (int j = 0; j < JB; ++j) bf[j] = load_frag_lds_sw(tile + BM * 128, wn * WN + 16 * j, lane);
+#pragma unroll
+      for (int i = 0; i < IB; ++i) {
+        const v8i af = load_frag_lds_sw(tile, wm * WM + 16 * i, lane);
+        const v4i alo = __builtin_shufflevector(af, af, 0, 1, 2, 3), ahi = __builtin_shufflevector(af, af, 4, 5, 6, 7);
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+          const v4i blo = __builtin_shufflevector(bf[j], bf[j], 0, 1, 2, 3);
+          const v4i bhi = __builtin_shufflevector(bf[j], bf[j], 4, 5, 6, 7);
+          acc[i][j] = mfma_i8(blo, alo, acc[i][j]);
+          acc[i][j] = mfma_i8(bhi, ahi, acc[i][j]);
+        }
       }
     }
   }
@@ -188,7 +211,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
     for (int j = 0; j < JB; ++j) {
       const int n = n0 + wn * WN + 16 * j + 4 * (lane >> 4);
       const int cnt = a.N - n < 4 ? a.N - n : 4;
-      if (cnt > 0) store4<OUT>(a.C, (int64_t)m * a.ldc + n, scale4(acc[i][j], as, b_s, a.bias, n, a.N), cnt, a.vec);
+      if (cnt > 0) store4<OUT>(a.C, (int64_t)m * a.ldc + n, scale4(acc[i][j], as, b_s, a.bias, n, a.N), cnt, a.vec & 1);
     }
   }
 }
@@ -202,8 +225,8 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
 // meet in LDS.  ROWS = 8 halves a 16-row tile's activation bytes: the upper
 // eight rows of the MFMA repeat the last one and are not stored.
 //
-// FAST: rows of whole 16-byte chunks on 16-byte boundaries; else chunks are
-// assembled at any alignment.
+// FAST: rows of whole 16-byte chunks on 16-byte boundaries; else chunks at any
+// alignment (load_window).
 //
 // Grouped: one workgroup per (expert, column tile), walking the expert's rows
 // ROWS at a time (the weights of a second pass come from L2).
@@ -261,7 +284,7 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
         for (int j = 0; j < NB; ++j) {
           if constexpr (FAST && GRP) fb[u][j] = *reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0));
           else if constexpr (FAST) fb[u][j] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0)));
-          else fb[u][j] = load_chunk(brow[j], k, a.K);
+          else fb[u][j] = load_window(brow[j], k, a.K);
         }
       }
 #pragma unroll
@@ -270,17 +293,19 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
           if constexpr (FAST) fa[u][i] = *reinterpret_cast<const v4i*>(arow[i] + (k < a.K ? k : 0));
-          else fa[u][i] = load_chunk(arow[i], k, a.K);
+          else fa[u][i] = load_window(arow[i], k, a.K);
         }
       }
     };
     auto multiply = [&](int g) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool in = (g * U + u) * 64 + 16 * h < a.K;  // chunks past K were read from the row's start
+        const int k = (g * U + u) * 64 + 16 * h;  // FAST: chunks past K were read from the row's start
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-          const v4i f = !FAST || in ? fa[u][i] : v4i{0, 0, 0, 0};
+          v4i f = fa[u][i];
+          if constexpr (FAST) f = k < a.K ? f : v4i{0, 0, 0, 0};
+          else if ((g * U + u + 1) * 64 > a.K) f = keep_tail(f, k, a.K);
 #pragma unroll
           for (int j = 0; j < NB; ++j) acc[i][j] = mfma_i8(fb[u][j], f, acc[i][j]);
         }
@@ -696,18 +721,38 @@ inline bool fast_rows(const I8Args& a) {
   return ((uintptr_t)a.A | (uintptr_t)a.B | (uintptr_t)a.lda | (uintptr_t)a.ldb | (uintptr_t)a.K) % 16 == 0;
 }
 
-// The empty sum: every output is its column's bias, or zero.
+// K < 16: rows shorter than a chunk, one output per thread.  K == 0 is the
+// empty sum: the column's bias, or zero, in every row (also of no expert).
 template <int OUT>
-__global__ __launch_bounds__(256) void k_i8_no_k(I8Args a) {
+__global__ __launch_bounds__(256) void k_i8_short(I8Args a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)a.M * a.N) return;
   const int64_t m = i / a.N, n = i - m * a.N;
-  store1<OUT>(a.C, m * a.ldc + n, a.bias ? a.bias[n] : 0.0f);
+  if (a.K == 0) {
+    store1<OUT>(a.C, m * a.ldc + n, a.bias ? a.bias[n] : 0.0f);
+    return;
+  }
+  int lo = 0, hi = a.offsets ? a.E : 1;  // the experts whose offset is at most m end before `hi`
+  if (a.offsets) {
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (a.offsets[mid] <= m) lo = mid;
+      else hi = mid;
+    }
+    if (m < a.offsets[lo] || m >= a.offsets[lo + 1]) return;
+  }
+  const int8_t* x = reinterpret_cast<const int8_t*>(a.A) + m * a.lda;
+  const int8_t* w = reinterpret_cast<const int8_t*>(a.B) + ((int64_t)lo * a.N + n) * a.ldb;
+  int sum = 0;
+  for (int k = 0; k < a.K; ++k) sum += (int)x[k] * (int)w[k];
+  float c = (a.a_s[m] * a.b_s[(int64_t)lo * a.N + n]) * (float)sum;
+  if (a.bias) c = c + a.bias[n];
+  store1<OUT>(a.C, m * a.ldc + n, c);
 }
 
 // Kernel configurations: X(index, kernel, its sizes).
 #define FBG_I8_CFGS(X)                \
-  X(0, ANY, 64, 64)                   \
+  X(0, ANY, 64, 64, 4)                \
   X(1, TILE, 256, 256, 2, 2, 128, 2, 2) \
   X(2, TILE, 256, 128, 2, 2, 128, 3, 2) \
   X(3, TILE, 128, 256, 2, 2, 128, 3, 2) \
@@ -728,24 +773,29 @@ __global__ __launch_bounds__(256) void k_i8_no_k(I8Args a) {
   X(18, TILE, 128, 128, 2, 2, 128, 2, 0) \
   X(19, TILE, 64, 128, 2, 2, 128, 6, 0) \
   X(20, TILE, 32, 64, 1, 2, 128, 4, 2)  \
-  X(21, TILE, 64, 256, 1, 4, 128, 3, 0)
+  X(21, TILE, 64, 256, 1, 4, 128, 3, 0) \
+  X(22, ANY, 128, 128, 2) \
+  X(23, ANY, 64, 64, 2) \
+  X(24, ANY, 32, 64, 4) \
+  X(25, ANY, 64, 64, 8) \
+  X(26, ANY, 128, 128, 4)
 
-template <int BM, int BN, int GRP>
+template <int BM, int BN, int AHEAD, int GRP>
 void start_any(const I8Args& a, dim3 g) {
   switch (a.out) {
-    case kOutBF16: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutBF16, GRP>), g, dim3(256), 0, a.stream, a); break;
-    case kOutFP16: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutFP16, GRP>), g, dim3(256), 0, a.stream, a); break;
-    default: hipLaunchKernelGGL((k_i8_any<BM, BN, kOutFP32, GRP>), g, dim3(256), 0, a.stream, a); break;
+    case kOutBF16: hipLaunchKernelGGL((k_i8_any<BM, BN, AHEAD, kOutBF16, GRP>), g, dim3(256), 0, a.stream, a); break;
+    case kOutFP16: hipLaunchKernelGGL((k_i8_any<BM, BN, AHEAD, kOutFP16, GRP>), g, dim3(256), 0, a.stream, a); break;
+    default: hipLaunchKernelGGL((k_i8_any<BM, BN, AHEAD, kOutFP32, GRP>), g, dim3(256), 0, a.stream, a); break;
   }
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int AHEAD>
 hipError_t launch_ANY(const I8Args& a) {
   const int64_t tn = (a.N + BN - 1) / BN, tm = a.offsets ? (int64_t)a.M / BM + a.E : ((int64_t)a.M + BM - 1) / BM;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   const dim3 g((unsigned)(tm * tn));
-  if (a.offsets) start_any<BM, BN, 1>(a, g);
-  else start_any<BM, BN, 0>(a, g);
+  if (a.offsets) start_any<BM, BN, AHEAD, 1>(a, g);
+  else start_any<BM, BN, AHEAD, 0>(a, g);
   return hipGetLastError();
 }
 
@@ -778,14 +828,15 @@ hipError_t launch_SKINNY(const I8Args& a) {
 }  // namespace
 
 hipError_t launch_i8(const I8Args& a, int force_cfg) {
-  if (a.K == 0) {
+  if (a.K < 16) {
+    if (a.K > 0 && force_cfg >= 0) return hipErrorInvalidValue;
     const int64_t grid = ((int64_t)a.M * a.N + 255) / 256;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     const dim3 g((unsigned)grid), b(256);
     switch (a.out) {
-      case kOutBF16: hipLaunchKernelGGL(k_i8_no_k<kOutBF16>, g, b, 0, a.stream, a); break;
-      case kOutFP16: hipLaunchKernelGGL(k_i8_no_k<kOutFP16>, g, b, 0, a.stream, a); break;
-      default: hipLaunchKernelGGL(k_i8_no_k<kOutFP32>, g, b, 0, a.stream, a); break;
+      case kOutBF16: hipLaunchKernelGGL(k_i8_short<kOutBF16>, g, b, 0, a.stream, a); break;
+      case kOutFP16: hipLaunchKernelGGL(k_i8_short<kOutFP16>, g, b, 0, a.stream, a); break;
+      default: hipLaunchKernelGGL(k_i8_short<kOutFP32>, g, b, 0, a.stream, a); break;
     }
     return hipGetLastError();
   }

@@ -131,7 +131,7 @@ def _expert(d, e, lo, hi):
 
 
 @pytest.mark.parametrize("name", list(GROUPS))
-@pytest.mark.parametrize("N,K,out", [(64, 256, "bf16"), (515, 776, "fp32"), (130, 1001, "fp16"), (512, 1024, "bf16")])
+@pytest.mark.parametrize("N,K,out", [(64, 256, "bf16"), (40, 11, "fp32"), (33, 17, "bf16"), (515, 776, "fp32"), (130, 1001, "fp16"), (512, 1024, "bf16")])
 def test_grouped(gpu, name, N, K, out):
     counts = GROUPS[name]
     d = T.make_gemm(sum(counts), N, K, seed=len(counts) + N, experts=len(counts))
@@ -235,7 +235,7 @@ def test_graph_replays(gpu):
 # ---------------------------------------------------------------------------
 # Every kernel configuration, forced
 # ---------------------------------------------------------------------------
-CONFIGS = range(0, 22)
+CONFIGS = range(0, 27)
 
 
 @pytest.mark.parametrize("cfg", CONFIGS)
