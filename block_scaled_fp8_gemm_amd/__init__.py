@@ -23,6 +23,7 @@ SUCCESS, INVALID_VALUE, UNSUPPORTED, OUT_OF_MEMORY, HIP_ERROR, SCRATCH_LIMIT = 0
 VARIANTS = {"auto": 0, "generic": 1, "short_k256": 2, "swap_ab": 3, "swap_ab_splitk": 4}
 VARIANT_NAMES = {v: k for k, v in VARIANTS.items()}
 VARIANT_NAMES[5] = "grouped"          # reported by grouped_plan only
+VARIANT_NAMES[6] = "int8"             # reported by int8_plan only
 OUT_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 OUT_DTYPES = {v: k for k, v in OUT_CODES.items()}
 FP8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
@@ -77,6 +78,8 @@ def load():
     lib.fbg_int8_gemm.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]
     lib.fbg_int8_grouped_gemm.restype = _int
     lib.fbg_int8_grouped_gemm.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _vp]
+    lib.fbg_int8_plan.restype = _int
+    lib.fbg_int8_plan.argtypes = [_i64, _i64, _i64, _i64, _int, _int, _vp]
     lib.fbg_quantize_tokens.restype = _int
     lib.fbg_quantize_tokens.argtypes = [_vp, _i64, _int, _i64, _i64, _vp, _i64, _vp, _vp]
     lib.fbg_block_norm.restype = _int
@@ -333,6 +336,18 @@ def _load_native():
     mod.set_error(FP8BGError)
     _native = mod
     return mod
+
+
+def int8_plan(M: int, N: int, K: int, E: int = 0, aligned_rows: bool = True, cu_count: int = 256) -> dict:
+    """The int8 products' tile choice (pure host call): int8_gemm's for E = 0,
+    int8_grouped_gemm's for E experts holding M rows."""
+    p = Plan()
+    st = load().fbg_int8_plan(E, M, N, K, int(aligned_rows), cu_count, ctypes.byref(p))
+    if st != SUCCESS:
+        raise FP8BGError(st, "fbg_int8_plan")
+    d = {f: getattr(p, f) for f, _ in Plan._fields_}
+    d["variant_name"] = VARIANT_NAMES.get(p.variant, "none")
+    return d
 
 
 def int8_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: torch.Tensor, bias: torch.Tensor = None,

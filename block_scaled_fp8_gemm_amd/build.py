@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8bg.so")
 SOURCES = ["fp8bg_api.hip", "fp8bg_kernels.hip", "fp8bg_quant.hip", "fp8bg_int8.hip", "fp8bg_rows.hip",
-           "fp8bg_plan.cpp"]
+           "fp8bg_plan.cpp", "fp8bg_int8_plan.cpp"]
 # The FP8 kernels fold every MFMA's result in the vector ALU, so theirs stay in
 # vector registers; the int8 kernels accumulate in the MFMA's own registers.
 MFMA_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]

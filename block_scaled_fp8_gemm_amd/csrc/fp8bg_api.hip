@@ -443,8 +443,11 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
   args.vec = (ldc % 4 == 0) && aligned(C, (uintptr_t)(4 * es));
   if (args.vec && (ldc * es) % 16 == 0 && aligned(C, 16)) args.vec |= 2;  // 16-byte rows
   args.stream = static_cast<hipStream_t>(stream);
+  int st = FBG_SUCCESS;
+  const int cus = device_cu_count(&st);
+  if (st != FBG_SUCCESS) return st;
   const int force = forced_config();
-  const hipError_t err = fbg::launch_i8(args, force);
+  const hipError_t err = fbg::launch_i8(args, cus, force);
   if (err == hipErrorInvalidValue && force >= 0) return FBG_ERROR_UNSUPPORTED;
   return err == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }

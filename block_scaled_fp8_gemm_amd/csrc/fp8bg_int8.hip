@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "fp8bg_device.hpp"
+#include "fp8bg_int8_configs.h"
 #include "fp8bg_internal.h"
 
 namespace fbg {
@@ -526,183 +527,114 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
     si[i] = a.bias ? a.bias[n] : 0.0f;
   }
 
-  auto scales_to_lds = [&] {
+  // A step's refill is spread over SPREAD slices, the last one of the step
+  // that frees the slot and the first ones of the step after it: load q goes
+  // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
+  // belong to the first part.
+  constexpr int NM = IB * JB;
+  constexpr int LPS0 = (LPS + SPREAD - 1) / SPREAD;
 #pragma unroll
-    for (int i = 0; i < SA; ++i)
-      if (i * NT + tid < BM) as_t[i * NT + tid] = sa[i];
+  for (int p = 0; p < STAGES; ++p)
+    if (p < nk) {
+      const uint32_t sub = p == nk - 1 ? tail : 0u;
 #pragma unroll
-    for (int i = 0; i < SB; ++i)
-      if (i * NT + tid < BN) {
-        bs_t[i * NT + tid] = sb[i];
-        bi_t[i * NT + tid] = si[i];
+      for (int i = 0; i < (p < STAGES - 1 ? LPS : LPS0); ++i) load_one(p, p, i, sub);
+    }
+#pragma unroll
+  for (int i = 0; i < SA; ++i)
+    if (i * NT + tid < BM) as_t[i * NT + tid] = sa[i];
+#pragma unroll
+  for (int i = 0; i < SB; ++i)
+    if (i * NT + tid < BN) {
+      bs_t[i * NT + tid] = sb[i];
+      bi_t[i * NT + tid] = si[i];
+    }
+  if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS + LPS0));
+  else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+  __builtin_amdgcn_s_barrier();
+  v4i fa[2][IB], fb[2][JB];
+#pragma unroll
+  for (int i = 0; i < IB; ++i) fa[0][i] = frag(0, 0, wm * WM + 32 * i, 0);
+#pragma unroll
+  for (int j = 0; j < JB; ++j) fb[0][j] = frag(0, A_BYTES, wn * WN + 32 * j, 0);
+
+  // One step.  kPrev: the rest of the refill that the step before began;
+  // kRefill: the first part of this slot's, with the step STAGES ahead; kNext:
+  // another step follows (the last one masks its tail instead).  The order of
+  // MFMAs, fragment reads and loads is pinned, a read or load behind an MFMA,
+  // so that none of them holds up the MFMA after it for long.
+  auto step = [&](int k, int slot, auto prev, auto refill, auto more) {
+    constexpr bool kPrev = decltype(prev)::value, kRefill = decltype(refill)::value, kNext = decltype(more)::value;
+    const int next = slot + 1 == STAGES ? 0 : slot + 1, before = slot == 0 ? STAGES - 1 : slot - 1;
+    uint32_t sub = 0, sub_prev = 0;
+    if constexpr (kRefill) sub = k + STAGES == nk - 1 ? tail : 0u;
+    if constexpr (kPrev) sub_prev = k - 1 + STAGES == nk - 1 ? tail : 0u;
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      const int cur = s & 1, nxt = cur ^ 1;
+      if (s == SL - 1 && kNext) {
+        // Every LDS read of this step has been issued: past the barrier the
+        // slot is free and the next step's tile is visible.
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(kPrev ? (STAGES - 2) * LPS : 0) & ~(15 << 8));
+        __builtin_amdgcn_s_barrier();
       }
-  };
-  if constexpr (SPREAD == 0) {
-    // Whole steps: all of a step's fragments are read one step ahead, behind
-    // the barrier that makes it visible, so that with few MFMAs per slice the
-    // latency of an LDS read is paid once per step and not once per slice.
-#pragma unroll
-    for (int p = 0; p < STAGES; ++p)
-      if (p < nk) {
-        const uint32_t sub = p == nk - 1 ? tail : 0u;
-#pragma unroll
-        for (int i = 0; i < LPS; ++i) load_one(p, p, i, sub);
-      }
-    scales_to_lds();
-    if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 1) * LPS));
-    else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
-    __builtin_amdgcn_s_barrier();
-    v4i fa[2][SL][IB], fb[2][SL][JB];
-    auto fetch = [&](int slot, v4i (&A_)[SL][IB], v4i (&B_)[SL][JB]) {
-#pragma unroll
-      for (int s = 0; s < SL; ++s) {
-#pragma unroll
-        for (int i = 0; i < IB; ++i) A_[s][i] = frag(slot, 0, wm * WM + 32 * i, s);
-#pragma unroll
-        for (int j = 0; j < JB; ++j) B_[s][j] = frag(slot, A_BYTES, wn * WN + 32 * j, s);
-      }
-    };
-    fetch(0, fa[0], fb[0]);
-    auto step = [&](int k, int slot, v4i (&A_)[SL][IB], v4i (&B_)[SL][JB], v4i (&An)[SL][IB], v4i (&Bn)[SL][JB]) {
-      // This step's fragments are in registers; past the barrier its slot is
-      // free and the next step's tile is visible.
-      if (k + STAGES - 1 < nk) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS) & ~(15 << 8));
-      else __builtin_amdgcn_s_waitcnt(vmcnt_only(0) & ~(15 << 8));
-      __builtin_amdgcn_s_barrier();
-      if (k + 1 < nk) fetch(slot + 1 == STAGES ? 0 : slot + 1, An, Bn);
-      __builtin_amdgcn_sched_barrier(0);
-      if (k + STAGES < nk) {
-        const uint32_t sub = k + STAGES == nk - 1 ? tail : 0u;
-#pragma unroll
-        for (int i = 0; i < LPS; ++i) load_one(k + STAGES, slot, i, sub);
-      }
-      if (k == nk - 1 && a.K % BK != 0) {
-#pragma unroll
-        for (int s = 0; s < SL; ++s) {
+      if constexpr (!kNext) {
+        if (a.K % BK != 0) {
           const bool in = k * BK + 16 * (2 * s + fh) < a.K;
 #pragma unroll
-          for (int i = 0; i < IB; ++i) A_[s][i] = in ? A_[s][i] : v4i{0, 0, 0, 0};
+          for (int i = 0; i < IB; ++i) fa[cur][i] = in ? fa[cur][i] : v4i{0, 0, 0, 0};
         }
       }
+      const int rs = s == SL - 1 ? next : slot, ss = (s + 1) % SL;
+      const bool reads = s < SL - 1 || kNext;
 #pragma unroll
-      for (int s = 0; s < SL; ++s)
+      for (int i = 0; i < IB; ++i)
 #pragma unroll
-        for (int i = 0; i < IB; ++i)
+        for (int j = 0; j < JB; ++j) {
+          const int t = i * JB + j;
+          __builtin_amdgcn_sched_barrier(0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if (reads) {  // A 0, B 0 .., A 1 ..: the order the next slice needs them in
+            constexpr int R = (IB + JB + NM - 1) / NM;
 #pragma unroll
-          for (int j = 0; j < JB; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(B_[s][j], A_[s][i], acc[i][j], 0, 0, 0);
-    };
-    int slot = 0;
-    for (int k = 0; k < nk; k += 2) {
-      step(k, slot, fa[0], fb[0], fa[1], fb[1]);
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-      if (k + 1 < nk) {
-        step(k + 1, slot, fa[1], fb[1], fa[0], fb[0]);
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
-      }
-    }
-  } else {
-    // A step's refill is spread over SPREAD slices, the last one of the step
-    // that frees the slot and the first ones of the step after it: load q goes
-    // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
-    // belong to the first part.
-    constexpr int NM = IB * JB;
-    constexpr int LPS0 = (LPS + SPREAD - 1) / (SPREAD > 0 ? SPREAD : 1);
-#pragma unroll
-    for (int p = 0; p < STAGES; ++p)
-      if (p < nk) {
-        const uint32_t sub = p == nk - 1 ? tail : 0u;
-#pragma unroll
-        for (int i = 0; i < (p < STAGES - 1 ? LPS : LPS0); ++i) load_one(p, p, i, sub);
-      }
-    scales_to_lds();
-    if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS + LPS0));
-    else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
-    __builtin_amdgcn_s_barrier();
-    v4i fa[2][IB], fb[2][JB];
-#pragma unroll
-    for (int i = 0; i < IB; ++i) fa[0][i] = frag(0, 0, wm * WM + 32 * i, 0);
-#pragma unroll
-    for (int j = 0; j < JB; ++j) fb[0][j] = frag(0, A_BYTES, wn * WN + 32 * j, 0);
-
-    // One step.  kPrev: the rest of the refill that the step before began;
-    // kRefill: the first part of this slot's, with the step STAGES ahead; kNext:
-    // another step follows (the last one masks its tail instead).  The order of
-    // MFMAs, fragment reads and loads is pinned, a read or load behind an MFMA,
-    // so that none of them holds up the MFMA after it for long.
-    auto step = [&](int k, int slot, auto prev, auto refill, auto more) {
-      constexpr bool kPrev = decltype(prev)::value, kRefill = decltype(refill)::value, kNext = decltype(more)::value;
-      const int next = slot + 1 == STAGES ? 0 : slot + 1, before = slot == 0 ? STAGES - 1 : slot - 1;
-      uint32_t sub = 0, sub_prev = 0;
-      if constexpr (kRefill) sub = k + STAGES == nk - 1 ? tail : 0u;
-      if constexpr (kPrev) sub_prev = k - 1 + STAGES == nk - 1 ? tail : 0u;
-#pragma unroll
-      for (int s = 0; s < SL; ++s) {
-        const int cur = s & 1, nxt = cur ^ 1;
-        if (s == SL - 1 && kNext) {
-          // Every LDS read of this step has been issued: past the barrier the
-          // slot is free and the next step's tile is visible.
-          __builtin_amdgcn_s_waitcnt(vmcnt_only(kPrev ? (STAGES - 2) * LPS : 0) & ~(15 << 8));
-          __builtin_amdgcn_s_barrier();
-        }
-        if constexpr (!kNext) {
-          if (a.K % BK != 0) {
-            const bool in = k * BK + 16 * (2 * s + fh) < a.K;
-#pragma unroll
-            for (int i = 0; i < IB; ++i) fa[cur][i] = in ? fa[cur][i] : v4i{0, 0, 0, 0};
-          }
-        }
-        const int rs = s == SL - 1 ? next : slot, ss = (s + 1) % SL;
-        const bool reads = s < SL - 1 || kNext;
-#pragma unroll
-        for (int i = 0; i < IB; ++i)
-#pragma unroll
-          for (int j = 0; j < JB; ++j) {
-            const int t = i * JB + j;
-            __builtin_amdgcn_sched_barrier(0);
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            if (reads) {  // A 0, B 0 .., A 1 ..: the order the next slice needs them in
-              constexpr int R = (IB + JB + NM - 1) / NM;
-#pragma unroll
-              for (int q = t * R; q < t * R + R && q < IB + JB; ++q) {
-                if (q == 0) fa[nxt][0] = frag(rs, 0, wm * WM, ss);
-                else if (q <= JB) fb[nxt][q - 1 < JB ? q - 1 : 0] = frag(rs, A_BYTES, wn * WN + 32 * (q - 1), ss);
-                else fa[nxt][q - JB < IB ? q - JB : 0] = frag(rs, 0, wm * WM + 32 * (q - JB), ss);
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < LPS; ++q) {
-              const int at = q < LPS0 ? q * NM / LPS0 : NM + (q - LPS0) * ((SPREAD - 1) * NM) / (LPS - LPS0 > 0 ? LPS - LPS0 : 1);
-              if (kRefill && s == SL - 1 && at == t) load_one(k + STAGES, slot, q, sub);
-              if (kPrev && s < SL - 1 && at == (s + 1) * NM + t) load_one(k - 1 + STAGES, before, q, sub_prev);
+            for (int q = t * R; q < t * R + R && q < IB + JB; ++q) {
+              if (q == 0) fa[nxt][0] = frag(rs, 0, wm * WM, ss);
+              else if (q <= JB) fb[nxt][q - 1 < JB ? q - 1 : 0] = frag(rs, A_BYTES, wn * WN + 32 * (q - 1), ss);
+              else fa[nxt][q - JB < IB ? q - JB : 0] = frag(rs, 0, wm * WM + 32 * (q - JB), ss);
             }
           }
-      }
-    };
-    constexpr std::true_type yes{};
-    constexpr std::false_type no{};
-    int slot = 0, k = 0;
-    auto advance = [&] {
-      ++k;
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-    };
-    while (k + STAGES < nk) {
-      step(k, slot, yes, yes, yes);
-      advance();
+#pragma unroll
+          for (int q = 0; q < LPS; ++q) {
+            const int at = q < LPS0 ? q * NM / LPS0 : NM + (q - LPS0) * ((SPREAD - 1) * NM) / (LPS - LPS0 > 0 ? LPS - LPS0 : 1);
+            if (kRefill && s == SL - 1 && at == t) load_one(k + STAGES, slot, q, sub);
+            if (kPrev && s < SL - 1 && at == (s + 1) * NM + t) load_one(k - 1 + STAGES, before, q, sub_prev);
+          }
+        }
     }
-    if (k + STAGES == nk) {
-      step(k, slot, yes, no, yes);
-      advance();
-    }
-    if constexpr (STAGES > 2) {
-      while (k + 1 < nk) {
-        step(k, slot, no, no, yes);
-        advance();
-      }
-    }
-    step(k, slot, no, no, no);
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  int slot = 0, k = 0;
+  auto advance = [&] {
+    ++k;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+  };
+  while (k + STAGES < nk) {
+    step(k, slot, yes, yes, yes);
+    advance();
   }
+  if (k + STAGES == nk) {
+    step(k, slot, yes, no, yes);
+    advance();
+  }
+  if constexpr (STAGES > 2) {
+    while (k + 1 < nk) {
+      step(k, slot, no, no, yes);
+      advance();
+    }
+  }
+  step(k, slot, no, no, no);
   __syncthreads();
   const float *as_w = as_t + wm * WM, *bs_w = bs_t + wn * WN, *bi_w = bi_t + wn * WN;
   const int mw = m0 + wm * WM, nw = n0 + wn * WN;
@@ -750,36 +682,6 @@ __global__ __launch_bounds__(256) void k_i8_short(I8Args a) {
   store1<OUT>(a.C, m * a.ldc + n, c);
 }
 
-// Kernel configurations: X(index, kernel, its sizes).
-#define FBG_I8_CFGS(X)                \
-  X(0, ANY, 64, 64, 4)                \
-  X(1, TILE, 256, 256, 2, 2, 128, 2, 2) \
-  X(2, TILE, 256, 128, 2, 2, 128, 3, 2) \
-  X(3, TILE, 128, 256, 2, 2, 128, 3, 2) \
-  X(4, TILE, 128, 128, 2, 2, 128, 4, 0) \
-  X(5, TILE, 128, 128, 2, 2, 128, 2, 2) \
-  X(6, TILE, 64, 128, 2, 2, 128, 3, 2)  \
-  X(7, TILE, 64, 128, 2, 2, 128, 3, 0)  \
-  X(8, TILE, 64, 64, 2, 2, 128, 4, 2)   \
-  X(9, SKINNY, 1, 8, 8, 8)              \
-  X(10, SKINNY, 1, 16, 8, 8)            \
-  X(11, TILE, 64, 64, 2, 2, 128, 4, 0)  \
-  X(12, SKINNY, 2, 16, 8, 4)            \
-  X(13, TILE, 32, 64, 1, 2, 128, 4, 0)  \
-  X(14, TILE, 64, 64, 2, 2, 128, 8, 0)  \
-  X(15, TILE, 32, 64, 1, 2, 128, 6, 0)  \
-  X(16, TILE, 32, 128, 1, 4, 128, 3, 0) \
-  X(17, TILE, 32, 128, 1, 4, 128, 7, 0) \
-  X(18, TILE, 128, 128, 2, 2, 128, 2, 0) \
-  X(19, TILE, 64, 128, 2, 2, 128, 6, 0) \
-  X(20, TILE, 32, 64, 1, 2, 128, 4, 2)  \
-  X(21, TILE, 64, 256, 1, 4, 128, 3, 0) \
-  X(22, ANY, 128, 128, 2) \
-  X(23, ANY, 64, 64, 2) \
-  X(24, ANY, 32, 64, 4) \
-  X(25, ANY, 64, 64, 8) \
-  X(26, ANY, 128, 128, 4)
-
 template <int BM, int BN, int AHEAD, int GRP>
 void start_any(const I8Args& a, dim3 g) {
   switch (a.out) {
@@ -790,31 +692,26 @@ void start_any(const I8Args& a, dim3 g) {
 }
 
 template <int BM, int BN, int AHEAD>
-hipError_t launch_ANY(const I8Args& a) {
-  const int64_t tn = (a.N + BN - 1) / BN, tm = a.offsets ? (int64_t)a.M / BM + a.E : ((int64_t)a.M + BM - 1) / BM;
-  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 g((unsigned)(tm * tn));
+hipError_t launch_ANY(const I8Args& a, unsigned grid) {
+  const dim3 g(grid);
   if (a.offsets) start_any<BM, BN, AHEAD, 1>(a, g);
   else start_any<BM, BN, AHEAD, 0>(a, g);
   return hipGetLastError();
 }
 
 template <int BM, int BN, int WM_, int WN_, int BK, int ST, int SP>
-hipError_t launch_TILE(const I8Args& a) {
+hipError_t launch_TILE(const I8Args& a, unsigned grid) {
   if (!fast_rows(a)) return hipErrorInvalidValue;
-  const int64_t tn = (a.N + BN - 1) / BN, tm = a.offsets ? (int64_t)a.M / BM + a.E : ((int64_t)a.M + BM - 1) / BM;
-  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 g((unsigned)(tm * tn)), b(64 * WM_ * WN_);
+  const dim3 g(grid), b(64 * WM_ * WN_);
   if (a.offsets) hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 1>), g, b, 0, a.stream, a);
   else hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 0>), g, b, 0, a.stream, a);
   return hipGetLastError();
 }
 
-template <int NB, int ROWS, int KW, int U>
-hipError_t launch_SKINNY(const I8Args& a) {
-  const int64_t tn = (a.N + 16 * NB - 1) / (16 * NB), tm = a.offsets ? a.E : ((int64_t)a.M + ROWS - 1) / ROWS;
-  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 g((unsigned)(tm * tn)), b(64 * KW);
+template <int ROWS, int COLS, int KW, int U>
+hipError_t launch_SKINNY(const I8Args& a, unsigned grid) {
+  constexpr int NB = COLS / 16;
+  const dim3 g(grid), b(64 * KW);
   if (fast_rows(a)) {
     if (a.offsets) hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 1>), g, b, 0, a.stream, a);
     else hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 0>), g, b, 0, a.stream, a);
@@ -827,7 +724,7 @@ hipError_t launch_SKINNY(const I8Args& a) {
 
 }  // namespace
 
-hipError_t launch_i8(const I8Args& a, int force_cfg) {
+hipError_t launch_i8(const I8Args& a, int cus, int force_cfg) {
   if (a.K < 16) {
     if (a.K > 0 && force_cfg >= 0) return hipErrorInvalidValue;
     const int64_t grid = ((int64_t)a.M * a.N + 255) / 256;
@@ -840,20 +737,14 @@ hipError_t launch_i8(const I8Args& a, int force_cfg) {
     }
     return hipGetLastError();
   }
-  int cfg = force_cfg;
-  if (cfg < 0) {
-    // The largest tile that still gives every compute unit one.
-    auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-    if (!fast_rows(a)) cfg = 0;
-    else if (tiles(256, 256) >= 192) cfg = 1;
-    else if (tiles(256, 128) >= 192) cfg = 2;
-    else if (tiles(128, 128) >= 256) cfg = 5;
-    else if (tiles(64, 128) >= 256) cfg = 6;
-    else cfg = 8;
-  }
+  const int64_t E = a.offsets ? a.E : 0;
+  const int cfg = force_cfg >= 0 ? force_cfg : int8_cfg_for(E, a.M, a.N, a.K, fast_rows(a), cus);
+  if (cfg >= kNumI8Cfgs) return hipErrorInvalidValue;
+  const int64_t grid = int8_grid(cfg, E, a.M, a.N);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
   switch (cfg) {
 #define X(id, kind, ...) \
-  case id: return launch_##kind<__VA_ARGS__>(a);
+  case id: return launch_##kind<__VA_ARGS__>(a, (unsigned)grid);
     FBG_I8_CFGS(X)
 #undef X
   }

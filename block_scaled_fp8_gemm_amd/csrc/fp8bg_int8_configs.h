@@ -1,0 +1,39 @@
+// Kernel configurations of the int8 products and the choice among them (host
+// code without HIP, shared by the planner and the launcher).
+#pragma once
+
+#include <stdint.h>
+
+namespace fbg {
+
+// X(index, kernel, rows, columns, then the kernel's other sizes)
+//   ANY: rows x columns tile, steps in flight (any alignment)
+//   SKINNY: rows, 16-column blocks, waves, K slices per group
+//   TILE: rows x columns tile, waves of each, K bytes per step, ring slots,
+//         slices a refill is spread over (16-byte rows)
+#define FBG_I8_CFGS(X)                   \
+  X(0, ANY, 64, 64, 2)                   \
+  X(1, ANY, 32, 64, 4)                   \
+  X(2, SKINNY, 8, 16, 8, 8)              \
+  X(3, SKINNY, 16, 16, 8, 8)             \
+  X(4, SKINNY, 16, 32, 8, 4)             \
+  X(5, TILE, 32, 64, 1, 2, 128, 4, 2)    \
+  X(6, TILE, 64, 64, 2, 2, 128, 4, 2)    \
+  X(7, TILE, 64, 128, 2, 2, 128, 3, 2)   \
+  X(8, TILE, 128, 128, 2, 2, 128, 2, 2)  \
+  X(9, TILE, 128, 256, 2, 2, 128, 3, 2)  \
+  X(10, TILE, 256, 256, 2, 2, 128, 2, 2)
+
+constexpr int kNumI8Cfgs = 11;
+constexpr int kI8FirstTile = 5;  // configurations from here on take 16-byte rows only
+constexpr int kI8FirstSkinny = 2;
+
+// The configuration for M rows (of E experts in the grouped form, E = 0 for
+// the dense one), N columns and K bytes on a device of `cus` compute units;
+// `fast`: the rows start on 16-byte boundaries and hold whole 16-byte chunks.
+int int8_cfg_for(int64_t E, int64_t M, int64_t N, int64_t K, bool fast, int cus);
+
+// The launch grid of a configuration (workgroups; may exceed INT32_MAX).
+int64_t int8_grid(int cfg, int64_t E, int64_t M, int64_t N);
+
+}  // namespace fbg

@@ -72,9 +72,9 @@ struct I8Args {
   int vec;  // as GemmArgs::vec, with ldc for the row pitch
   hipStream_t stream;
 };
-// force_cfg >= 0: that kernel configuration (hipErrorInvalidValue if it does
+// cus: the device's compute units.  force_cfg >= 0: that configuration (hipErrorInvalidValue if it does
 // not take these operands).
-hipError_t launch_i8(const I8Args& a, int force_cfg);
+hipError_t launch_i8(const I8Args& a, int cus, int force_cfg);
 
 // One row per token (fp8bg_rows.hip).  dtype: the FBG_OUT_* code of x, h,
 // gate and r; rows ld* elements apart.

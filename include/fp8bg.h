@@ -32,7 +32,7 @@
  * Environment variables (tuning and test hooks, read on every call; unset in
  * normal use): FBG_FORCE_CONFIG=<i> pins the tile configuration index of the
  * chosen variant (for fp8_block_gemm_grouped, the grouped configuration
- * index); an index that does not exist -> UNSUPPORTED.  FBG_RASTER_BAND=<rows>
+ * index; for the int8 products, theirs); an index that does not exist -> UNSUPPORTED.  FBG_RASTER_BAND=<rows>
  * sets the generic kernel's raster band height (default 8).  FBG_LOG=1
  * prints each call's plan to stderr.  FBG_TEST_FAIL_ALLOC=1 makes the
  * library-owned split-K workspace allocation fail (OUT_OF_MEMORY), for tests.
@@ -68,7 +68,8 @@ enum {
     FBG_VARIANT_SHORT_K256 = 2,    /* K == 256: both groups unrolled, a_s*b_s pre-folded */
     FBG_VARIANT_SWAP_AB = 3,       /* C^T = B A^T: weight rows on the 16-row MFMA side, small M on the other */
     FBG_VARIANT_SWAP_AB_SPLITK = 4, /* swap-AB with K split over workgroups, fixed-order FP32 reduction */
-    FBG_VARIANT_GROUPED = 5        /* reported by fp8_block_gemm_grouped_plan only; not a forcible variant */
+    FBG_VARIANT_GROUPED = 5,       /* reported by fp8_block_gemm_grouped_plan only; not a forcible variant */
+    FBG_VARIANT_INT8 = 6           /* reported by fbg_int8_plan only */
 };
 
 /* One dispatcher decision (pure data, filled by fp8_block_gemm_plan). */
@@ -305,6 +306,18 @@ int fbg_int8_gemm(const void *A, int64_t lda, const float *a_s, const void *B, i
 int fbg_int8_grouped_gemm(const void *A, int64_t lda, const float *a_s, const void *B, const float *b_s, void *C,
                           int64_t ldc, const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
                           int out_dtype, void *stream);
+
+/*
+ * fbg_int8_plan -- the tile configuration that fbg_int8_gemm (E == 0) or
+ * fbg_int8_grouped_gemm (E experts holding M rows in total) takes on a device
+ * of cu_count compute units: variant FBG_VARIANT_INT8, the tile's rows and
+ * columns, waves, configuration index and grid.  aligned_rows: whether A's and
+ * B's rows start on 16-byte boundaries.  config -1, grid 0: no tile kernel
+ * (nothing to do, or K < 16: one thread per output).  Pure host code; statuses
+ * as for the products.  FBG_FORCE_CONFIG pins the products' configuration and
+ * is not read here.
+ */
+int fbg_int8_plan(int64_t E, int64_t M, int64_t N, int64_t K, int aligned_rows, int cu_count, fbg_plan *out);
 
 /*
  * fbg_quantize_tokens -- per-row symmetric int8 quantisation of x [M,K]

@@ -34,7 +34,8 @@ def _norm(h=P, ldh=256, x=2 * P, ldx=256, gate=None, grow=0, gcol=0, post=3 * P,
 def test_every_declared_function_is_exported():
     text = open(os.path.join(ROOT, "include", "fp8bg.h")).read()
     names = set(re.findall(r"^int (fbg_\w+)\(", text, re.M))
-    assert names == {"fbg_int8_gemm", "fbg_int8_grouped_gemm", "fbg_quantize_tokens", "fbg_block_norm"}
+    assert names == {"fbg_int8_gemm", "fbg_int8_grouped_gemm", "fbg_quantize_tokens", "fbg_block_norm",
+                     "fbg_int8_plan"}
     for n in names:
         assert isinstance(getattr(fbg.load(), n), ctypes._CFuncPtr)
 
@@ -106,3 +107,39 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
         fbg.quantize_tokens(torch.zeros(4, 64))
     with pytest.raises(ValueError):
         fbg.block_norm(torch.zeros(4, 64))
+
+
+def test_plan():
+    for M, N, K, want in [(1, 4096, 4096, (2, 3)), (64, 512, 4096, (2, 3)), (16384, 4096, 4096, (10,)), (128, 8192, 1024, (5, 6))]:
+        p = fbg.int8_plan(M, N, K)
+        assert p["variant_name"] == "int8" and p["config"] in want, (M, N, K, p)
+        assert p["grid"] == -(-M // p["tile_m"]) * -(-N // p["tile_n"])
+        assert p["split_k"] == 1 and p["workspace_bytes"] == 0
+    # rows that are not whole 16-byte chunks never take the direct-to-LDS tiles
+    for M in (1, 40, 300, 5000):
+        assert fbg.int8_plan(M, 1000, 4096, aligned_rows=False)["config"] < 5
+        assert fbg.int8_plan(M, 1000, 1001)["config"] < 5
+    # small experts: long K over few of them on the skinny kernel; the grouped
+    # grid bounds the experts' row tiles by floor(M / rows) + E
+    assert fbg.int8_plan(64, 512, 4096, E=8)["config"] == 3
+    p = fbg.int8_plan(512, 512, 4096, E=256)
+    assert p["config"] == 5 and p["grid"] == (512 // 32 + 256) * 8
+    assert fbg.int8_plan(32768, 512, 4096, E=256)["config"] >= 7
+    assert fbg.int8_plan(0, 512, 4096)["config"] == -1 and fbg.int8_plan(7, 9, 15)["config"] == -1
+    for kw in ({"M": -1}, {"E": -1}, {"cu_count": 0}):
+        with pytest.raises(fbg.FP8BGError) as e:
+            fbg.int8_plan(**{"M": 4, "N": 4, "K": 64, **kw})
+        assert e.value.status == fbg.INVALID_VALUE
+    with pytest.raises(fbg.FP8BGError) as e:
+        fbg.int8_plan(4, 4, 131072)
+    assert e.value.status == fbg.UNSUPPORTED
+
+
+def test_every_configuration_is_chosen_for_some_shape():
+    seen = set()
+    for aligned in (True, False):
+        for M in (1, 4, 12, 16, 24, 48, 100, 200, 400, 1000, 2048, 4096, 16384):
+            for N in (64, 512, 1536, 4096, 8192):
+                for K in (256, 1024, 4096):
+                    seen.add(fbg.int8_plan(M, N, K, aligned_rows=aligned)["config"])
+    assert seen == set(range(11)), seen
