@@ -14,9 +14,9 @@ namespace fbg {
 #define FBG_I8_CFGS(X)                   \
   X(0, ANY, 64, 64, 2)                   \
   X(1, ANY, 32, 64, 4)                   \
-  X(2, SKINNY, 8, 16, 8, 8)              \
-  X(3, SKINNY, 16, 16, 8, 8)             \
-  X(4, SKINNY, 16, 32, 8, 4)             \
+  X(2, SKINNY, 8, 16, 8, 4)              \
+  X(3, SKINNY, 16, 16, 8, 4)             \
+  X(4, SKINNY, 16, 32, 4, 4)             \
   X(5, TILE, 32, 64, 1, 2, 128, 4, 2)    \
   X(6, TILE, 64, 64, 2, 2, 128, 4, 2)    \
   X(7, TILE, 64, 128, 2, 2, 128, 3, 2)   \

@@ -16,9 +16,10 @@ enum Kind { ANY, SKINNY, TILE };
 // and `again` is the share of `start` that a queued round still shows.
 // Least-squares fits in the logarithm to 167 dense shapes of M 1 .. 16384, N
 // 64 .. 8192 and K 256, 1024 and 4096 (configurations 2-10, 16-byte rows; the
-// fits' own deviation is 4-13%) and to 79 of the same range with odd K (any
-// rows).  Choosing by it costs 2.0% over the best configuration of each shape
-// on average (any rows: 2.9%).
+// fits' own deviation is 4-10%) and to 79 of the same range with odd K (any
+// rows; 9-22%), `per_cu` being the count that fits best, not an occupancy.
+// Choosing by it costs 1.9% over the best configuration of each shape on
+// average (any rows: 1.8%), 20% at worst.
 struct Cost {
   Kind kind;
   int rows, cols, per_cu, waves;
@@ -27,9 +28,9 @@ struct Cost {
 constexpr Cost kFast[kNumI8Cfgs] = {
     {ANY, 64, 64, 4, 4, 0, 0, 0, 0},
     {ANY, 32, 64, 4, 4, 0, 0, 0, 0},
-    {SKINNY, 8, 16, 3, 8, 2.615f, 0.075f, 0.264f, 0.654f},
-    {SKINNY, 16, 16, 3, 8, 2.655f, 0.081f, 0.328f, 0.744f},
-    {SKINNY, 16, 32, 3, 8, 2.385f, 0.151f, 0.549f, 0.800f},
+    {SKINNY, 8, 16, 8, 8, 2.380f, 0.073f, 0.745f, 0.643f},
+    {SKINNY, 16, 16, 8, 8, 2.341f, 0.084f, 0.910f, 0.661f},
+    {SKINNY, 16, 32, 8, 4, 2.309f, 0.148f, 1.378f, 0.975f},
     {TILE, 32, 64, 3, 2, 2.700f, 0.218f, 0.455f, 0.751f},
     {TILE, 64, 64, 2, 4, 2.828f, 0.238f, 0.447f, 0.667f},
     {TILE, 64, 128, 2, 4, 3.343f, 0.280f, 0.697f, 0.841f},
@@ -38,11 +39,11 @@ constexpr Cost kFast[kNumI8Cfgs] = {
     {TILE, 256, 256, 1, 4, 11.821f, 0.976f, 1.581f, 0.975f},
 };
 constexpr Cost kAny[kI8FirstTile] = {
-    {ANY, 64, 64, 4, 4, 4.169f, 0.367f, 1.924f, 1.769f},
-    {ANY, 32, 64, 4, 4, 3.796f, 0.240f, 1.487f, 1.532f},
-    {SKINNY, 8, 16, 3, 8, 3.263f, 0.176f, 0.901f, 0.629f},
-    {SKINNY, 16, 16, 3, 8, 3.174f, 0.206f, 1.046f, 0.826f},
-    {SKINNY, 16, 32, 3, 8, 3.135f, 0.329f, 1.429f, 0.736f},
+    {ANY, 64, 64, 2, 4, 4.149f, 0.391f, 0.922f, 0.983f},
+    {ANY, 32, 64, 1, 4, 3.584f, 0.299f, 0.316f, 0.578f},
+    {SKINNY, 8, 16, 2, 8, 3.019f, 0.178f, 0.537f, 0.250f},
+    {SKINNY, 16, 16, 1, 8, 3.066f, 0.223f, 0.304f, 0.216f},
+    {SKINNY, 16, 32, 1, 4, 3.141f, 0.401f, 0.487f, 0.285f},
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -63,16 +64,16 @@ int int8_cfg_for(int64_t E, int64_t M, int64_t N, int64_t K, bool fast, int cus)
   const double mean = E > 0 ? (double)M / (double)E : 0.0;
   if (E > 0 && mean <= 12.0) {
     // Small experts: the weights of those that hold rows are what is read.
-    // 16-byte rows: the 32 x 64 tile (256 experts of 512 x 4096, 64 tokens of 8
-    // experts each: 97 us, skinny 93-100, 64 x 128 tile 103; of 1536 x 1024:
-    // 64 us against 91-127 and 64), except over a long K with at most two
-    // skinny workgroups per compute unit, where those are faster (8 experts
-    // of 512 x 4096: 5.6 us at 64 rows, 10.4 in the tile).  Any rows: the
-    // 32-column skinny form up to about one workgroup per compute unit (64
-    // rows over 64 experts of 512 x 1000: 6.4 us, the 32 x 64 tile 6.4; 8
-    // experts: 4.0 against 5.1), else the 32 x 64 tile (256 experts: 27.7 us
-    // against 32.9).
-    if (fast) return K >= 2048 && E * ceil_div(N, 16) <= 2 * cus ? 3 : 5;
+    // 16-byte rows: over a long K the skinny kernel streams them best (64
+    // tokens, 8 of 256 experts of 512 x 4096: 83 us in 32-column workgroups of
+    // 4 waves, 5.5 TB/s; 32 x 64 tile 97; 8 rows to a expert on average: 105
+    // against 110), in 16 columns while that makes at most two workgroups per
+    // compute unit (8 experts: 5.6 us, 32 columns 7.5, the tile 10.5); over a
+    // short K the tile does (of 1536 x 1024: 64 us, skinny 71).  Any rows: the
+    // 32-column skinny form up to a few workgroups per compute unit (64 rows
+    // over 8 experts of 515 x 776: 4.0 us, the 32 x 64 tile 5.1), else the
+    // 32 x 64 tile (256 experts: 27.7 us against 32.9).
+    if (fast) return K < 2048 ? 5 : E * ceil_div(N, 16) <= 2 * cus ? 3 : 4;
     return E * ceil_div(N, 32) <= 4 * cus ? 4 : 1;
   }
   // A skinny workgroup walks an expert's rows one pass after the other.

@@ -123,6 +123,8 @@ def test_plan():
     # grid bounds the experts' row tiles by floor(M / rows) + E
     assert fbg.int8_plan(64, 512, 4096, E=8)["config"] == 3
     p = fbg.int8_plan(512, 512, 4096, E=256)
+    assert p["config"] == 4 and p["grid"] == 256 * 16
+    p = fbg.int8_plan(512, 512, 1024, E=256)
     assert p["config"] == 5 and p["grid"] == (512 // 32 + 256) * 8
     assert fbg.int8_plan(32768, 512, 4096, E=256)["config"] >= 7
     assert fbg.int8_plan(0, 512, 4096)["config"] == -1 and fbg.int8_plan(7, 9, 15)["config"] == -1
