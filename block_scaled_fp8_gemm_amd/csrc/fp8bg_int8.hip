@@ -65,6 +65,14 @@ __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, 
   return e_out >= 0;
 }
 
+// An fp32 value as it is rounded: a product whose conversion to fp16 follows
+// becomes one instruction with one rounding otherwise, which is not what the
+// other kernels and types give (it differs in about one value of 1e5).
+__device__ __forceinline__ float rounded(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
 // c = (a_s * b_s) * acc (+ bias) for 4 consecutive columns n .. n+3 of one
 // row; columns at or past N are not read.
 __device__ __forceinline__ v4f scale4(const v4i& acc, float as, const float* __restrict__ b_s,
@@ -73,7 +81,7 @@ __device__ __forceinline__ v4f scale4(const v4i& acc, float as, const float* __r
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int nn = n + r < N ? n + r : N - 1;
-    c[r] = (as * b_s[nn]) * (float)acc[r];
+    c[r] = rounded((as * b_s[nn]) * (float)acc[r]);
     if (bias) c[r] = c[r] + bias[nn];
   }
   return c;
@@ -347,56 +355,103 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 
 // Scales a wave's IB x JB blocks of 32 x 32 sums and stores them.  Block
 // (i, j), element 4q + r of lane l: row m = 32i + (l & 31), column
-// n = 32j + 8q + 4(l >> 5) + r.  Where C's rows are 16-byte aligned and the
-// columns are all there, 32 rows at a time go through the wave's own padded
-// slab of LDS and out as whole row segments, 16 bytes per lane (C is written
-// once and not read back: non-temporal); else 4 outputs per lane.
+// n = 32j + 8q + 4(l >> 5) + r.  32 rows of up to 128 bytes at a time go
+// through the wave's own padded slab of LDS, and from there out as whole row
+// segments, 16 bytes per lane (C is written once and not read back:
+// non-temporal), where C's rows are 16-byte aligned and the columns are all
+// there; else value by value.  The sums themselves pass no branch: with the
+// edge's tests around each of them the epilogue was 3600 basic blocks.
 //
 // as_t, bs_t, bi_t: the wave's row scales, column scales and bias in LDS
 // (loaded before the K loop: read from memory here, their latency would add
-// to every tile's end).
-template <int OUT, int IB, int JB>
+// to every tile's end; 16384 x 4096 x 4096 278 -> 248 us).
+template <int OUT, int JB>
+struct Slab {
+  static constexpr int ES = (int)sizeof(typename Out<OUT>::T);
+  static constexpr int JG = JB * 32 * ES <= 128 ? JB : 128 / (32 * ES);  // blocks side by side
+  static constexpr int ROWB = 32 * JG * ES, ROWP = ROWB + 16, BYTES = 32 * ROWP;
+  static constexpr int PER_ROW = ROWB / 16, STORES = 32 * PER_ROW / 64;
+};
+
+// Large tiles keep their sums in accumulator registers, and the compiler
+// would copy all of them to vector registers before the first is used (256 of
+// them: spills).  ACC_REGS: they are held there, past the last MFMA's wait
+// states, and read one at a time.
+template <int IB, int JB>
+constexpr bool kAccRegs = IB * JB >= 8;
+
+template <int IB, int JB>
+__device__ __forceinline__ void hold_sums(v16i (&acc)[IB][JB]) {
+  if constexpr (kAccRegs<IB, JB>) {
+    static_assert(JB == 4, "four operands");
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+      asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]));
+  }
+}
+
+template <bool ACC_REGS>
+__device__ __forceinline__ float sum_of(int v) {
+  if constexpr (ACC_REGS) {
+    int s;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(s) : "a"(v));
+    return (float)s;
+  } else {
+    return (float)v;
+  }
+}
+
+template <int OUT, bool BIAS, int IB, int JB>
 __device__ __forceinline__ void store_tile(const I8Args& a, const v16i (&acc)[IB][JB], uint8_t* slab,
                                            const float* as_t, const float* bs_t, const float* bi_t, int lane, int m0,
                                            int m_end, int n0) {
+  typedef Slab<OUT, JB> S;
   typedef typename Out<OUT>::T T;
-  constexpr int ES = (int)sizeof(T), ROWB = 32 * JB * ES, ROWP = ROWB + 16, PER_ROW = ROWB / 16;
   const int h = lane >> 5;
   const bool whole = (a.vec & 2) && n0 + 32 * JB <= a.N;
 #pragma unroll
   for (int i = 0; i < IB; ++i) {
-    const int m = m0 + 32 * i + (lane & 31);
     const float as = as_t[32 * i + (lane & 31)];
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int j0 = 0; j0 < JB; j0 += S::JG) {
+      // The column scales and the bias are read again for every row block:
+      // kept in registers they cost up to 128 of them, which spill, and a
+      // reload from scratch waits for every store before it.
+      asm volatile("" ::: "memory");
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = 32 * j + 8 * q + 4 * h;
-        const v4f bs = *reinterpret_cast<const v4f*>(bs_t + col);
-        v4f c;
+      for (int j = j0; j < j0 + S::JG; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) c[r] = (as * bs[r]) * (float)acc[i][j][4 * q + r];
-        if (a.bias) {
-          const v4f bi = *reinterpret_cast<const v4f*>(bi_t + col);
+        for (int q = 0; q < 4; ++q) {
+          const int col = 32 * j + 8 * q + 4 * h;
+          const v4f bs = *reinterpret_cast<const v4f*>(bs_t + col);
+          v4f c;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) c[r] = c[r] + bi[r];
+          for (int r = 0; r < 4; ++r) c[r] = rounded((as * bs[r]) * sum_of<kAccRegs<IB, JB>>(acc[i][j][4 * q + r]));
+          if constexpr (BIAS) {
+            const v4f bi = *reinterpret_cast<const v4f*>(bi_t + col);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[r] = c[r] + bi[r];
+          }
+          store4<OUT>(slab + (lane & 31) * S::ROWP, col - 32 * j0, c, 4, true);
         }
-        if (whole) {
-          store4<OUT>(slab + (lane & 31) * ROWP, col, c, 4, true);
-        } else {
-          const int cnt = a.N - (n0 + col) < 4 ? a.N - (n0 + col) : 4;
-          if (m < m_end && cnt > 0) store4<OUT>(a.C, (int64_t)m * a.ldc + n0 + col, c, cnt, a.vec & 1);
-        }
-      }
-    if (whole) {
+      uint8_t* base = reinterpret_cast<uint8_t*>(a.C) + ((int64_t)(m0 + 32 * i) * a.ldc + n0 + 32 * j0) * S::ES;
+      if (whole) {
 #pragma unroll
-      for (int t = 0; t < 32 * PER_ROW / 64; ++t) {
-        const int q = t * 64 + lane, row = q / PER_ROW, cb = (q % PER_ROW) * 16;
-        const int mm = m0 + 32 * i + row;
-        if (mm < m_end)
-          __builtin_nontemporal_store(*reinterpret_cast<const v4i*>(slab + row * ROWP + cb),
-                                      reinterpret_cast<v4i*>(reinterpret_cast<uint8_t*>(a.C) +
-                                                             ((int64_t)mm * a.ldc + n0) * ES + cb));
+        for (int t = 0; t < S::STORES; ++t) {
+          const int q = t * 64 + lane, row = q / S::PER_ROW, cb = (q % S::PER_ROW) * 16;
+          if (m0 + 32 * i + row < m_end)
+            __builtin_nontemporal_store(*reinterpret_cast<const v4i*>(slab + row * S::ROWP + cb),
+                                        reinterpret_cast<v4i*>(base + (int64_t)row * a.ldc * S::ES + cb));
+        }
+      } else {
+        const int cols = a.N - (n0 + 32 * j0);
+#pragma unroll 1
+        for (int q = lane; q < 32 * 32 * S::JG; q += 64) {
+          const int row = q / (32 * S::JG), c = q % (32 * S::JG);
+          if (c < cols && m0 + 32 * i + row < m_end)
+            reinterpret_cast<T*>(base + (int64_t)row * a.ldc * S::ES)[c] =
+                *reinterpret_cast<const T*>(slab + row * S::ROWP + c * S::ES);
+        }
       }
     }
   }
@@ -421,8 +476,16 @@ __device__ __forceinline__ void store_tile(const I8Args& a, const v16i (&acc)[IB
 // next step's loads, meets the others, refills the slot with the step STAGES
 // ahead and reads the next step's first fragments.
 // ---------------------------------------------------------------------------
+template <int BM, int BN, int BK, int STAGES>
+struct TileLds {
+  static constexpr int SLOT = (BM + BN) * BK;
+  static constexpr int AI = (BM + 63) / 64, BI = BN / 64;   // 64-value images of the row and the column scales
+  static constexpr int BYTES = STAGES * SLOT + (AI + 2 * BI) * 256;
+  static constexpr int PER_CU = 160 * 1024 / BYTES;
+};
+
 template <int BM, int BN, int WAVES_M, int WAVES_N, int BK, int STAGES, int SPREAD, int GRP>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 72 * 1024 ? 2 : 1) void k_i8_tile(I8Args a) {
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, BK, STAGES>::PER_CU > 1 ? 2 : 1)) void k_i8_tile(I8Args a) {
   constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, IB = WM / 32, JB = WN / 32;
   constexpr int CH = BK / 16, RI = 64 / CH, SL = BK / 32;           // chunks per row, rows per load image, slices
@@ -432,10 +495,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
   static_assert(BM * CH % NT == 0 && BN * CH % NT == 0, "whole load images per wave");
   static_assert((NW * RI) % 16 == 0, "a lane's chunk is the same in all its images");
   static_assert((STAGES - 1) * LPS < 64, "vmcnt counts at most 63 outstanding loads");
-  __shared__ __attribute__((aligned(16))) uint8_t smem[STAGES * SLOT + (BM + 2 * BN) * 4];
-  float* const as_t = reinterpret_cast<float*>(smem + STAGES * SLOT);  // row scales, column scales, bias
-  float* const bs_t = as_t + BM;
-  float* const bi_t = bs_t + BN;
+  typedef TileLds<BM, BN, BK, STAGES> L;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[L::BYTES];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -460,15 +521,14 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
   n0 = __builtin_amdgcn_readfirstlane(n0);
   m_end = __builtin_amdgcn_readfirstlane(m_end);
   e = __builtin_amdgcn_readfirstlane(e);
-  const uint8_t* Bt = a.B + (int64_t)e * a.N * a.ldb + (int64_t)n0 * a.ldb;
   // The resources end with the last row that the tile may use: lanes of rows
   // past it read zeros and touch no memory (their outputs are never stored).
-  auto bytes_to = [](int64_t rows, int64_t ld, int K) {
-    const int64_t b = (rows - 1) * ld + K;
+  auto upto = [](int64_t rows, int64_t ld, int64_t len) {
+    const int64_t b = (rows - 1) * ld + len;
     return (uint32_t)(b < UINT32_MAX ? b : UINT32_MAX);
   };
-  const buf_rsrc rA = make_rsrc_n(a.A + (int64_t)m0 * a.lda, bytes_to(m_end - m0, a.lda, a.K));
-  const buf_rsrc rB = make_rsrc_n(Bt, bytes_to(a.N - n0, a.ldb, a.K));
+  const buf_rsrc rA = make_rsrc_n(a.A + (int64_t)m0 * a.lda, upto(m_end - m0, a.lda, a.K));
+  const buf_rsrc rB = make_rsrc_n(a.B + ((int64_t)e * a.N + n0) * a.ldb, upto(a.N - n0, a.ldb, a.K));
   const int nk = (a.K + BK - 1) / BK;
 
   // Load image q (q = i*NW + wave) fills RI LDS rows of a tile; lane l writes
@@ -497,7 +557,12 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
     if (i < AP) lds_dma16(rA, aoff[i < AP ? i : 0] - sub, k * BK, base + 1024 * (i * NW + wave));
     else lds_dma16(rB, boff[i < AP ? 0 : i - AP] - sub, k * BK, base + A_BYTES + 1024 * ((i - AP) * NW + wave));
   };
-
+  // A step's refill is spread over SPREAD slices, the last one of the step
+  // that frees the slot and the first ones of the step after it: load q goes
+  // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
+  // belong to the first part.
+  constexpr int NM = IB * JB;
+  constexpr int LPS0 = (LPS + SPREAD - 1) / SPREAD;
   // Slice s of row block b: this lane's 16 bytes.
   const int frow = lane & 31, fh = lane >> 5, fsw = swz(frow);
   auto frag = [&](int slot, int off, int row0, int s) {
@@ -512,42 +577,28 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  // The scales, loaded ahead of the tiles and put into LDS behind them.
-  constexpr int SA = (BM + NT - 1) / NT, SB = (BN + NT - 1) / NT;
-  float sa[SA], sb[SB], si[SB];
+  // The scales go straight to LDS too, 64 values per load and as many loads in
+  // every wave (the last ones repeat the last image; without a bias its images
+  // hold column scales that no one reads).
+  {
+    constexpr int IMAGES = L::AI + 2 * L::BI;
+    const float* b_s = a.b_s + (int64_t)e * a.N + n0;
+    const buf_rsrc ra = make_rsrc_n(a.a_s + m0, upto(m_end - m0, 4, 4)), rb = make_rsrc_n(b_s, upto(a.N - n0, 4, 4));
+    const buf_rsrc ri = make_rsrc_n(a.bias ? a.bias + n0 : b_s, upto(a.N - n0, 4, 4));
 #pragma unroll
-  for (int i = 0; i < SA; ++i) {
-    const int m = m0 + i * NT + tid;
-    sa[i] = a.a_s[m < m_end ? m : m_end - 1];
+    for (int i = 0; i < (IMAGES + NW - 1) / NW; ++i) {
+      const int q = i * NW + wave < IMAGES ? i * NW + wave : IMAGES - 1;
+      const int first = q < L::AI ? 0 : q < L::AI + L::BI ? L::AI : L::AI + L::BI;
+      lds_dma4(q < L::AI ? ra : q < L::AI + L::BI ? rb : ri, 256u * (uint32_t)(q - first) + 4u * (uint32_t)lane, 0,
+               lds + STAGES * SLOT + 256 * q);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < SB; ++i) {
-    const int n = n0 + i * NT + tid < a.N ? n0 + i * NT + tid : a.N - 1;
-    sb[i] = a.b_s[(int64_t)e * a.N + n];
-    si[i] = a.bias ? a.bias[n] : 0.0f;
-  }
-
-  // A step's refill is spread over SPREAD slices, the last one of the step
-  // that frees the slot and the first ones of the step after it: load q goes
-  // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
-  // belong to the first part.
-  constexpr int NM = IB * JB;
-  constexpr int LPS0 = (LPS + SPREAD - 1) / SPREAD;
 #pragma unroll
   for (int p = 0; p < STAGES; ++p)
     if (p < nk) {
       const uint32_t sub = p == nk - 1 ? tail : 0u;
 #pragma unroll
       for (int i = 0; i < (p < STAGES - 1 ? LPS : LPS0); ++i) load_one(p, p, i, sub);
-    }
-#pragma unroll
-  for (int i = 0; i < SA; ++i)
-    if (i * NT + tid < BM) as_t[i * NT + tid] = sa[i];
-#pragma unroll
-  for (int i = 0; i < SB; ++i)
-    if (i * NT + tid < BN) {
-      bs_t[i * NT + tid] = sb[i];
-      bi_t[i * NT + tid] = si[i];
     }
   if (nk >= STAGES) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS + LPS0));
   else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
@@ -635,16 +686,24 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, STAGES * (BM + BN) * BK <= 
     }
   }
   step(k, slot, no, no, no);
-  __syncthreads();
-  const float *as_w = as_t + wm * WM, *bs_w = bs_t + wn * WN, *bi_w = bi_t + wn * WN;
-  const int mw = m0 + wm * WM, nw = n0 + wn * WN;
-  constexpr int SLAB2 = 32 * (32 * JB * 2 + 16), SLAB4 = 32 * (32 * JB * 4 + 16);  // 2- and 4-byte outputs
-  static_assert(NW * SLAB4 <= STAGES * SLOT, "the slabs fit in the ring");
-  switch (a.out) {
-    case kOutBF16: store_tile<kOutBF16, IB, JB>(a, acc, smem + wave * SLAB2, as_w, bs_w, bi_w, lane, mw, m_end, nw); break;
-    case kOutFP16: store_tile<kOutFP16, IB, JB>(a, acc, smem + wave * SLAB2, as_w, bs_w, bi_w, lane, mw, m_end, nw); break;
-    default: store_tile<kOutFP32, IB, JB>(a, acc, smem + wave * SLAB4, as_w, bs_w, bi_w, lane, mw, m_end, nw); break;
-  }
+  lds_barrier();  // the ring is free: the slabs take its place
+  hold_sums(acc);
+  const float* as_w = reinterpret_cast<const float*>(smem + STAGES * SLOT) + wm * WM;
+  const float* bs_w = reinterpret_cast<const float*>(smem + STAGES * SLOT) + 64 * L::AI + wn * WN;
+  const float* bi_w = bs_w + BN;
+  auto store = [&](auto out, auto bias) {
+    typedef Slab<decltype(out)::value, JB> S;
+    static_assert(NW * S::BYTES <= STAGES * SLOT, "room for the slabs");
+    store_tile<decltype(out)::value, decltype(bias)::value, IB, JB>(a, acc, smem + wave * S::BYTES, as_w, bs_w, bi_w, lane,
+                                                                    m0 + wm * WM, m_end, n0 + wn * WN);
+  };
+  auto store_as = [&](auto out) {
+    if (a.bias) store(out, yes);
+    else store(out, no);
+  };
+  if (a.out == kOutBF16) store_as(std::integral_constant<int, kOutBF16>{});
+  else if (a.out == kOutFP16) store_as(std::integral_constant<int, kOutFP16>{});
+  else store_as(std::integral_constant<int, kOutFP32>{});
 }
 
 // Whether every row of A and B starts on a 16-byte boundary and holds whole
@@ -677,7 +736,7 @@ __global__ __launch_bounds__(256) void k_i8_short(I8Args a) {
   const int8_t* w = reinterpret_cast<const int8_t*>(a.B) + ((int64_t)lo * a.N + n) * a.ldb;
   int sum = 0;
   for (int k = 0; k < a.K; ++k) sum += (int)x[k] * (int)w[k];
-  float c = (a.a_s[m] * a.b_s[(int64_t)lo * a.N + n]) * (float)sum;
+  float c = rounded((a.a_s[m] * a.b_s[(int64_t)lo * a.N + n]) * (float)sum);
   if (a.bias) c = c + a.bias[n];
   store1<OUT>(a.C, m * a.ldc + n, c);
 }
