@@ -387,6 +387,10 @@ namespace {
 // int32 sums of products of int8 codes, -128 included: 2^14 * K < 2^31.
 constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 1;
 
+// Largest row and column counts: the kernels round them up to a tile, or step
+// over them, in 32 bits.
+constexpr int64_t kMaxExtent = INT32_MAX - 1024;
+
 // Bytes from the first element of `rows` rows of `cols` elements, `ld` apart,
 // to the end of the last one; false if that overflows.
 bool extent(int64_t rows, int64_t cols, int64_t ld, int64_t size, int64_t* bytes) {
@@ -403,7 +407,7 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
               const float* bias, void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N,
               int64_t K, int out_dtype, bool grouped, void* stream) {
   if (E < 0 || M < 0 || N < 0 || K < 0 || !known_dtype(out_dtype)) return FBG_ERROR_INVALID_VALUE;
-  if (M > INT32_MAX || N > INT32_MAX || K > kMaxInt8K || E > INT32_MAX - 1) return FBG_ERROR_UNSUPPORTED;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxInt8K || E > kMaxExtent) return FBG_ERROR_UNSUPPORTED;
   const bool many_b = N > 1 || (grouped && E > 1);
   if ((M > 1 && lda < K) || (many_b && ldb < K) || (M > 1 && ldc < N)) return FBG_ERROR_INVALID_VALUE;
   if (M <= 1) lda = K, ldc = N;  // the pitch of a single row says nothing
@@ -448,7 +452,7 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
   if (st != FBG_SUCCESS) return st;
   const int force = forced_config();
   const hipError_t err = fbg::launch_i8(args, cus, force);
-  if (err == hipErrorInvalidValue && force >= 0) return FBG_ERROR_UNSUPPORTED;
+  if (err == hipErrorInvalidValue) return FBG_ERROR_UNSUPPORTED;  // a grid past 2^32 threads, or a forced configuration
   return err == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }
 
@@ -469,7 +473,7 @@ extern "C" int fbg_int8_grouped_gemm(const void* A, int64_t lda, const float* a_
 extern "C" int fbg_quantize_tokens(const void* x, int64_t ldx, int in_dtype, int64_t M, int64_t K, void* q,
                                    int64_t ldq, float* scale, void* stream) {
   if (M < 0 || K < 0 || !known_dtype(in_dtype)) return FBG_ERROR_INVALID_VALUE;
-  if (M > INT32_MAX || K > INT32_MAX) return FBG_ERROR_UNSUPPORTED;
+  if (M > kMaxExtent || K > kMaxExtent) return FBG_ERROR_UNSUPPORTED;
   if (M > 1 && (ldx < K || ldq < K)) return FBG_ERROR_INVALID_VALUE;
   if (M <= 1) ldx = K, ldq = K;
   const int64_t es = elem_size(in_dtype);
@@ -501,7 +505,7 @@ extern "C" int fbg_block_norm(const void* h, int64_t ldh, const void* x, int64_t
   if (M < 0 || D < 0 || gate_row < 0 || gate_col < 0 || !known_dtype(dtype) ||
       (weight_dtype != dtype && weight_dtype != FBG_OUT_FP32) || quantize < FBG_QUANT_NONE || quantize > FBG_QUANT_FP8)
     return FBG_ERROR_INVALID_VALUE;
-  if (M > INT32_MAX || D > INT32_MAX) return FBG_ERROR_UNSUPPORTED;
+  if (M > kMaxExtent || D > kMaxExtent) return FBG_ERROR_UNSUPPORTED;
   if (pre && quantize == FBG_QUANT_FP8 && D % 128 != 0) return FBG_ERROR_UNSUPPORTED;
   if (M > 1 && (ldh < D || (x && ldx < D) || ldr < D || (pre && ldy < D))) return FBG_ERROR_INVALID_VALUE;
   if (M <= 1) ldh = ldx = ldr = ldy = D;

@@ -712,13 +712,10 @@ inline bool fast_rows(const I8Args& a) {
   return ((uintptr_t)a.A | (uintptr_t)a.B | (uintptr_t)a.lda | (uintptr_t)a.ldb | (uintptr_t)a.K) % 16 == 0;
 }
 
-// K < 16: rows shorter than a chunk, one output per thread.  K == 0 is the
+// K < 16: rows shorter than a chunk, one output at a time.  K == 0 is the
 // empty sum: the column's bias, or zero, in every row (also of no expert).
 template <int OUT>
-__global__ __launch_bounds__(256) void k_i8_short(I8Args a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.M * a.N) return;
-  const int64_t m = i / a.N, n = i - m * a.N;
+__device__ __forceinline__ void short_output(const I8Args& a, int64_t m, int64_t n) {
   if (a.K == 0) {
     store1<OUT>(a.C, m * a.ldc + n, a.bias ? a.bias[n] : 0.0f);
     return;
@@ -739,6 +736,12 @@ __global__ __launch_bounds__(256) void k_i8_short(I8Args a) {
   float c = rounded((a.a_s[m] * a.b_s[(int64_t)lo * a.N + n]) * (float)sum);
   if (a.bias) c = c + a.bias[n];
   store1<OUT>(a.C, m * a.ldc + n, c);
+}
+
+template <int OUT>
+__global__ __launch_bounds__(256) void k_i8_short(I8Args a) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)a.M * a.N; i += (int64_t)gridDim.x * 256)
+    short_output<OUT>(a, i / a.N, i % a.N);
 }
 
 template <int BM, int BN, int AHEAD, int GRP>
@@ -786,9 +789,8 @@ hipError_t launch_SKINNY(const I8Args& a, unsigned grid) {
 hipError_t launch_i8(const I8Args& a, int cus, int force_cfg) {
   if (a.K < 16) {
     if (a.K > 0 && force_cfg >= 0) return hipErrorInvalidValue;
-    const int64_t grid = ((int64_t)a.M * a.N + 255) / 256;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 g((unsigned)grid), b(256);
+    const int64_t blocks = ((int64_t)a.M * a.N + 255) / 256;
+    const dim3 g((unsigned)(blocks < 65536 ? blocks : 65536)), b(256);
     switch (a.out) {
       case kOutBF16: hipLaunchKernelGGL(k_i8_short<kOutBF16>, g, b, 0, a.stream, a); break;
       case kOutFP16: hipLaunchKernelGGL(k_i8_short<kOutFP16>, g, b, 0, a.stream, a); break;
@@ -800,7 +802,7 @@ hipError_t launch_i8(const I8Args& a, int cus, int force_cfg) {
   const int cfg = force_cfg >= 0 ? force_cfg : int8_cfg_for(E, a.M, a.N, a.K, fast_rows(a), cus);
   if (cfg >= kNumI8Cfgs) return hipErrorInvalidValue;
   const int64_t grid = int8_grid(cfg, E, a.M, a.N);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid >= (int64_t)1 << 23) return hipErrorInvalidValue;  // of up to 512 threads: 2^32 in a launch
   switch (cfg) {
 #define X(id, kind, ...) \
   case id: return launch_##kind<__VA_ARGS__>(a, (unsigned)grid);

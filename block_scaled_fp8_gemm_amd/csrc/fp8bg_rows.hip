@@ -168,6 +168,14 @@ __device__ __forceinline__ void int8_codes(const float (&v)[VE], float s, float 
 // are 0 or NaN, so every code is 0.
 __device__ __forceinline__ bool finite(float s) { return abs_bits(s) < 0x7f800000u; }
 
+// A launch holds less than 2^32 threads along x: many rows take a grid of two
+// dimensions.
+constexpr int64_t kGridX = 1 << 20;
+inline dim3 row_grid(int64_t blocks) {
+  return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t block_of_grid() { return (int64_t)blockIdx.y * kGridX + blockIdx.x; }
+
 // A row is held by TPR threads: half a wave or one (eight or four rows to a
 // workgroup), or a workgroup of its own.
 constexpr int threads(int tpr) { return tpr <= 64 ? 256 : tpr; }
@@ -184,8 +192,8 @@ __global__ __launch_bounds__(threads(TPR)) void k_quantize_tokens(QuantArgs a) {
   constexpr int VE = Chunk<T>::VE;
   __shared__ uint32_t slots[waves(TPR)];
   const int t = threadIdx.x % TPR;
-  const int64_t m = (int64_t)blockIdx.x * rows_per_block(TPR) + threadIdx.x / TPR;
-  if (TPR <= 64 && m >= a.M) return;  // rows within a wave meet at no barrier
+  const int64_t m = block_of_grid() * rows_per_block(TPR) + threadIdx.x / TPR;
+  if (m >= a.M) return;  // a whole workgroup, or rows within a wave, which meet at no barrier
   const T* x = reinterpret_cast<const T*>(a.x) + m * a.ldx;
   Chunk<T> c[ITEMS];
 #pragma unroll
@@ -214,7 +222,8 @@ __global__ __launch_bounds__(threads(TPR)) void k_quantize_tokens(QuantArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_long(QuantArgs a) {
   __shared__ uint32_t slots[4];
-  const int64_t m = blockIdx.x;
+  const int64_t m = block_of_grid();
+  if (m >= a.M) return;
   const T* x = reinterpret_cast<const T*>(a.x) + m * a.ldx;
   int8_t* q = a.q + m * a.ldq;
   uint32_t amax = 0;
@@ -234,8 +243,8 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
   __shared__ float slots[2 * waves(TPR)];
   __shared__ uint32_t uslots[waves(TPR)];
   const int t = threadIdx.x % TPR;
-  const int64_t m = (int64_t)blockIdx.x * rows_per_block(TPR) + threadIdx.x / TPR;
-  if (TPR <= 64 && m >= a.M) return;
+  const int64_t m = block_of_grid() * rows_per_block(TPR) + threadIdx.x / TPR;
+  if (m >= a.M) return;
   const bool wf32 = a.wdtype == kOutFP32;
   const T* h = reinterpret_cast<const T*>(a.h) + m * a.ldh;
   const T* x = reinterpret_cast<const T*>(a.x) + m * a.ldx;
@@ -370,7 +379,8 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_block_norm_long(NormArgs a) {
   __shared__ float fslots[8];
   __shared__ uint32_t uslots[4];
-  const int64_t m = blockIdx.x;
+  const int64_t m = block_of_grid();
+  if (m >= a.M) return;
   const int tid = threadIdx.x;
   const bool wf32 = a.wdtype == kOutFP32;
   const void* h = reinterpret_cast<const T*>(a.h) + m * a.ldh;
@@ -477,12 +487,12 @@ hipError_t quantize(const QuantArgs& a) {
   const int64_t chunks = ((int64_t)a.K + Chunk<T>::VE - 1) / Chunk<T>::VE;
   const RowShape s = row_shape(a.M, chunks, chunks > 512);
   if (s.items == 0) {
-    hipLaunchKernelGGL(k_quantize_long<T>, dim3((unsigned)a.M), dim3(256), 0, a.stream, a);
+    hipLaunchKernelGGL(k_quantize_long<T>, row_grid(a.M), dim3(256), 0, a.stream, a);
     return hipGetLastError();
   }
   return with_shape(s.tpr, s.items, [&](auto tp, auto it) {
     constexpr int TPR = decltype(tp)::value, ITEMS = decltype(it)::value;
-    const dim3 g((unsigned)(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR))), b(threads(TPR));
+    const dim3 g = row_grid(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR)), b(threads(TPR));
     hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS>), g, b, 0, a.stream, a);
     return hipGetLastError();
   });
@@ -495,12 +505,12 @@ hipError_t norm(const NormArgs& a) {
   const int64_t chunks = ((int64_t)a.D + Chunk<T>::VE - 1) / Chunk<T>::VE;
   const RowShape s = row_shape(a.M, chunks, sizeof(T) == 2 && chunks > 512);
   if (s.items == 0) {
-    hipLaunchKernelGGL(k_block_norm_long<T>, dim3((unsigned)a.M), dim3(256), 0, a.stream, a);
+    hipLaunchKernelGGL(k_block_norm_long<T>, row_grid(a.M), dim3(256), 0, a.stream, a);
     return hipGetLastError();
   }
   return with_shape(s.tpr, s.items, [&](auto tp, auto it) {
     constexpr int TPR = decltype(tp)::value, ITEMS = decltype(it)::value;
-    const dim3 g((unsigned)(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR))), b(threads(TPR));
+    const dim3 g = row_grid(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR)), b(threads(TPR));
     hipLaunchKernelGGL((k_block_norm<T, TPR, ITEMS>), g, b, 0, a.stream, a);
     return hipGetLastError();
   });

@@ -282,8 +282,8 @@ int fp8_block_gemm_quantize_blocks(const void *w, int64_t N, int64_t K, void *B,
  * boundaries (base and pitch) take the faster loads.  a_s, b_s and bias 4-byte
  * aligned, C aligned to its element size.  M == 0 or N == 0: nothing launched;
  * K == 0: C is the bias, or zero.  K > 131071 (the int32 sum could overflow),
- * M or N above INT32_MAX, or a pitch above 2^24 - 128 for A or B ->
- * UNSUPPORTED; a pitch below the row's length, a null pointer with a
+ * M or N above INT32_MAX - 1024, a pitch above 2^24 - 128 for A or B, or more
+ * than 2^23 output tiles -> UNSUPPORTED; a pitch below the row's length, a null pointer with a
  * non-empty extent, an unknown out_dtype or C overlapping an input ->
  * INVALID_VALUE.
  */
@@ -329,8 +329,9 @@ int fbg_int8_plan(int64_t E, int64_t M, int64_t N, int64_t K, int aligned_rows, 
  * with correctly rounded fp32 divisions.  Makes A and a_s from activations,
  * and B and b_s from weights [N,K].  A row that holds a NaN or an infinity
  * gets a scale that is one, and code 0 where x / scale is NaN: the products of
- * that row are NaN.  x aligned to its element size, q at any byte, scale 4-byte aligned.
- * K == 0: every scale is 1e-12f / 127.
+ * that row are NaN.  x aligned to its element size, q at any byte, scale 4-byte
+ * aligned.  K == 0: every scale is 1e-12f / 127.  M or K above INT32_MAX - 1024 ->
+ * UNSUPPORTED.
  */
 int fbg_quantize_tokens(const void *x, int64_t ldx, int in_dtype, int64_t M, int64_t K, void *q, int64_t ldq,
                         float *scale, void *stream);

@@ -269,3 +269,25 @@ def test_forced_configuration_that_does_not_take_the_operands(gpu):
         with forced_config(cfg), pytest.raises(gpu.FP8BGError) as e:
             _gemm(gpu, d, "bf16")
         assert e.value.status == gpu.UNSUPPORTED
+
+
+def test_offsets_past_32_bits(gpu):
+    """C, A and B of more than 2^31 (and A's rows of 2^32) elements: the first
+    and last rows and columns, with pitches that put them that far apart."""
+    K, N, M, lda = 64, 24, 70000, 65536
+    A = torch.zeros(M * lda // 4 + 16, dtype=torch.int32, device=DEV).view(torch.int8)[:M * lda].view(M, lda)[:, :K]
+    d = T.make_gemm(64, N, K, seed=2)
+    rows = torch.cat([torch.arange(32), torch.arange(M - 32, M)]).to(DEV)
+    A[rows] = d["A"].to(DEV)
+    a_s = torch.ones(M, device=DEV)
+    a_s[rows] = d["a_s"].to(DEV)
+    C = gpu.int8_gemm(A, a_s, d["B"].to(DEV), d["b_s"].to(DEV), out_dtype=torch.float32)
+    T.assert_gemm(C[rows], d, "fp32", "A past 2^32 bytes")
+    del A, C
+    out = torch.empty(40000, 65536, device=DEV, dtype=torch.bfloat16)[:, :N]       # C past 2^31 elements
+    q = torch.zeros(40000, K, dtype=torch.int8, device=DEV)
+    q[-64:] = d["A"].to(DEV)
+    s = torch.ones(40000, device=DEV)
+    s[-64:] = d["a_s"].to(DEV)
+    C = gpu.int8_gemm(q, s, d["B"].to(DEV), d["b_s"].to(DEV), out=out)
+    T.assert_gemm(C[-64:], d, "bf16", "C past 2^31 elements")

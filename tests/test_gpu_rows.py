@@ -205,3 +205,17 @@ def test_norm_quantised_outputs_feed_the_products(gpu):
     w8 = w8 * a8.cpu().double().repeat_interleave(128, 0)[:200].repeat_interleave(128, 1)
     # 512 products and 4 folds in fp32.
     assert bool(((C8 - y8 @ w8.t()).abs() <= 600 * T.U32 * (y8.abs() @ w8.abs().t())).all())
+
+
+def test_more_rows_than_one_grid_dimension(gpu):
+    """Rows past 2^20 workgroups: the grid's second dimension."""
+    M, K = (1 << 23) + 5000, 32           # eight rows to a workgroup
+    x = torch.randn(M, K, device=DEV, dtype=torch.bfloat16)
+    q, s = gpu.quantize_tokens(x)
+    r, y = gpu.block_norm(x, pre_weight=torch.ones(K, device=DEV, dtype=torch.bfloat16))
+    for lo in (0, (1 << 23) - 7, M - 20):
+        wq, ws = T.quantize(x[lo:lo + 20].cpu())
+        assert torch.equal(q[lo:lo + 20].cpu(), wq) and torch.equal(s[lo:lo + 20].cpu(), ws)
+        assert torch.equal(r[lo:lo + 20], x[lo:lo + 20])
+        _, ref, _, tol = T.block_norm(x[lo:lo + 20].cpu(), None, None, None, torch.ones(K, dtype=torch.bfloat16), 1.0, 1e-6, 0.0)
+        T.assert_close(y[lo:lo + 20], ref, tol, "bf16")

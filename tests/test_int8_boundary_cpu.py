@@ -50,6 +50,8 @@ def test_gemm_refusals():
         assert _gemm(**kw) == bad, kw
     assert _gemm(K=131072, lda=131072, ldb=131072) == unsup          # the int32 sum could overflow
     assert _gemm(M=1 << 31) == unsup and _gemm(N=1 << 31, ldc=1 << 31) == unsup
+    assert _gemm(M=(1 << 31) - 1000) == unsup                        # rounding up to a tile would pass 32 bits
+    assert _quant(M=(1 << 31) - 1) == unsup and _norm(D=(1 << 31) - 1, ldh=1 << 31, ldx=1 << 31, ldr=1 << 31, ldy=1 << 31) == unsup
     assert _gemm(lda=1 << 24) == unsup and _gemm(ldb=1 << 24) == unsup
     assert _gemm(a_s=2 * P + 2) == unsup and _gemm(b_s=4 * P + 1) == unsup and _gemm(bias=8 * P + 3) == unsup
     assert _gemm(C=5 * P + 1) == unsup and _gemm(C=5 * P + 2, out=2) == unsup
