@@ -353,6 +353,187 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 
+// ---------------------------------------------------------------------------
+// The slim kernel, between the skinny one and the tiles: small tiles, so that
+// a few dozen rows still give every compute unit its share of the weights to
+// stream, whose four waves split K: of every 128-byte step in the ring, wave
+// w multiplies slice w for the whole BM x BN.  In the tile kernel a wave of
+// such a tile has one or two MFMAs between an LDS read and the next that waits
+// for it, and a step takes that latency four times; here it takes it once, and
+// a round of U steps shares one barrier.  The four sums meet in LDS.
+//
+// Rows and loads as in the tile kernel.  A round's fragments are multiplied
+// while the next one's are read; the refill of a slot goes out behind those
+// reads, past the barrier of the round after it.
+//
+// 64 x 4096 x 4096: 6.4 us, where the tile kernel's 32 x 64 takes 10.1 and the
+// skinny kernel 14.7; 17 x 4096 x 4096 6.2 (9.3).  One round per step instead
+// of two steps 7.4; the refill ahead of the reads 9.1.  Grouped, the weights
+// take the non-temporal hint, one expert's being read by one row of tiles: 64
+// tokens over 256 experts of 512 x 4096 88.8 -> 79.2 us; dense, where the row
+// tiles share them, it costs (64 x 4096 x 4096 7.8 us).
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int U, int STAGES>
+struct SlimLds {
+  static constexpr int STEP = (BM + BN) * 128, RING = STAGES * U * STEP;
+  static constexpr int PITCH = BN * 4 + 16, SUMS = 4 * BM * PITCH;  // each wave's sums, rows padded by 16 bytes
+  static constexpr int BYTES = RING > SUMS ? RING : SUMS;
+};
+
+template <int BM, int BN, int U, int STAGES, int GRP>
+__global__ __launch_bounds__(256, 2) void k_i8_slim(I8Args a) {
+  typedef SlimLds<BM, BN, U, STAGES> L;
+  constexpr int IB = BM / 32, JB = BN / 32, SLOT = U * L::STEP;
+  constexpr int LPS = U * (IB + JB);  // loads per wave and round
+  static_assert((STAGES - 1) * LPS < 64 && STAGES >= 3, "vmcnt counts at most 63 outstanding loads");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[L::BYTES];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles_n = (a.N + BN - 1) / BN;
+  int m0, n0, m_end = a.M, e = 0;
+  {
+    const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+    if constexpr (GRP) {
+      if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(smem))) return;
+      n0 = (lid % tiles_n) * BN;
+    } else {  // the row tiles of a column are neighbours: they share its weights
+      const int tiles_m = (a.M + BM - 1) / BM;
+      n0 = lid / tiles_m * BN;
+      m0 = lid % tiles_m * BM;
+    }
+  }
+  m0 = __builtin_amdgcn_readfirstlane(m0);  // scalar registers, as the buffer resources have to be
+  n0 = __builtin_amdgcn_readfirstlane(n0);
+  m_end = __builtin_amdgcn_readfirstlane(m_end);
+  e = __builtin_amdgcn_readfirstlane(e);
+  auto upto = [](int64_t rows, int64_t ld, int64_t len) {
+    const int64_t b = (rows - 1) * ld + len;
+    return (uint32_t)(b < UINT32_MAX ? b : UINT32_MAX);
+  };
+  const buf_rsrc rA = make_rsrc_n(a.A + (int64_t)m0 * a.lda, upto(m_end - m0, a.lda, a.K));
+  const buf_rsrc rB = make_rsrc_n(a.B + ((int64_t)e * a.N + n0) * a.ldb, upto(a.N - n0, a.ldb, a.K));
+  const int nk = (a.K + 127) / 128, rounds = (nk + U - 1) / U;
+  // Image i*4 + wave of a tile: rows 32i + 8*wave .., this lane's row and chunk.
+  const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz_row(row);
+  const uint32_t tail = (nk - 1) * 128 + 16 * chunk >= a.K ? 16u * (uint32_t)chunk : 0u;  // as in the tile kernel
+  uint32_t aoff[IB], boff[JB];
+#pragma unroll
+  for (int i = 0; i < IB; ++i) aoff[i] = (uint32_t)(32 * i + row) * (uint32_t)a.lda + 16u * (uint32_t)chunk;
+#pragma unroll
+  for (int j = 0; j < JB; ++j) boff[j] = (uint32_t)(32 * j + row) * (uint32_t)a.ldb + 16u * (uint32_t)chunk;
+  lds_u8* const lds = (lds_u8*)smem;
+  // Round g: the steps g*U .. g*U + U-1 (past the last one, that one again).
+  auto load_round = [&](int g, int slot) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = g * U + u < nk ? g * U + u : nk - 1;
+      const uint32_t sub = k == nk - 1 ? tail : 0u;
+      lds_u8* base = lds + slot * SLOT + u * L::STEP + 1024 * wave;
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        if constexpr (GRP) lds_dma16_nt(rB, boff[j] - sub, k * 128, base + BM * 128 + 4096 * j);
+        else lds_dma16(rB, boff[j] - sub, k * 128, base + BM * 128 + 4096 * j);
+      }
+#pragma unroll
+      for (int i = 0; i < IB; ++i) lds_dma16(rA, aoff[i] - sub, k * 128, base + 4096 * i);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < STAGES - 1; ++p)
+    if (p < rounds) load_round(p, p);
+
+  const int r32 = lane & 31, h = lane >> 5;
+  const int off = 128 * r32 + 16 * ((2 * wave + h) ^ swz_row(r32));
+  v16i acc[IB][JB];
+#pragma unroll
+  for (int i = 0; i < IB; ++i)
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+  v4i fa[U][IB], fb[U][JB];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < IB; ++i) fa[u][i] = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < JB; ++j) fb[u][j] = v4i{0, 0, 0, 0};
+  }
+  auto multiply = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[u][j], fa[u][i], acc[i][j], 0, 0, 0);
+  };
+  int slot = 0;
+  for (int g = 0; g < rounds; ++g) {
+    // Round g has landed; g+1 .. g+STAGES-2 may still be on their way.
+    if (g + STAGES - 2 < rounds) __builtin_amdgcn_s_waitcnt(vmcnt_only((STAGES - 2) * LPS) & ~(15 << 8));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_only(0) & ~(15 << 8));
+    __builtin_amdgcn_s_barrier();  // and every wave has read round g - 1: its slot is free
+    v4i na[U][IB], nb[U][JB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* base = smem + slot * SLOT + u * L::STEP + off;
+#pragma unroll
+      for (int i = 0; i < IB; ++i) na[u][i] = *reinterpret_cast<const v4i*>(base + 4096 * i);
+#pragma unroll
+      for (int j = 0; j < JB; ++j) nb[u][j] = *reinterpret_cast<const v4i*>(base + BM * 128 + 4096 * j);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (g + STAGES - 1 < rounds) load_round(g + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+    multiply();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < IB; ++i) fa[u][i] = na[u][i];
+#pragma unroll
+      for (int j = 0; j < JB; ++j) fb[u][j] = nb[u][j];
+    }
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool in = ((rounds - 1) * U + u) * 128 + 16 * (2 * wave + h) < a.K;
+#pragma unroll
+    for (int i = 0; i < IB; ++i) fa[u][i] = in ? fa[u][i] : v4i{0, 0, 0, 0};
+  }
+  multiply();
+  lds_barrier();  // the ring is free: the waves' sums take its place, rows of BN words
+#pragma unroll
+  for (int i = 0; i < IB; ++i)
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<v4i*>(smem + (wave * BM + 32 * i + r32) * L::PITCH + 4 * (32 * j + 8 * q + 4 * h)) =
+            v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+  lds_barrier();
+  // Four columns per thread, neighbouring threads on neighbouring columns.
+  const float* b_s = a.b_s + (int64_t)e * a.N;
+#pragma unroll
+  for (int t = 0; t < BM * BN / 1024; ++t) {
+    const int q = t * 256 + tid, mr = q / (BN / 4), nc = 4 * (q % (BN / 4));
+    const uint8_t* s0 = smem + mr * L::PITCH + 4 * nc;
+    v4i s = *reinterpret_cast<const v4i*>(s0);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) s += *reinterpret_cast<const v4i*>(s0 + w * BM * L::PITCH);
+    const int m = m0 + mr, n = n0 + nc, cnt = a.N - n < 4 ? a.N - n : 4;
+    if (m < m_end && cnt > 0) {
+      const v4f c = scale4(s, a.a_s[m], b_s, a.bias, n, a.N);
+      const int64_t at = (int64_t)m * a.ldc + n;
+      switch (a.out) {
+        case kOutBF16: store4<kOutBF16>(a.C, at, c, cnt, a.vec & 1); break;
+        case kOutFP16: store4<kOutFP16>(a.C, at, c, cnt, a.vec & 1); break;
+        default: store4<kOutFP32>(a.C, at, c, cnt, a.vec & 1); break;
+      }
+    }
+  }
+}
+
 // Scales a wave's IB x JB blocks of 32 x 32 sums and stores them.  Block
 // (i, j), element 4q + r of lane l: row m = 32i + (l & 31), column
 // n = 32j + 8q + 4(l >> 5) + r.  32 rows of up to 128 bytes at a time go
@@ -770,13 +951,26 @@ hipError_t launch_TILE(const I8Args& a, unsigned grid) {
   return hipGetLastError();
 }
 
-template <int ROWS, int COLS, int KW, int U>
+template <int BM, int BN, int U, int STAGES>
+hipError_t launch_SLIM(const I8Args& a, unsigned grid) {
+  if (!fast_rows(a)) return hipErrorInvalidValue;
+  if (a.offsets) hipLaunchKernelGGL((k_i8_slim<BM, BN, U, STAGES, 1>), dim3(grid), dim3(256), 0, a.stream, a);
+  else hipLaunchKernelGGL((k_i8_slim<BM, BN, U, STAGES, 0>), dim3(grid), dim3(256), 0, a.stream, a);
+  return hipGetLastError();
+}
+
+template <int ROWS, int COLS, int KW, int U, bool FORM>
 hipError_t launch_SKINNY(const I8Args& a, unsigned grid) {
   constexpr int NB = COLS / 16;
   const dim3 g(grid), b(64 * KW);
-  if (fast_rows(a)) {
-    if (a.offsets) hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 1>), g, b, 0, a.stream, a);
-    else hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 0>), g, b, 0, a.stream, a);
+  if constexpr (FORM) {
+    if (fast_rows(a)) {
+      if (a.offsets) hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 1>), g, b, 0, a.stream, a);
+      else hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, true, 0>), g, b, 0, a.stream, a);
+      return hipGetLastError();
+    }
+    if (a.offsets) return hipErrorInvalidValue;  // experts of such rows take the 32-column form
+    hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, false, 0>), g, b, 0, a.stream, a);
   } else {
     if (a.offsets) hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, false, 1>), g, b, 0, a.stream, a);
     else hipLaunchKernelGGL((k_i8_skinny<NB, ROWS, KW, U, false, 0>), g, b, 0, a.stream, a);

@@ -8,18 +8,18 @@ namespace fbg {
 
 namespace {
 
-enum Kind { ANY, SKINNY, TILE };
+enum Kind { ANY, SKINNY, SLIM, TILE };
 
 // What a configuration costs, in microseconds: `start` once per workgroup and
 // `step` per 128 bytes of K, rising from `step` for one workgroup alone to
 // `full` with `per_cu` on every compute unit; past that the rounds queue up,
 // and `again` is the share of `start` that a queued round still shows.
 // Least-squares fits in the logarithm to 167 dense shapes of M 1 .. 16384, N
-// 64 .. 8192 and K 256, 1024 and 4096 (configurations 2-10, 16-byte rows; the
-// fits' own deviation is 4-10%) and to 79 of the same range with odd K (any
+// 64 .. 8192 and K 256, 1024 and 4096 (configurations 2-12, 16-byte rows; the
+// fits' own deviation is 4-11%) and to 79 of the same range with odd K (any
 // rows; 9-22%), `per_cu` being the count that fits best, not an occupancy.
-// Choosing by it costs 1.9% over the best configuration of each shape on
-// average (any rows: 1.8%), 20% at worst.
+// Choosing by it costs 0.9% over the best configuration of each shape on
+// average and 11% at worst (any rows: 1.8% and 18%).
 struct Cost {
   Kind kind;
   int rows, cols, per_cu, waves;
@@ -28,15 +28,17 @@ struct Cost {
 constexpr Cost kFast[kNumI8Cfgs] = {
     {ANY, 64, 64, 4, 4, 0, 0, 0, 0},
     {ANY, 32, 64, 4, 4, 0, 0, 0, 0},
-    {SKINNY, 8, 16, 8, 8, 2.380f, 0.073f, 0.745f, 0.643f},
-    {SKINNY, 16, 16, 8, 8, 2.341f, 0.084f, 0.910f, 0.661f},
-    {SKINNY, 16, 32, 8, 4, 2.309f, 0.148f, 1.378f, 0.975f},
-    {TILE, 32, 64, 3, 2, 2.700f, 0.218f, 0.455f, 0.751f},
+    {SKINNY, 8, 16, 8, 8, 2.400f, 0.072f, 0.747f, 0.590f},
+    {SKINNY, 16, 16, 8, 8, 2.385f, 0.084f, 0.904f, 0.652f},
+    {SKINNY, 16, 32, 8, 4, 2.351f, 0.146f, 1.365f, 0.969f},
+    {TILE, 32, 64, 3, 2, 2.614f, 0.213f, 0.437f, 0.737f},
     {TILE, 64, 64, 2, 4, 2.828f, 0.238f, 0.447f, 0.667f},
     {TILE, 64, 128, 2, 4, 3.343f, 0.280f, 0.697f, 0.841f},
     {TILE, 128, 128, 2, 4, 3.959f, 0.511f, 1.221f, 0.968f},
     {TILE, 128, 256, 1, 4, 7.084f, 0.546f, 0.968f, 0.925f},
     {TILE, 256, 256, 1, 4, 11.821f, 0.976f, 1.581f, 0.975f},
+    {SLIM, 32, 32, 2, 4, 2.504f, 0.091f, 0.226f, 0.727f},
+    {SLIM, 32, 32, 3, 4, 2.521f, 0.130f, 0.331f, 0.857f},
 };
 constexpr Cost kAny[kI8FirstTile] = {
     {ANY, 64, 64, 2, 4, 4.149f, 0.391f, 0.922f, 0.983f},
@@ -64,17 +66,18 @@ int int8_cfg_for(int64_t E, int64_t M, int64_t N, int64_t K, bool fast, int cus)
   const double mean = E > 0 ? (double)M / (double)E : 0.0;
   if (E > 0 && mean <= 12.0) {
     // Small experts: the weights of those that hold rows are what is read.
-    // 16-byte rows: over a long K the skinny kernel streams them best (64
-    // tokens, 8 of 256 experts of 512 x 4096: 83 us in 32-column workgroups of
-    // 4 waves, 5.5 TB/s; 32 x 64 tile 97; 8 rows to a expert on average: 105
-    // against 110), in 16 columns while that makes at most two workgroups per
-    // compute unit (8 experts: 5.6 us, 32 columns 7.5, the tile 10.5); over a
-    // short K the tile does (of 1536 x 1024: 64 us, skinny 71).  Any rows: the
+    // 16-byte rows: over a long K the slim kernel streams them best (64 tokens,
+    // 8 of 256 experts of 512 x 4096: 79 us, 5.8 TB/s, skinny 83, 32 x 64 tile
+    // 97; 8 rows to an expert on average 88 us, 105 and 110), and the skinny one
+    // while that makes at most two workgroups per compute unit (8 experts of
+    // 1-8 rows: 5.0-5.6 us, slim 6.7, the tile 10.4); over a short K the tile
+    // does (of 1536 x 1024: 64 us, slim 79, skinny 71).  Any rows: the
     // 32-column skinny form up to a few workgroups per compute unit (64 rows
     // over 8 experts of 515 x 776: 4.0 us, the 32 x 64 tile 5.1), else the
     // 32 x 64 tile (256 experts: 27.7 us against 32.9).
-    if (fast) return K < 2048 ? 5 : E * ceil_div(N, 16) <= 2 * cus ? 3 : 4;
-    return E * ceil_div(N, 32) <= 4 * cus ? 4 : 1;
+    if (!fast) return E * ceil_div(N, 32) <= 4 * cus ? 4 : 1;
+    if (K < 2048) return 5;
+    return E * ceil_div(N, 16) > 2 * cus || mean > 8.0 ? 12 : mean > 4.0 ? 3 : 2;
   }
   // A skinny workgroup walks an expert's rows one pass after the other.
   if (E > 0 && fast) first = kI8FirstTile;

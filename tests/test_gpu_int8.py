@@ -235,7 +235,7 @@ def test_graph_replays(gpu):
 # ---------------------------------------------------------------------------
 # Every kernel configuration, forced
 # ---------------------------------------------------------------------------
-CONFIGS = range(11)
+CONFIGS = range(13)
 
 
 @pytest.mark.parametrize("cfg", CONFIGS)

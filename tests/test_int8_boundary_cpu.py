@@ -112,7 +112,7 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
 
 
 def test_plan():
-    for M, N, K, want in [(1, 4096, 4096, (2, 3)), (64, 512, 4096, (2, 3)), (16384, 4096, 4096, (10,)), (128, 8192, 1024, (5, 6))]:
+    for M, N, K, want in [(1, 512, 1024, (2, 3)), (64, 4096, 4096, (11,)), (16384, 4096, 4096, (10,)), (128, 8192, 1024, (5, 6))]:
         p = fbg.int8_plan(M, N, K)
         assert p["variant_name"] == "int8" and p["config"] in want, (M, N, K, p)
         assert p["grid"] == -(-M // p["tile_m"]) * -(-N // p["tile_n"])
@@ -124,8 +124,9 @@ def test_plan():
     # small experts: long K over few of them on the skinny kernel; the grouped
     # grid bounds the experts' row tiles by floor(M / rows) + E
     assert fbg.int8_plan(64, 512, 4096, E=8)["config"] == 3
+    assert fbg.int8_plan(8, 512, 4096, E=8)["config"] == 2
     p = fbg.int8_plan(512, 512, 4096, E=256)
-    assert p["config"] == 4 and p["grid"] == 256 * 16
+    assert p["config"] == 12 and p["grid"] == (512 // 32 + 256) * 16
     p = fbg.int8_plan(512, 512, 1024, E=256)
     assert p["config"] == 5 and p["grid"] == (512 // 32 + 256) * 8
     assert fbg.int8_plan(32768, 512, 4096, E=256)["config"] >= 7
@@ -146,4 +147,5 @@ def test_every_configuration_is_chosen_for_some_shape():
             for N in (64, 512, 1536, 4096, 8192):
                 for K in (256, 1024, 4096):
                     seen.add(fbg.int8_plan(M, N, K, aligned_rows=aligned)["config"])
-    assert seen == set(range(11)), seen
+                    seen.add(fbg.int8_plan(M, N, K, E=64, aligned_rows=aligned)["config"])
+    assert seen == set(range(13)), seen
