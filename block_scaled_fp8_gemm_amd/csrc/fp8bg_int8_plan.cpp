@@ -79,6 +79,12 @@ int int8_cfg_for(int64_t E, int64_t M, int64_t N, int64_t K, bool fast, int cus)
     if (K < 2048) return 5;
     return E * ceil_div(N, 16) > 2 * cus || mean > 8.0 ? 12 : mean > 4.0 ? 3 : 2;
   }
+  // Up to four rows: the skinny tile's other rows repeat them, so that it reads
+  // less than the fit, made over full tiles, supposes.  With at most one such
+  // workgroup per compute unit it is the fastest (1 x 4096 x 4096 5.5 us, slim
+  // 6.0; 1 x 1536 x 4096 4.9 and 5.8; 4 x 4096 x 4096 5.9 and 6.0; 8 rows 6.2
+  // and 6.0; past that 1 x 8192 x 4096 8.6 and 8.1).
+  if (E == 0 && fast && M <= 4 && ceil_div(N, 16) <= cus) return 2;
   // A skinny workgroup walks an expert's rows one pass after the other.
   if (E > 0 && fast) first = kI8FirstTile;
   if (E > 0 && !fast) end = kI8FirstSkinny;
