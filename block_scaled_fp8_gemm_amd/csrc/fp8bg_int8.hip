@@ -41,24 +41,35 @@ __device__ __forceinline__ v4i mfma_i8(const v4i& x, const v4i& y, const v4i& ac
 // last tile exit.  There are floor(M / BM) + E slots.
 // Returns whether slot `t` holds rows; all threads of the workgroup call it.
 // `found`: three words of LDS, free again afterwards.
+//
+// Malformed offsets never lead outside the operands: each is clamped, and
+// where several experts claim a slot the last of them has it alone (its rows
+// come from one thread).
 template <int BM>
 __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, int E, int M, int t, int& e_out,
                                                int& m0, int& m_end, int* found) {
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
+  int mine = -1, first = 0, last = 0;
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int lo = offsets[e], hi = offsets[e + 1];
-    lo = lo < 0 ? 0 : (lo > M ? M : lo);  // malformed offsets never lead outside the operands
+    lo = lo < 0 ? 0 : (lo > M ? M : lo);
     hi = hi < lo ? lo : (hi > M ? M : hi);
     const int i = t - (lo / BM + e);
     if (i >= 0 && (int64_t)i * BM < hi - lo) {
-      found[0] = e;
-      found[1] = lo + i * BM;
-      found[2] = hi;
+      mine = e;
+      first = lo + i * BM;
+      last = hi;
     }
   }
+  if (mine >= 0) atomicMax(&found[0], mine);
   __syncthreads();
   e_out = found[0];
+  if (mine >= 0 && mine == e_out) {
+    found[1] = first;
+    found[2] = last;
+  }
+  __syncthreads();
   m0 = found[1];
   m_end = found[2];
   __syncthreads();

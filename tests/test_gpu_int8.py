@@ -291,3 +291,23 @@ def test_offsets_past_32_bits(gpu):
     s[-64:] = d["a_s"].to(DEV)
     C = gpu.int8_gemm(q, s, d["B"].to(DEV), d["b_s"].to(DEV), out=out)
     T.assert_gemm(C[-64:], d, "bf16", "C past 2^31 elements")
+
+
+@pytest.mark.parametrize("cfg", [None, *CONFIGS])
+def test_arbitrary_offsets_stay_inside_the_operands(gpu, cfg):
+    """Offsets in no order at all: nothing outside C is written, and no value of
+    C is anything but some expert's product for its row (ranges that overlap
+    may each write a part of one) or what was there."""
+    E, M, N, K = 70, 300, 64, 64
+    r = np.random.default_rng(11)
+    d = T.make_gemm(M, N, K, seed=6, experts=E)
+    off = r.integers(-50, M + 50, E + 1)
+    guard = torch.full((M + 2, N), 9.0, device=DEV)
+    with forced_config(cfg):
+        C = _grouped(gpu, d, None, "fp32", offsets=off.tolist(), out=guard[1:M + 1])
+    assert bool((guard[0] == 9).all()) and bool((guard[-1] == 9).all())
+    C = C.cpu()
+    fine = C == 9
+    for e in range(E):
+        fine |= C == T.gemm_bits({"A": d["A"], "a_s": d["a_s"], "B": d["B"][e], "b_s": d["b_s"][e]}, "fp32")
+    assert bool(fine.all())
