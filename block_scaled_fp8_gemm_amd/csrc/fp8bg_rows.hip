@@ -113,11 +113,25 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int at, int n) {
   return c;
 }
 
-// VE values of type S (of any size) to row[at ..], those before n.
-template <typename S, int VE>
+// VE values of type S (of any size) to row[at ..], those before n.  STREAM: the
+// non-temporal hint (a template flag: of two stores that differ only in it the
+// compiler makes one without).
+template <bool STREAM, typename S, int VE>
 __device__ __forceinline__ void store_values(S* row, int at, int n, const S (&v)[VE]) {
+  typedef unsigned int U4 __attribute__((ext_vector_type(4), aligned(1)));
+  typedef unsigned int U2 __attribute__((ext_vector_type(2), aligned(1)));
   if (at + VE <= n) {
-    __builtin_memcpy(row + at, v, sizeof(v));
+    if constexpr (STREAM && sizeof(v) == 16) {
+      U4 w;
+      __builtin_memcpy(&w, v, 16);
+      __builtin_nontemporal_store(w, reinterpret_cast<U4*>(row + at));
+    } else if constexpr (STREAM && sizeof(v) == 8) {
+      U2 w;
+      __builtin_memcpy(&w, v, 8);
+      __builtin_nontemporal_store(w, reinterpret_cast<U2*>(row + at));
+    } else {
+      __builtin_memcpy(row + at, v, sizeof(v));
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < VE; ++i)
@@ -187,7 +201,7 @@ constexpr int rows_per_block(int tpr) { return threads(tpr) / tpr; }
 // chunks each, so x is read once; all loads are issued before the maximum is
 // taken.
 // ---------------------------------------------------------------------------
-template <typename T, int TPR, int ITEMS>
+template <typename T, int TPR, int ITEMS, bool STREAM>
 __global__ __launch_bounds__(threads(TPR)) void k_quantize_tokens(QuantArgs a) {
   constexpr int VE = Chunk<T>::VE;
   __shared__ uint32_t slots[waves(TPR)];
@@ -213,7 +227,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_quantize_tokens(QuantArgs a) {
 #pragma unroll
     for (int j = 0; j < VE; ++j) v[j] = (float)c[i].v[j];
     if (finite(s)) int8_codes<sizeof(T) == 4>(v, s, y, o);
-    store_values(q, (i * TPR + t) * VE, a.K, o);
+    store_values<STREAM>(q, (i * TPR + t) * VE, a.K, o);
   }
   if (t == 0) a.scale[m] = s;
 }
@@ -237,7 +251,7 @@ __global__ __launch_bounds__(256) void k_quantize_long(QuantArgs a) {
 // Norms.  As above a row of h, x and the gate is loaded into registers once,
 // and r stays there in fp32 between the two norms.
 // ---------------------------------------------------------------------------
-template <typename T, int TPR, int ITEMS>
+template <typename T, int TPR, int ITEMS, bool STREAM>
 __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
   constexpr int VE = Chunk<T>::VE;
   __shared__ float slots[2 * waves(TPR)];
@@ -307,7 +321,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
       o[j] = (T)r[i][j];
       if (at + j < a.D) ss = __builtin_fmaf(r[i][j], r[i][j], ss);
     }
-    store_values(ro, at, a.D, o);
+    store_values<STREAM>(ro, at, a.D, o);
   }
   if (!a.pre) return;
   const float rstd = 1.0f / __builtin_sqrtf(row_sum<TPR>(ss, slots + waves(TPR)) / (float)a.D + a.eps);
@@ -325,7 +339,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
       T o[VE];
 #pragma unroll
       for (int j = 0; j < VE; ++j) o[j] = (T)r[i][j];
-      store_values(yo, (i * TPR + t) * VE, a.D, o);
+      store_values<STREAM>(yo, (i * TPR + t) * VE, a.D, o);
     }
   } else if (a.quant == FBG_QUANT_INT8) {
     uint32_t amax = 0;
@@ -341,7 +355,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
     for (int i = 0; i < ITEMS; ++i) {
       int8_t o[VE] = {};
       if (finite(s)) int8_codes<false>(r[i], s, y, o);
-      store_values(yo, (i * TPR + t) * VE, a.D, o);
+      store_values<STREAM>(yo, (i * TPR + t) * VE, a.D, o);
     }
     if (t == 0) a.y_scale[m] = s;
   } else {  // E4M3: 128 / VE neighbouring threads hold a group of 128 columns (D % 128 == 0: whole groups)
@@ -367,7 +381,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
         o[j] = (uint8_t)(w & 255);
         o[j + 1] = (uint8_t)((w >> 8) & 255);
       }
-      store_values(yo, at, a.D, o);
+      store_values<STREAM>(yo, at, a.D, o);
       if (t % (128 / VE) == 0 && at < a.D) a.y_scale[m * (a.D / 128) + at / 128] = s;
     }
   }
@@ -466,7 +480,7 @@ hipError_t with_shape(int tpr, int items, const F& launch) {
 // over as many threads as it has chunks, since only latency counts (64 x 4096
 // bf16: norm 4.5 us with 1 chunk per thread, 5.1 with 2, 6.6 with 4).  With
 // many, more bytes in flight per wave win: 2 chunks (16384 x 4096 bf16: norm to
-// int8 111 us, against 144 with 1 and 119 with 4; quantiser 34.7 against 50
+// int8 111 us then, against 144 with 1 and 119 with 4; quantiser 34.7 against 50
 // and 34.2), and 4 in the long rows of `many` (2048 x 16384: norm 70 us against
 // 80 with 2, quantiser 19.7 against 20.9).  A row of at most 32 chunks takes
 // half a wave (16384 x 256: norm 13.2 us, 19.3 on a whole one).
@@ -482,10 +496,20 @@ inline RowShape row_shape(int64_t rows, int64_t chunks, bool many) {
   }
 }
 
+// Outputs of more than 8 MB go out with the non-temporal hint, the others
+// stay in the caches for the product that reads them next.  Alone, with the
+// hint and without: norm to int8 105 and 111 us at 16384 x 4096, 10.5 and
+// 12.1 at 1024 x 4096 (12 MB); quantiser 36 and 39 us, 11.1 and 12.7 at 16384 x
+// 1024.  In a chain of norm, product and quantiser, 4096 columns: 31.8 and 32.3 us
+// at 1024 rows, but 19.05 and 18.55 at 256 (3 MB), 17.0 and 16.1 at 64.
+constexpr int64_t kStreamBytes = (int64_t)8 << 20;
+inline bool stream_outputs(int64_t rows, int64_t bytes_per_row) { return rows * bytes_per_row > kStreamBytes; }
+
 template <typename T>
 hipError_t quantize(const QuantArgs& a) {
   const int64_t chunks = ((int64_t)a.K + Chunk<T>::VE - 1) / Chunk<T>::VE;
   const RowShape s = row_shape(a.M, chunks, chunks > 512);
+  const bool stream = stream_outputs(a.M, a.K);
   if (s.items == 0) {
     hipLaunchKernelGGL(k_quantize_long<T>, row_grid(a.M), dim3(256), 0, a.stream, a);
     return hipGetLastError();
@@ -493,7 +517,13 @@ hipError_t quantize(const QuantArgs& a) {
   return with_shape(s.tpr, s.items, [&](auto tp, auto it) {
     constexpr int TPR = decltype(tp)::value, ITEMS = decltype(it)::value;
     const dim3 g = row_grid(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR)), b(threads(TPR));
-    hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS>), g, b, 0, a.stream, a);
+    if constexpr (ITEMS > 1) {  // (rows of at most 32 chunks are left out: 512 bytes each)
+      if (stream) {
+        hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS, true>), g, b, 0, a.stream, a);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS, false>), g, b, 0, a.stream, a);
     return hipGetLastError();
   });
 }
@@ -504,6 +534,8 @@ hipError_t norm(const NormArgs& a) {
   // stay at 2 (8192 columns: 238 us against 243).
   const int64_t chunks = ((int64_t)a.D + Chunk<T>::VE - 1) / Chunk<T>::VE;
   const RowShape s = row_shape(a.M, chunks, sizeof(T) == 2 && chunks > 512);
+  const int y_size = !a.pre ? 0 : a.quant == FBG_QUANT_NONE ? (int)sizeof(T) : 1;
+  const bool stream = stream_outputs(a.M, a.D * (int64_t)(sizeof(T) + y_size));
   if (s.items == 0) {
     hipLaunchKernelGGL(k_block_norm_long<T>, row_grid(a.M), dim3(256), 0, a.stream, a);
     return hipGetLastError();
@@ -511,7 +543,13 @@ hipError_t norm(const NormArgs& a) {
   return with_shape(s.tpr, s.items, [&](auto tp, auto it) {
     constexpr int TPR = decltype(tp)::value, ITEMS = decltype(it)::value;
     const dim3 g = row_grid(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR)), b(threads(TPR));
-    hipLaunchKernelGGL((k_block_norm<T, TPR, ITEMS>), g, b, 0, a.stream, a);
+    if constexpr (ITEMS > 1) {  // (rows of at most 32 chunks are left out: 512 bytes each)
+      if (stream) {
+        hipLaunchKernelGGL((k_block_norm<T, TPR, ITEMS, true>), g, b, 0, a.stream, a);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((k_block_norm<T, TPR, ITEMS, false>), g, b, 0, a.stream, a);
     return hipGetLastError();
   });
 }
