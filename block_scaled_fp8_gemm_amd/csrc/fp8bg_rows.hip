@@ -114,21 +114,17 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int at, int n) {
 }
 
 // VE values of type S (of any size) to row[at ..], those before n.  STREAM: the
-// non-temporal hint (a template flag: of two stores that differ only in it the
-// compiler makes one without).
-template <bool STREAM, typename S, int VE>
+// non-temporal hint, for 16-byte chunks (a template flag: of two stores that
+// differ only in it the compiler makes one without).
+template <bool STREAM = false, typename S, int VE>
 __device__ __forceinline__ void store_values(S* row, int at, int n, const S (&v)[VE]) {
-  typedef unsigned int U4 __attribute__((ext_vector_type(4), aligned(1)));
-  typedef unsigned int U2 __attribute__((ext_vector_type(2), aligned(1)));
   if (at + VE <= n) {
-    if constexpr (STREAM && sizeof(v) == 16) {
+    if constexpr (STREAM) {
+      static_assert(sizeof(v) == 16, "a chunk");
+      typedef unsigned int U4 __attribute__((ext_vector_type(4), aligned(2)));
       U4 w;
       __builtin_memcpy(&w, v, 16);
       __builtin_nontemporal_store(w, reinterpret_cast<U4*>(row + at));
-    } else if constexpr (STREAM && sizeof(v) == 8) {
-      U2 w;
-      __builtin_memcpy(&w, v, 8);
-      __builtin_nontemporal_store(w, reinterpret_cast<U2*>(row + at));
     } else {
       __builtin_memcpy(row + at, v, sizeof(v));
     }
@@ -201,7 +197,7 @@ constexpr int rows_per_block(int tpr) { return threads(tpr) / tpr; }
 // chunks each, so x is read once; all loads are issued before the maximum is
 // taken.
 // ---------------------------------------------------------------------------
-template <typename T, int TPR, int ITEMS, bool STREAM>
+template <typename T, int TPR, int ITEMS>
 __global__ __launch_bounds__(threads(TPR)) void k_quantize_tokens(QuantArgs a) {
   constexpr int VE = Chunk<T>::VE;
   __shared__ uint32_t slots[waves(TPR)];
@@ -227,7 +223,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_quantize_tokens(QuantArgs a) {
 #pragma unroll
     for (int j = 0; j < VE; ++j) v[j] = (float)c[i].v[j];
     if (finite(s)) int8_codes<sizeof(T) == 4>(v, s, y, o);
-    store_values<STREAM>(q, (i * TPR + t) * VE, a.K, o);
+    store_values(q, (i * TPR + t) * VE, a.K, o);
   }
   if (t == 0) a.scale[m] = s;
 }
@@ -339,7 +335,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
       T o[VE];
 #pragma unroll
       for (int j = 0; j < VE; ++j) o[j] = (T)r[i][j];
-      store_values<STREAM>(yo, (i * TPR + t) * VE, a.D, o);
+      store_values(yo, (i * TPR + t) * VE, a.D, o);
     }
   } else if (a.quant == FBG_QUANT_INT8) {
     uint32_t amax = 0;
@@ -355,7 +351,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
     for (int i = 0; i < ITEMS; ++i) {
       int8_t o[VE] = {};
       if (finite(s)) int8_codes<false>(r[i], s, y, o);
-      store_values<STREAM>(yo, (i * TPR + t) * VE, a.D, o);
+      store_values(yo, (i * TPR + t) * VE, a.D, o);
     }
     if (t == 0) a.y_scale[m] = s;
   } else {  // E4M3: 128 / VE neighbouring threads hold a group of 128 columns (D % 128 == 0: whole groups)
@@ -381,7 +377,7 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
         o[j] = (uint8_t)(w & 255);
         o[j + 1] = (uint8_t)((w >> 8) & 255);
       }
-      store_values<STREAM>(yo, at, a.D, o);
+      store_values(yo, at, a.D, o);
       if (t % (128 / VE) == 0 && at < a.D) a.y_scale[m * (a.D / 128) + at / 128] = s;
     }
   }
@@ -496,20 +492,10 @@ inline RowShape row_shape(int64_t rows, int64_t chunks, bool many) {
   }
 }
 
-// Outputs of more than 8 MB go out with the non-temporal hint, the others
-// stay in the caches for the product that reads them next.  Alone, with the
-// hint and without: norm to int8 105 and 111 us at 16384 x 4096, 10.5 and
-// 12.1 at 1024 x 4096 (12 MB); quantiser 36 and 39 us, 11.1 and 12.7 at 16384 x
-// 1024.  In a chain of norm, product and quantiser, 4096 columns: 31.8 and 32.3 us
-// at 1024 rows, but 19.05 and 18.55 at 256 (3 MB), 17.0 and 16.1 at 64.
-constexpr int64_t kStreamBytes = (int64_t)8 << 20;
-inline bool stream_outputs(int64_t rows, int64_t bytes_per_row) { return rows * bytes_per_row > kStreamBytes; }
-
 template <typename T>
 hipError_t quantize(const QuantArgs& a) {
   const int64_t chunks = ((int64_t)a.K + Chunk<T>::VE - 1) / Chunk<T>::VE;
   const RowShape s = row_shape(a.M, chunks, chunks > 512);
-  const bool stream = stream_outputs(a.M, a.K);
   if (s.items == 0) {
     hipLaunchKernelGGL(k_quantize_long<T>, row_grid(a.M), dim3(256), 0, a.stream, a);
     return hipGetLastError();
@@ -517,13 +503,7 @@ hipError_t quantize(const QuantArgs& a) {
   return with_shape(s.tpr, s.items, [&](auto tp, auto it) {
     constexpr int TPR = decltype(tp)::value, ITEMS = decltype(it)::value;
     const dim3 g = row_grid(((int64_t)a.M + rows_per_block(TPR) - 1) / rows_per_block(TPR)), b(threads(TPR));
-    if constexpr (ITEMS > 1) {  // (rows of at most 32 chunks are left out: 512 bytes each)
-      if (stream) {
-        hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS, true>), g, b, 0, a.stream, a);
-        return hipGetLastError();
-      }
-    }
-    hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS, false>), g, b, 0, a.stream, a);
+    hipLaunchKernelGGL((k_quantize_tokens<T, TPR, ITEMS>), g, b, 0, a.stream, a);
     return hipGetLastError();
   });
 }
@@ -534,8 +514,14 @@ hipError_t norm(const NormArgs& a) {
   // stay at 2 (8192 columns: 238 us against 243).
   const int64_t chunks = ((int64_t)a.D + Chunk<T>::VE - 1) / Chunk<T>::VE;
   const RowShape s = row_shape(a.M, chunks, sizeof(T) == 2 && chunks > 512);
-  const int y_size = !a.pre ? 0 : a.quant == FBG_QUANT_NONE ? (int)sizeof(T) : 1;
-  const bool stream = stream_outputs(a.M, a.D * (int64_t)(sizeof(T) + y_size));
+  // A residual of more than 4 MB goes out with the non-temporal hint where y,
+  // and not the residual, is what the next product reads: 103 us against 110 at
+  // 16384 x 4096 to int8, 11.1 against 12.1 at 1024 x 4096; in a chain of norm,
+  // product and quantiser of the residual 233 and 236 us at 16384 rows, 31.6 and
+  // 32.3 at 1024, but 19.1 and 18.5 at 256 (2 MB).  On y, or on the quantiser's
+  // codes, the hint gains up to 6 us and costs the pass that reads them next 30
+  // (16384 x 4096).
+  const bool stream = a.pre && (int64_t)a.M * a.D * (int64_t)sizeof(T) > ((int64_t)4 << 20);
   if (s.items == 0) {
     hipLaunchKernelGGL(k_block_norm_long<T>, row_grid(a.M), dim3(256), 0, a.stream, a);
     return hipGetLastError();
