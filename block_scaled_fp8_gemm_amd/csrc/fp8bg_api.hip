@@ -509,7 +509,11 @@ extern "C" int fbg_block_norm(const void* h, int64_t ldh, const void* x, int64_t
   if (pre && quantize == FBG_QUANT_FP8 && D % 128 != 0) return FBG_ERROR_UNSUPPORTED;
   if (M > 1 && (ldh < D || (x && ldx < D) || ldr < D || (pre && ldy < D))) return FBG_ERROR_INVALID_VALUE;
   if (M <= 1) ldh = ldx = ldr = ldy = D;
-  if (M == 0 || D == 0) return FBG_SUCCESS;
+  if (M == 0) return FBG_SUCCESS;
+  if (D == 0)  // no pointer to an empty row says anything: y_scale alone asks for the scales
+    return quantize == FBG_QUANT_INT8 && y_scale
+               ? fbg_quantize_tokens(nullptr, 0, dtype, M, 0, nullptr, 0, y_scale, stream)
+               : FBG_SUCCESS;
   const int64_t es = elem_size(dtype), ws = elem_size(weight_dtype), ys = quantize == FBG_QUANT_NONE ? es : 1;
   const int64_t bytesS = quantize == FBG_QUANT_NONE ? 0 : quantize == FBG_QUANT_INT8 ? M * 4 : M * (D / 128) * 4;
   int64_t bytesH = 0, bytesX = 0, bytesR = 0, bytesY = 0, bytesG = 0, g0 = 0, g1 = 0;

@@ -361,7 +361,8 @@ enum {
  * E4M3 codes with y_scale [M, D/128] (contiguous) by the rule of
  * fp8_block_gemm_quantize_rows (D % 128 == 0, else UNSUPPORTED), both taken
  * from the fp32 values.  r and y must not overlap an input or each other.
- * M == 0 or D == 0: nothing launched (int8 with D == 0 leaves y_scale alone).
+ * M == 0 or D == 0: nothing to do, but int8 with D == 0 and a y_scale sets every
+ * scale to 1e-12f / 127, as fbg_quantize_tokens does.
  */
 int fbg_block_norm(const void *h, int64_t ldh, const void *x, int64_t ldx, const void *gate, int64_t gate_row,
                    int64_t gate_col, const void *post, const void *pre, int dtype, int weight_dtype, int64_t M,

@@ -232,3 +232,16 @@ def test_large_residuals(gpu):
         ref_r, ref_y, tr, ty = T.block_norm(h[rows].cpu(), x[rows].cpu(), w.cpu(), None, w.cpu(), 1.0, 1e-6, 0.0)
         T.assert_close(r[rows], ref_r, tr, "bf16")
         T.assert_codes(c[rows], cs[rows], ref_y, ty, "int8")
+
+
+def test_rows_without_columns_have_a_scale(gpu):
+    """The scales of rows of no columns are written (their products are zero, not what the memory held)."""
+    want = T.quantize(torch.zeros(3, 0))[1]
+    for n in (3, 5000):
+        full = torch.full((n,), float("nan"), device=DEV)  # its memory is what the call below allocates
+        del full
+        h, w = torch.zeros(n, 0, device=DEV, dtype=torch.bfloat16), torch.zeros(0, device=DEV, dtype=torch.bfloat16)
+        r, q, s = gpu.block_norm(h, h, post_weight=w, pre_weight=w, quantize="int8")
+        assert r.shape == (n, 0) and q.shape == (n, 0) and torch.equal(s.cpu(), want[:1].expand(n))
+        c = gpu.int8_gemm(q, s, torch.zeros(4, 0, device=DEV, dtype=torch.int8), torch.ones(4, device=DEV))
+        assert torch.equal(c.cpu(), torch.zeros(n, 4, dtype=torch.bfloat16))
