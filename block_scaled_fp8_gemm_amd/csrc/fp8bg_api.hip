@@ -444,8 +444,6 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
   args.K = grouped && E == 0 ? 0 : (int)K;
   args.E = (int)E;
   args.out = out_dtype;
-  args.vec = (ldc % 4 == 0) && aligned(C, (uintptr_t)(4 * es));
-  if (args.vec && (ldc * es) % 16 == 0 && aligned(C, 16)) args.vec |= 2;  // 16-byte rows
   args.stream = static_cast<hipStream_t>(stream);
   int st = FBG_SUCCESS;
   const int cus = device_cu_count(&st);

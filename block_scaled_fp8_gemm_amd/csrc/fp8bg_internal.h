@@ -69,7 +69,6 @@ struct I8Args {
   int64_t lda, ldb, ldc;
   int M, N, K, E;
   int out;
-  int vec;  // as GemmArgs::vec, with ldc for the row pitch
   hipStream_t stream;
 };
 // cus: the device's compute units.  force_cfg >= 0: that configuration (hipErrorInvalidValue if it does

@@ -311,3 +311,18 @@ def test_arbitrary_offsets_stay_inside_the_operands(gpu, cfg):
     for e in range(E):
         fine |= C == T.gemm_bits({"A": d["A"], "a_s": d["a_s"], "B": d["B"][e], "b_s": d["b_s"][e]}, "fp32")
     assert bool(fine.all())
+
+
+@pytest.mark.parametrize("cfg", CONFIGS)
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N,off,pitch", [(257, 1, 259), (300, 3, 307), (513, 2, 516), (67, 5, 77)])
+def test_outputs_that_start_anywhere(gpu, cfg, out, N, off, pitch):
+    """Rows of C at any element, every configuration: what lies around them stays."""
+    M, K = 261, 272
+    d = T.make_gemm(M, N, K, seed=cfg + N, bias=cfg % 2 == 1)
+    buf = torch.full((M + 2, pitch), 7.0, device=DEV, dtype=T.DTYPES[out])
+    with forced_config(cfg):
+        C = _gemm(gpu, d, out, out=buf[1:M + 1, off:off + N])
+    T.assert_gemm(C, d, out, f"configuration {cfg}, {N} columns from {off}")
+    assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all())
+    assert bool((buf[:, :off] == 7).all()) and bool((buf[:, off + N:] == 7).all())
