@@ -174,8 +174,10 @@ __device__ __forceinline__ void int8_codes(const float (&v)[VE], float s, float 
   }
 }
 
-// A scale that is a NaN or an infinity: the row held one.  All its quotients
-// are 0 or NaN, so every code is 0.
+// A scale that is a NaN or an infinity: the row (or the 128 columns) held
+// one.  All its quotients are 0 or NaN, so every code is 0, and the products of
+// such a row are NaN.  (E4M3's clamp makes -448 of a quotient that is NaN,
+// whose products would be an infinity of the weights' sign.)
 __device__ __forceinline__ bool finite(float s) { return abs_bits(s) < 0x7f800000u; }
 
 // A launch holds less than 2^32 threads along x: many rows take a grid of two
@@ -371,7 +373,8 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float v = r[i][j + k], e = v * y;
-          q[k] = __builtin_amdgcn_fmed3f(__builtin_fmaf(__builtin_fmaf(-e, s, v), y, e), -448.0f, 448.0f);
+          const float t = __builtin_amdgcn_fmed3f(__builtin_fmaf(__builtin_fmaf(-e, s, v), y, e), -448.0f, 448.0f);
+          q[k] = finite(s) ? t : 0.0f;
         }
         const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
         o[j] = (uint8_t)(w & 255);
@@ -439,8 +442,9 @@ __global__ __launch_bounds__(256) void k_block_norm_long(NormArgs a) {
 #pragma unroll
       for (int o = 32; o > 0; o >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, o, 64));
       const float s = scale_of(amax, 448.0f);
-      const int c = __builtin_amdgcn_cvt_pk_fp8_f32(fminf(fmaxf(v0 / s, -448.0f), 448.0f),
-                                                    fminf(fmaxf(v1 / s, -448.0f), 448.0f), 0, false);
+      const int c = finite(s) ? __builtin_amdgcn_cvt_pk_fp8_f32(fminf(fmaxf(v0 / s, -448.0f), 448.0f),
+                                                                fminf(fmaxf(v1 / s, -448.0f), 448.0f), 0, false)
+                              : 0;
       y[d] = (uint8_t)(c & 255);
       y[d + 1] = (uint8_t)((c >> 8) & 255);
       if ((tid & 63) == 0) a.y_scale[m * (a.D / 128) + g] = s;

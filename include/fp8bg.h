@@ -360,7 +360,9 @@ enum {
  * `dtype`; int8 codes with y_scale [M] by the rule of fbg_quantize_tokens; or
  * E4M3 codes with y_scale [M, D/128] (contiguous) by the rule of
  * fp8_block_gemm_quantize_rows (D % 128 == 0, else UNSUPPORTED), both taken
- * from the fp32 values.  r and y must not overlap an input or each other.
+ * from the fp32 values; a group of 128 columns that holds a NaN or an infinity
+ * gets a scale that is one and zero codes, as a row does in int8.  r and y must
+ * not overlap an input or each other.
  * M == 0 or D == 0: nothing to do, but int8 with D == 0 and a y_scale sets every
  * scale to 1e-12f / 127, as fbg_quantize_tokens does.
  */
