@@ -34,3 +34,18 @@ def test_groups_with_an_infinity_or_a_nan(gpu, D, dtype):
     assert torch.equal(s[fine][:, others], clean_s[fine][:, others])
     B, b_s = gpu.quantize_blocks(torch.randn(64, D, device=DEV).to(torch.bfloat16))
     assert bool(gpu.gemm(q, s, B, b_s, out_dtype=torch.float32).isnan().all())
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_zeros_keep_their_sign(gpu, D, dtype):
+    """x / scale of a negative zero is a negative zero, as in the activation
+    quantiser's codes."""
+    _, x, w = _inputs(4, D, dtype)
+    x[:, ::3] = 0
+    _, q, _ = gpu.block_norm(x, pre_weight=w, quantize="fp8")
+    want = torch.where(w < 0, 128, 0).to(torch.uint8).expand(4, D)
+    assert torch.equal(q.view(torch.uint8)[:, ::3], want[:, ::3])
+    flat = torch.tensor([-0.0, 0.0] * 64, device=DEV, dtype=torch.bfloat16)[None]
+    codes, _ = gpu.quantize_rows(flat)
+    assert codes.view(torch.uint8)[0, :2].tolist() == [128, 0]
