@@ -368,7 +368,8 @@ def int8_grouped_gemm(A: torch.Tensor, a_s: torch.Tensor, B: torch.Tensor, b_s: 
     """The product per expert: rows offsets[e] .. offsets[e+1]-1 of A [M,K]
     int8 use weight B[e] of B [E,N,K] int8 and scales b_s[e] of b_s [E,N];
     a_s [M] float32, offsets int32 [E+1] on the same GPU (never read by the
-    host).  Rows of no expert are left as they are in `out`.  See
+    host).  B may be padded codes or a slice of wider rows, its E * N rows all
+    one distance apart.  Rows of no expert are left as they are in `out`.  See
     fbg_int8_grouped_gemm in include/fp8bg.h."""
     return (_native or _load_native()).int8_grouped_gemm(A, a_s, B, b_s, offsets, out_dtype, out, stream)
 
@@ -378,8 +379,10 @@ def quantize_tokens(x: torch.Tensor, q: torch.Tensor = None, scale: torch.Tensor
     """Per-row int8 quantisation of x [M,K] (bf16, fp16 or fp32; rows any
     distance apart): scale [M] = max(max_k |x|, 1e-12) / 127 and
     q [M,K] = round(clamp(x / scale, +-127)), ties to even.  Returns (q, scale),
-    the A and a_s (or, from weights, the B and b_s) of int8_gemm.  Where q is
-    not given and K is not a multiple of 16, its rows are padded to one.  See
+    the A and a_s (or, from weights, the B and b_s) of int8_gemm, and viewed as
+    [E,N,K] those of int8_grouped_gemm.  Where q is not given and K is not a
+    multiple of 16, its rows are padded to one, so that they start on 16-byte
+    boundaries.  See
     fbg_quantize_tokens in include/fp8bg.h."""
     return (_native or _load_native()).quantize_tokens(x, q, scale, stream)
 

@@ -60,11 +60,11 @@ def _build_torch(verbose: bool) -> None:
 
     import torch
     from torch.utils import cpp_extension
-    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include", INCLUDE]
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include", INCLUDE, CSRC]
     libs = cpp_extension.library_paths()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *[f for d in inc for f in ("-isystem" if d != INCLUDE else "-I", d)],
+           *[f for d in inc for f in ("-I" if d in (INCLUDE, CSRC) else "-isystem", d)],
            os.path.join(CSRC, TORCH_SOURCE), "-o", TORCH_LIB + ".tmp", "-L", PKG, "-lfp8bg", "-Wl,-rpath,$ORIGIN",
            *[f"-L{d}" for d in libs], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     if verbose:

@@ -468,6 +468,12 @@ extern "C" int fbg_int8_grouped_gemm(const void* A, int64_t lda, const float* a_
   return int8_call(A, lda, a_s, B, K, b_s, nullptr, C, ldc, offsets, E, M, N, K, out_dtype, true, stream);
 }
 
+int fbg::int8_grouped_gemm(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb, const float* b_s,
+                           void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                           int out_dtype, void* stream) {
+  return int8_call(A, lda, a_s, B, ldb, b_s, nullptr, C, ldc, offsets, E, M, N, K, out_dtype, true, stream);
+}
+
 extern "C" int fbg_quantize_tokens(const void* x, int64_t ldx, int in_dtype, int64_t M, int64_t K, void* q,
                                    int64_t ldq, float* scale, void* stream) {
   if (M < 0 || K < 0 || !known_dtype(in_dtype)) return FBG_ERROR_INVALID_VALUE;

@@ -32,6 +32,12 @@ int grouped_num_skinny_cfgs();
 int64_t workspace_bytes(const fbg_plan& p, int64_t M, int64_t N);
 int64_t workspace_counter_offset(const fbg_plan& p, int64_t M, int64_t N);
 
+// fbg_int8_grouped_gemm for weights whose E * N rows are ldb elements apart
+// (the Python binding's: torch slices and padded codes).
+int int8_grouped_gemm(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb, const float* b_s,
+                      void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                      int out_dtype, void* stream);
+
 #ifdef __HIPCC__
 struct GemmArgs {
   const uint8_t* A;

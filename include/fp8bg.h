@@ -279,8 +279,9 @@ int fp8_block_gemm_quantize_blocks(const void *w, int64_t N, int64_t K, void *B,
  * C [M,N] of out_dtype.  The integer sum is exact; the epilogue is fp32,
  * fl(fl(a_s*b_s) * fl(sum)) + bias, then one rounding to nearest even.  A and
  * B may start at any byte and have any pitch; rows that start on 16-byte
- * boundaries (base and pitch) take the faster loads.  a_s, b_s and bias 4-byte
- * aligned, C aligned to its element size.  M == 0 or N == 0: nothing launched;
+ * boundaries (base and pitch) are read faster, and where K is a multiple of 16
+ * too they take kernels of their own, faster by up to twice.  a_s, b_s and bias
+ * 4-byte aligned, C aligned to its element size.  M == 0 or N == 0: nothing launched;
  * K == 0: C is the bias, or zero.  K > 131071 (the int32 sum could overflow),
  * M or N above INT32_MAX - 1024, a pitch above 2^24 - 128 for A or B, or more
  * than 2^23 output tiles -> UNSUPPORTED; a pitch below the row's length, a null pointer with a
@@ -297,7 +298,8 @@ int fbg_int8_gemm(const void *A, int64_t lda, const float *a_s, const void *B, i
  *
  *     C[m,n] = a_s[m] * b_s[e,n] * sum_k A[m,k] * B[e,n,k]
  *
- * B [E,N,K] int8 and b_s [E,N] fp32, contiguous; A, a_s and C as above.
+ * B [E,N,K] int8 (from fbg_quantize_tokens: with ldq = K) and b_s [E,N] fp32,
+ * contiguous; A, a_s and C as above.
  * offsets: DEVICE pointer to E+1 int32, as for fp8_block_gemm_grouped: read
  * by the kernels alone, clamped into [0, M] (malformed offsets leave rows
  * unwritten or written twice, never address outside the operands), rows of no
