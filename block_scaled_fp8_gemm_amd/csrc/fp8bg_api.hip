@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include "fp8bg.h"
+#include "fp8bg_int8_configs.h"
 #include "fp8bg_internal.h"
 
 namespace {
@@ -384,12 +385,8 @@ extern "C" int fp8_block_gemm_grouped(const void* A, const float* a_s, const voi
 // ---------------------------------------------------------------------------
 namespace {
 
-// int32 sums of products of int8 codes, -128 included: 2^14 * K < 2^31.
-constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 1;
-
-// Largest row and column counts: the kernels round them up to a tile, or step
-// over them, in 32 bits.
-constexpr int64_t kMaxExtent = INT32_MAX - 1024;
+using fbg::kMaxExtent;
+using fbg::kMaxInt8K;
 
 // Bytes from the first element of `rows` rows of `cols` elements, `ld` apart,
 // to the end of the last one; false if that overflows.
@@ -444,13 +441,14 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
   args.K = grouped && E == 0 ? 0 : (int)K;
   args.E = (int)E;
   args.out = out_dtype;
+  args.first = 0;
   args.stream = static_cast<hipStream_t>(stream);
   int st = FBG_SUCCESS;
   const int cus = device_cu_count(&st);
   if (st != FBG_SUCCESS) return st;
   const int force = forced_config();
   const hipError_t err = fbg::launch_i8(args, cus, force);
-  if (err == hipErrorInvalidValue) return FBG_ERROR_UNSUPPORTED;  // a grid past 2^32 threads, or a forced configuration
+  if (err == hipErrorInvalidValue) return FBG_ERROR_UNSUPPORTED;  // more tiles than 32 bits hold, or a forced configuration
   return err == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }
 

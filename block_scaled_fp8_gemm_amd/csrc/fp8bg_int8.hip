@@ -76,6 +76,12 @@ __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, 
   return e_out >= 0;
 }
 
+// This workgroup's tile: launches hold fewer workgroups than a product may
+// have, each one starting at tile `first`.
+__device__ __forceinline__ int logical_tile(const I8Args& a) {
+  return a.first + xcd_remap(blockIdx.x, (int)gridDim.x);
+}
+
 // An fp32 value as it is rounded: a product whose conversion to fp16 follows
 // becomes one instruction with one rounding otherwise, which is not what the
 // other kernels and types give (it differs in about one value of 1e5).
@@ -160,7 +166,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const int tiles_n = (a.N + BN - 1) / BN;
-  const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+  const int lid = logical_tile(a);
   int m0, n0, m_end = a.M, e = 0;
   if constexpr (GRP) {
     if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(smem))) return;
@@ -279,7 +285,7 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
-  const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+  const int lid = logical_tile(a);
   int e = 0, m_lo, m_end, tn;
   if constexpr (GRP) {
     e = lid / tiles_n;
@@ -424,7 +430,7 @@ __global__ __launch_bounds__(256, 2) void k_i8_slim(I8Args a) {
   const int tiles_n = (a.N + BN - 1) / BN;
   int m0, n0, m_end = a.M, e = 0;
   {
-    const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+    const int lid = logical_tile(a);
     if constexpr (GRP) {
       if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(smem))) return;
       n0 = (lid % tiles_n) * BN;
@@ -725,7 +731,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, BK, STAGES
   const int tiles_n = (a.N + BN - 1) / BN;
   int m0, n0, m_end = a.M, e = 0;
   {
-    const int lid = xcd_remap(blockIdx.x, (int)gridDim.x);
+    const int lid = logical_tile(a);
     if constexpr (GRP) {
       if (!expert_of_slot<BM>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(smem))) return;
       n0 = (lid % tiles_n) * BN;
@@ -1036,14 +1042,23 @@ hipError_t launch_i8(const I8Args& a, int cus, int force_cfg) {
   const int cfg = force_cfg >= 0 ? force_cfg : int8_cfg_for(E, a.M, a.N, a.K, fast_rows(a), cus);
   if (cfg >= kNumI8Cfgs) return hipErrorInvalidValue;
   const int64_t grid = int8_grid(cfg, E, a.M, a.N);
-  if (grid >= (int64_t)1 << 23) return hipErrorInvalidValue;  // of up to 512 threads: 2^32 in a launch
-  switch (cfg) {
+  if (grid > kMaxI8Grid) return hipErrorInvalidValue;
+  // A launch holds less than 2^32 threads, and a workgroup up to 512.
+  constexpr int64_t kPerLaunch = ((int64_t)1 << 23) - kXcds;
+  for (int64_t first = 0; first < grid; first += kPerLaunch) {
+    I8Args part = a;
+    part.first = (int)first;
+    const unsigned n = (unsigned)(grid - first < kPerLaunch ? grid - first : kPerLaunch);
+    hipError_t e = hipErrorInvalidValue;
+    switch (cfg) {
 #define X(id, kind, ...) \
-  case id: return launch_##kind<__VA_ARGS__>(a, (unsigned)grid);
-    FBG_I8_CFGS(X)
+  case id: e = launch_##kind<__VA_ARGS__>(part, n); break;
+      FBG_I8_CFGS(X)
 #undef X
+    }
+    if (e != hipSuccess) return e;
   }
-  return hipErrorInvalidValue;
+  return hipSuccess;
 }
 
 }  // namespace fbg

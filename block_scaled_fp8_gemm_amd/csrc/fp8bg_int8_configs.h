@@ -32,6 +32,16 @@ constexpr int kNumI8Cfgs = 13;
 constexpr int kI8FirstTile = 5;  // configurations from here on (tiles and slim) take 16-byte rows only
 constexpr int kI8FirstSkinny = 2;
 
+// Largest K: int32 sums of products of int8 codes, -128 included, 2^14 * K < 2^31.
+constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 1;
+
+// Largest row, column and expert counts: the kernels round them up to a tile,
+// or step over them, in 32 bits.
+constexpr int64_t kMaxExtent = INT32_MAX - 1024;
+
+// Largest count of a product's tiles, which are numbered in 32 bits.
+constexpr int64_t kMaxI8Grid = INT32_MAX;
+
 // The configuration for M rows (of E experts in the grouped form, E = 0 for
 // the dense one), N columns and K bytes on a device of `cus` compute units;
 // `fast`: the rows start on 16-byte boundaries and hold whole 16-byte chunks.

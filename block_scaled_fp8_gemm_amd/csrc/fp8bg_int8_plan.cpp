@@ -116,7 +116,8 @@ int64_t int8_grid(int cfg, int64_t E, int64_t M, int64_t N) {
 extern "C" int fbg_int8_plan(int64_t E, int64_t M, int64_t N, int64_t K, int aligned_rows, int cu_count,
                              fbg_plan* out) {
   if (!out || E < 0 || M < 0 || N < 0 || K < 0 || cu_count <= 0) return FBG_ERROR_INVALID_VALUE;
-  if (M > INT32_MAX || N > INT32_MAX || E > INT32_MAX - 1 || K > 131071) return FBG_ERROR_UNSUPPORTED;
+  if (M > fbg::kMaxExtent || N > fbg::kMaxExtent || E > fbg::kMaxExtent || K > fbg::kMaxInt8K)
+    return FBG_ERROR_UNSUPPORTED;
   *out = fbg_plan{};
   out->variant = FBG_VARIANT_INT8;
   out->split_k = 1;
@@ -124,10 +125,12 @@ extern "C" int fbg_int8_plan(int64_t E, int64_t M, int64_t N, int64_t K, int ali
   if (M == 0 || N == 0 || K < 16) return FBG_SUCCESS;
   const int cfg = fbg::int8_cfg_for(E, M, N, K, aligned_rows != 0 && K % 16 == 0, cu_count);
   const fbg::Cost& c = fbg::kFast[cfg];
+  const int64_t grid = fbg::int8_grid(cfg, E, M, N);
+  if (grid > fbg::kMaxI8Grid) return FBG_ERROR_UNSUPPORTED;
   out->tile_m = c.rows;
   out->tile_n = c.cols;
   out->waves = c.waves;
   out->config = cfg;
-  out->grid = fbg::int8_grid(cfg, E, M, N);
+  out->grid = grid;
   return FBG_SUCCESS;
 }

@@ -75,10 +75,11 @@ struct I8Args {
   int64_t lda, ldb, ldc;
   int M, N, K, E;
   int out;
+  int first;  // the launch's first tile (launch_i8 sets it)
   hipStream_t stream;
 };
 // cus: the device's compute units.  force_cfg >= 0: that configuration (hipErrorInvalidValue if it does
-// not take these operands).
+// not take these operands, as for more than kMaxI8Grid tiles).
 hipError_t launch_i8(const I8Args& a, int cus, int force_cfg);
 
 // One row per token (fp8bg_rows.hip).  dtype: the FBG_OUT_* code of x, h,

@@ -284,9 +284,10 @@ int fp8_block_gemm_quantize_blocks(const void *w, int64_t N, int64_t K, void *B,
  * 4-byte aligned, C aligned to its element size.  M == 0 or N == 0: nothing launched;
  * K == 0: C is the bias, or zero.  K > 131071 (the int32 sum could overflow),
  * M or N above INT32_MAX - 1024, a pitch above 2^24 - 128 for A or B, or more
- * than 2^23 output tiles -> UNSUPPORTED; a pitch below the row's length, a null pointer with a
- * non-empty extent, an unknown out_dtype or C overlapping an input ->
- * INVALID_VALUE.
+ * than INT32_MAX output tiles -> UNSUPPORTED; a pitch below the row's length, a
+ * null pointer with a non-empty extent, an unknown out_dtype or C overlapping
+ * an input -> INVALID_VALUE.  Products of 2^23 tiles and more go out as several
+ * launches.
  */
 int fbg_int8_gemm(const void *A, int64_t lda, const float *a_s, const void *B, int64_t ldb, const float *b_s,
                   const float *bias, void *C, int64_t ldc, int64_t M, int64_t N, int64_t K, int out_dtype,
