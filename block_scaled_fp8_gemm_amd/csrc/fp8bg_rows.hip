@@ -372,12 +372,12 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
         float q[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+          // The remainder with its sign turned: as v - e * s the step makes
+          // +0 of a negative zero.
           const float v = r[i][j + k], e = v * y;
-          // v's sign: the correction step makes +0 of a negative zero.
-          const float t = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-e, s, v), y, e), v);
-          q[k] = finite(s) ? __builtin_amdgcn_fmed3f(t, -448.0f, 448.0f) : 0.0f;
+          q[k] = __builtin_amdgcn_fmed3f(__builtin_fmaf(-__builtin_fmaf(e, s, -v), y, e), -448.0f, 448.0f);
         }
-        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+        const int w = finite(s) ? __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false) : 0;
         o[j] = (uint8_t)(w & 255);
         o[j + 1] = (uint8_t)((w >> 8) & 255);
       }
