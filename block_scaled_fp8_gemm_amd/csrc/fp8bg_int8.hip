@@ -45,7 +45,11 @@ __device__ __forceinline__ v4i mfma_i8(const v4i& x, const v4i& y, const v4i& ac
 // Malformed offsets never lead outside the operands: each is clamped, and
 // where several experts claim a slot the last of them has it alone (its rows
 // come from one thread).
-template <int BM>
+//
+// REST: slots for an expert's tiles from its second on.  They start at
+// floor(offsets[e] / BM): floor((r + n) / BM) >= ceil(n / BM) - 1 of them, and
+// floor(M / BM) in all.
+template <int BM, bool REST = false>
 __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, int E, int M, int t, int& e_out,
                                                int& m0, int& m_end, int* found) {
   if (threadIdx.x == 0) found[0] = -1;
@@ -55,8 +59,8 @@ __device__ __forceinline__ bool expert_of_slot(const int* __restrict__ offsets, 
     int lo = offsets[e], hi = offsets[e + 1];
     lo = lo < 0 ? 0 : (lo > M ? M : lo);
     hi = hi < lo ? lo : (hi > M ? M : hi);
-    const int i = t - (lo / BM + e);
-    if (i >= 0 && (int64_t)i * BM < hi - lo) {
+    const int s = t - (lo / BM + (REST ? 0 : e)), i = REST ? s + 1 : s;
+    if (s >= 0 && (int64_t)i * BM < hi - lo) {
       mine = e;
       first = lo + i * BM;
       last = hi;
@@ -275,8 +279,11 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
 // FAST: rows of whole 16-byte chunks on 16-byte boundaries; else chunks at any
 // alignment (load_window).
 //
-// Grouped: one workgroup per (expert, column tile), walking the expert's rows
-// ROWS at a time (the weights of a second pass come from L2).
+// Grouped: one workgroup per (expert, column tile) takes the expert's first
+// ROWS rows, and further ones (floor(M / ROWS) slots, see expert_of_slot) the
+// rest: walked by the first, all rows in one expert took 137 us where they take
+// 9.9 (64 experts of 128 x 4096, 512 rows), and 617 where they take 13.8 (256 of
+// 128 x 1001, 3072 rows); spread evenly both ways take the same.
 // ---------------------------------------------------------------------------
 template <int NB, int ROWS, int KW, int U, bool FAST, int GRP>
 __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
@@ -285,21 +292,33 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
-  const int lid = logical_tile(a);
-  int e = 0, m_lo, m_end, tn;
+  int e = 0, m0, m_end, tn;
   if constexpr (GRP) {
-    e = lid / tiles_n;
-    tn = lid - e * tiles_n;
-    int lo = a.offsets[e], hi = a.offsets[e + 1];
-    lo = lo < 0 ? 0 : (lo > a.M ? a.M : lo);  // malformed offsets never lead outside the operands
-    hi = hi < lo ? lo : (hi > a.M ? a.M : hi);
-    m_lo = lo;
-    m_end = hi;
+    const int g = a.first + (int)blockIdx.x, firsts = a.E * tiles_n;
+    if (g < firsts) {
+      const int lid = xcd_remap(g, firsts);
+      e = lid / tiles_n;
+      tn = lid - e * tiles_n;
+      int lo = a.offsets[e], hi = a.offsets[e + 1];
+      lo = lo < 0 ? 0 : (lo > a.M ? a.M : lo);  // malformed offsets never lead outside the operands
+      hi = hi < lo ? lo : (hi > a.M ? a.M : hi);
+      m0 = lo;
+      m_end = hi;
+    } else {
+      const int lid = xcd_remap(g - firsts, a.M / ROWS * tiles_n);
+      if (!expert_of_slot<ROWS, true>(a.offsets, a.E, a.M, lid / tiles_n, e, m0, m_end, reinterpret_cast<int*>(red)))
+        return;
+      tn = lid % tiles_n;
+    }
+    if (m0 >= m_end) return;
+    m0 = __builtin_amdgcn_readfirstlane(m0);
+    m_end = __builtin_amdgcn_readfirstlane(m0 + ROWS < m_end ? m0 + ROWS : m_end);
+    e = __builtin_amdgcn_readfirstlane(e);
   } else {
-    const int tiles_m = (a.M + ROWS - 1) / ROWS;
+    const int lid = logical_tile(a), tiles_m = (a.M + ROWS - 1) / ROWS;
     tn = lid / tiles_m;
-    m_lo = (lid - tn * tiles_m) * ROWS;
-    m_end = m_lo + ROWS < a.M ? m_lo + ROWS : a.M;
+    m0 = (lid - tn * tiles_m) * ROWS;
+    m_end = m0 + ROWS < a.M ? m0 + ROWS : a.M;
   }
   const int n0 = tn * 16 * NB, r = lane & 15, h = lane >> 4;
   const uint8_t* brow[NB];
@@ -309,83 +328,78 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
     brow[j] = a.B + ((int64_t)e * a.N + n) * a.ldb;
   }
   const int groups = (a.K + 64 * U - 1) / (64 * U);
-  for (int m0 = m_lo; m0 < m_end; m0 += ROWS) {
-    const uint8_t* arow[MB];
+  const uint8_t* arow[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int last = m0 + ROWS < m_end ? m0 + ROWS - 1 : m_end - 1;
-      const int m = m0 + 16 * i + r < last ? m0 + 16 * i + r : last;
-      arow[i] = a.A + (int64_t)m * a.lda;
-    }
-    v4i acc[MB][NB];
+  for (int i = 0; i < MB; ++i) {
+    const int m = m0 + 16 * i + r < m_end ? m0 + 16 * i + r : m_end - 1;
+    arow[i] = a.A + (int64_t)m * a.lda;
+  }
+  v4i acc[MB][NB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+  for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-    v4i fa[U][MB], fb[U][NB];
-    auto load = [&](int g) {
+    for (int j = 0; j < NB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  v4i fa[U][MB], fb[U][NB];
+  auto load = [&](int g) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (g * U + u) * 64 + 16 * h;
+    for (int u = 0; u < U; ++u) {
+      const int k = (g * U + u) * 64 + 16 * h;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          if constexpr (FAST && GRP) fb[u][j] = *reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0));
-          else if constexpr (FAST) fb[u][j] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0)));
-          else fb[u][j] = load_window(brow[j], k, a.K);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (g * U + u) * 64 + 16 * h;
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          if constexpr (FAST) fa[u][i] = *reinterpret_cast<const v4i*>(arow[i] + (k < a.K ? k : 0));
-          else fa[u][i] = load_window(arow[i], k, a.K);
-        }
-      }
-    };
-    auto multiply = [&](int g) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (g * U + u) * 64 + 16 * h;  // FAST: chunks past K were read from the row's start
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          v4i f = fa[u][i];
-          if constexpr (FAST) f = k < a.K ? f : v4i{0, 0, 0, 0};
-          else if ((g * U + u + 1) * 64 > a.K) f = keep_tail(f, k, a.K);
-#pragma unroll
-          for (int j = 0; j < NB; ++j) acc[i][j] = mfma_i8(fb[u][j], f, acc[i][j]);
-        }
-      }
-    };
-    for (int g = wave; g < groups; g += KW) {
-      load(g);
-      __builtin_amdgcn_sched_barrier(0);  // every load of the group in flight before the first product
-      multiply(g);
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) red[wave][i * NB + j][lane] = acc[i][j];
-    __syncthreads();
-    for (int b = wave; b < BLOCKS; b += KW) {
-      const int i = b / NB, j = b % NB, m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * h;
-      const int stop = m0 + ROWS < m_end ? m0 + ROWS : m_end;
-      v4i s = red[0][b][lane];
-#pragma unroll
-      for (int w = 1; w < KW; ++w) s += red[w][b][lane];
-      const int cnt = a.N - n < 4 ? a.N - n : 4;
-      if (m < stop && cnt > 0) {
-        const v4f c = scale4(s, a.a_s[m], a.b_s + (int64_t)e * a.N, a.bias, n, a.N);
-        const int64_t at = (int64_t)m * a.ldc + n;
-        switch (a.out) {
-          case kOutBF16: store_run<kOutBF16>(a.C, at, c, cnt); break;
-          case kOutFP16: store_run<kOutFP16>(a.C, at, c, cnt); break;
-          default: store_run<kOutFP32>(a.C, at, c, cnt); break;
-        }
+      for (int j = 0; j < NB; ++j) {
+        if constexpr (FAST && GRP) fb[u][j] = *reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0));
+        else if constexpr (FAST) fb[u][j] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(brow[j] + (k < a.K ? k : 0)));
+        else fb[u][j] = load_window(brow[j], k, a.K);
       }
     }
-    if constexpr (GRP) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (g * U + u) * 64 + 16 * h;
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        if constexpr (FAST) fa[u][i] = *reinterpret_cast<const v4i*>(arow[i] + (k < a.K ? k : 0));
+        else fa[u][i] = load_window(arow[i], k, a.K);
+      }
+    }
+  };
+  auto multiply = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (g * U + u) * 64 + 16 * h;  // FAST: chunks past K were read from the row's start
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        v4i f = fa[u][i];
+        if constexpr (FAST) f = k < a.K ? f : v4i{0, 0, 0, 0};
+        else if ((g * U + u + 1) * 64 > a.K) f = keep_tail(f, k, a.K);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma_i8(fb[u][j], f, acc[i][j]);
+      }
+    }
+  };
+  for (int g = wave; g < groups; g += KW) {
+    load(g);
+    __builtin_amdgcn_sched_barrier(0);  // every load of the group in flight before the first product
+    multiply(g);
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) red[wave][i * NB + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int b = wave; b < BLOCKS; b += KW) {
+    const int i = b / NB, j = b % NB, m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * h;
+    v4i s = red[0][b][lane];
+#pragma unroll
+    for (int w = 1; w < KW; ++w) s += red[w][b][lane];
+    const int cnt = a.N - n < 4 ? a.N - n : 4;
+    if (m < m_end && cnt > 0) {
+      const v4f c = scale4(s, a.a_s[m], a.b_s + (int64_t)e * a.N, a.bias, n, a.N);
+      const int64_t at = (int64_t)m * a.ldc + n;
+      switch (a.out) {
+        case kOutBF16: store_run<kOutBF16>(a.C, at, c, cnt); break;
+        case kOutFP16: store_run<kOutFP16>(a.C, at, c, cnt); break;
+        default: store_run<kOutFP32>(a.C, at, c, cnt); break;
+      }
+    }
   }
 }
 

@@ -85,7 +85,8 @@ int int8_cfg_for(int64_t E, int64_t M, int64_t N, int64_t K, bool fast, int cus)
   // 6.0; 1 x 1536 x 4096 4.9 and 5.8; 4 x 4096 x 4096 5.9 and 6.0; 8 rows 6.2
   // and 6.0; past that 1 x 8192 x 4096 8.6 and 8.1).
   if (E == 0 && fast && M <= 4 && ceil_div(N, 16) <= cus) return 2;
-  // A skinny workgroup walks an expert's rows one pass after the other.
+  // Larger experts: the skinny kernel's fits, over dense products, say nothing
+  // of its grouped form.
   if (E > 0 && fast) first = kI8FirstTile;
   if (E > 0 && !fast) end = kI8FirstSkinny;
   int best = first;
@@ -108,7 +109,7 @@ int64_t int8_grid(int cfg, int64_t E, int64_t M, int64_t N) {
   const Cost& c = kFast[cfg];
   const int64_t across = ceil_div(N, c.cols);
   if (E == 0) return ceil_div(M, c.rows) * across;
-  return (c.kind == SKINNY ? E : M / c.rows + E) * across;
+  return (M / c.rows + E) * across;
 }
 
 }  // namespace fbg
