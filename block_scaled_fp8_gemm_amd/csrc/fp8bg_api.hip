@@ -446,8 +446,7 @@ int int8_call(const void* A, int64_t lda, const float* a_s, const void* B, int64
   int st = FBG_SUCCESS;
   const int cus = device_cu_count(&st);
   if (st != FBG_SUCCESS) return st;
-  const int force = forced_config();
-  const hipError_t err = fbg::launch_i8(args, cus, force);
+  const hipError_t err = fbg::launch_i8(args, cus, forced_config(), env_flag("FBG_LOG"));
   if (err == hipErrorInvalidValue) return FBG_ERROR_UNSUPPORTED;  // more tiles than 32 bits hold, or a forced configuration
   return err == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }

@@ -16,6 +16,8 @@
 //
 // The grouped (mixture-of-experts) form gives rows offsets[e] ..
 // offsets[e+1]-1 of A the weight B[e]; see expert_of_slot.
+#include <stdio.h>
+
 #include <type_traits>
 
 #include "fp8bg_device.hpp"
@@ -1040,9 +1042,16 @@ hipError_t launch_SKINNY(const I8Args& a, unsigned grid) {
 
 }  // namespace
 
-hipError_t launch_i8(const I8Args& a, int cus, int force_cfg) {
+hipError_t launch_i8(const I8Args& a, int cus, int force_cfg, bool log) {
+  const int64_t E = a.offsets ? a.E : 0;
+  auto report = [&](int cfg, int64_t grid) {
+    if (log)
+      fprintf(stderr, "fp8bg int8: E=%lld M=%d N=%d K=%d out=%d -> cfg=%d grid=%lld\n", (long long)E, a.M, a.N, a.K, a.out,
+              cfg, (long long)grid);
+  };
   if (a.K < 16) {
     if (a.K > 0 && force_cfg >= 0) return hipErrorInvalidValue;
+    report(-1, 0);
     const int64_t blocks = ((int64_t)a.M * a.N + 255) / 256;
     const dim3 g((unsigned)(blocks < 65536 ? blocks : 65536)), b(256);
     switch (a.out) {
@@ -1052,11 +1061,11 @@ hipError_t launch_i8(const I8Args& a, int cus, int force_cfg) {
     }
     return hipGetLastError();
   }
-  const int64_t E = a.offsets ? a.E : 0;
   const int cfg = force_cfg >= 0 ? force_cfg : int8_cfg_for(E, a.M, a.N, a.K, fast_rows(a), cus);
   if (cfg >= kNumI8Cfgs) return hipErrorInvalidValue;
   const int64_t grid = int8_grid(cfg, E, a.M, a.N);
   if (grid > kMaxI8Grid) return hipErrorInvalidValue;
+  report(cfg, grid);
   // A launch holds less than 2^32 threads, and a workgroup up to 512.
   constexpr int64_t kPerLaunch = ((int64_t)1 << 23) - kXcds;
   for (int64_t first = 0; first < grid; first += kPerLaunch) {

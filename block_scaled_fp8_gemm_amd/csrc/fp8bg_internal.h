@@ -78,9 +78,9 @@ struct I8Args {
   int first;  // the launch's first tile (launch_i8 sets it)
   hipStream_t stream;
 };
-// cus: the device's compute units.  force_cfg >= 0: that configuration (hipErrorInvalidValue if it does
+// cus: the device's compute units.  log: the plan goes to stderr.  force_cfg >= 0: that configuration (hipErrorInvalidValue if it does
 // not take these operands, as for more than kMaxI8Grid tiles).
-hipError_t launch_i8(const I8Args& a, int cus, int force_cfg);
+hipError_t launch_i8(const I8Args& a, int cus, int force_cfg, bool log);
 
 // One row per token (fp8bg_rows.hip).  dtype: the FBG_OUT_* code of x, h,
 // gate and r; rows ld* elements apart.
