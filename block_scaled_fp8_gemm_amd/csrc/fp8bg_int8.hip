@@ -273,9 +273,10 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
 // The skinny kernel: few rows, so the weights' bytes and the launch's latency
 // are what counts.  A workgroup takes 16*NB columns and ROWS rows; its KW
 // waves split K, each loading its own fragments straight into registers in
-// groups of U slices of 64 K bytes (wave w takes groups w, w + KW, ..), the
-// next group's loads in flight while this one is multiplied; the waves' sums
-// meet in LDS.  ROWS = 8 halves a 16-row tile's activation bytes: the upper
+// groups of U slices of 64 K bytes (wave w takes groups w, w + KW, ..), all of
+// a group's loads in flight together and the next group's once it is
+// multiplied (K = 4096 over 8 waves is two such rounds); the waves' sums meet
+// in LDS.  ROWS = 8 halves a 16-row tile's activation bytes: the upper
 // eight rows of the MFMA repeat the last one and are not stored.
 //
 // FAST: rows of whole 16-byte chunks on 16-byte boundaries; else chunks at any
@@ -289,8 +290,8 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args a) {
 // ---------------------------------------------------------------------------
 template <int NB, int ROWS, int KW, int U, bool FAST, int GRP>
 __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
-  constexpr int MB = (ROWS + 15) / 16, BLOCKS = NB * MB;
-  __shared__ v4i red[KW][BLOCKS][64];
+  static_assert(ROWS <= 16, "one row block of the MFMA");
+  __shared__ v4i red[KW][NB][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
@@ -330,18 +331,11 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
     brow[j] = a.B + ((int64_t)e * a.N + n) * a.ldb;
   }
   const int groups = (a.K + 64 * U - 1) / (64 * U);
-  const uint8_t* arow[MB];
+  const uint8_t* arow = a.A + (int64_t)(m0 + r < m_end ? m0 + r : m_end - 1) * a.lda;
+  v4i acc[NB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = m0 + 16 * i + r < m_end ? m0 + 16 * i + r : m_end - 1;
-    arow[i] = a.A + (int64_t)m * a.lda;
-  }
-  v4i acc[MB][NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  v4i fa[U][MB], fb[U][NB];
+  for (int j = 0; j < NB; ++j) acc[j] = v4i{0, 0, 0, 0};
+  v4i fa[U], fb[U][NB];
   auto load = [&](int g) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -356,25 +350,19 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (g * U + u) * 64 + 16 * h;
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        if constexpr (FAST) fa[u][i] = *reinterpret_cast<const v4i*>(arow[i] + (k < a.K ? k : 0));
-        else fa[u][i] = load_window(arow[i], k, a.K);
-      }
+      if constexpr (FAST) fa[u] = *reinterpret_cast<const v4i*>(arow + (k < a.K ? k : 0));
+      else fa[u] = load_window(arow, k, a.K);
     }
   };
   auto multiply = [&](int g) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (g * U + u) * 64 + 16 * h;  // FAST: chunks past K were read from the row's start
+      v4i f = fa[u];
+      if constexpr (FAST) f = k < a.K ? f : v4i{0, 0, 0, 0};
+      else if ((g * U + u + 1) * 64 > a.K) f = keep_tail(f, k, a.K);
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        v4i f = fa[u][i];
-        if constexpr (FAST) f = k < a.K ? f : v4i{0, 0, 0, 0};
-        else if ((g * U + u + 1) * 64 > a.K) f = keep_tail(f, k, a.K);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mfma_i8(fb[u][j], f, acc[i][j]);
-      }
+      for (int j = 0; j < NB; ++j) acc[j] = mfma_i8(fb[u][j], f, acc[j]);
     }
   };
   for (int g = wave; g < groups; g += KW) {
@@ -383,15 +371,13 @@ __global__ __launch_bounds__(64 * KW) void k_i8_skinny(I8Args a) {
     multiply(g);
   }
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) red[wave][i * NB + j][lane] = acc[i][j];
+  for (int j = 0; j < NB; ++j) red[wave][j][lane] = acc[j];
   __syncthreads();
-  for (int b = wave; b < BLOCKS; b += KW) {
-    const int i = b / NB, j = b % NB, m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * h;
-    v4i s = red[0][b][lane];
+  for (int j = wave; j < NB; j += KW) {
+    const int m = m0 + r, n = n0 + 16 * j + 4 * h;
+    v4i s = red[0][j][lane];
 #pragma unroll
-    for (int w = 1; w < KW; ++w) s += red[w][b][lane];
+    for (int w = 1; w < KW; ++w) s += red[w][j][lane];
     const int cnt = a.N - n < 4 ? a.N - n : 4;
     if (m < m_end && cnt > 0) {
       const v4f c = scale4(s, a.a_s[m], a.b_s + (int64_t)e * a.N, a.bias, n, a.N);
@@ -719,26 +705,25 @@ __device__ __forceinline__ void store_tile(const I8Args& a, const v16i (&acc)[IB
 // next step's loads, meets the others, refills the slot with the step STAGES
 // ahead and reads the next step's first fragments.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int BK, int STAGES>
+template <int BM, int BN, int STAGES>
 struct TileLds {
-  static constexpr int SLOT = (BM + BN) * BK;
+  static constexpr int SLOT = (BM + BN) * 128;
   static constexpr int AI = (BM + 63) / 64, BI = BN / 64;   // 64-value images of the row and the column scales
   static constexpr int BYTES = STAGES * SLOT + (AI + 2 * BI) * 256;
   static constexpr int PER_CU = 160 * 1024 / BYTES;
 };
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int BK, int STAGES, int SPREAD, int GRP>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, BK, STAGES>::PER_CU > 1 ? 2 : 1)) void k_i8_tile(I8Args a) {
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int GRP>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, STAGES>::PER_CU > 1 ? 2 : 1)) void k_i8_tile(I8Args a) {
   constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, IB = WM / 32, JB = WN / 32;
-  constexpr int CH = BK / 16, RI = 64 / CH, SL = BK / 32;           // chunks per row, rows per load image, slices
+  constexpr int BK = 128, CH = BK / 16, RI = 64 / CH, SL = BK / 32;  // bytes of K and chunks per row, rows per load image, slices
   constexpr int AP = BM * CH / NT, BP = BN * CH / NT, LPS = AP + BP;  // loads per thread per step
   constexpr int A_BYTES = BM * BK, SLOT = (BM + BN) * BK;
-  static_assert(BK == 64 || BK == 128, "");
   static_assert(BM * CH % NT == 0 && BN * CH % NT == 0, "whole load images per wave");
   static_assert((NW * RI) % 16 == 0, "a lane's chunk is the same in all its images");
   static_assert((STAGES - 1) * LPS < 64, "vmcnt counts at most 63 outstanding loads");
-  typedef TileLds<BM, BN, BK, STAGES> L;
+  typedef TileLds<BM, BN, STAGES> L;
   __shared__ __attribute__((aligned(16))) uint8_t smem[L::BYTES];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -777,9 +762,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, BK, STAGES
   // Load image q (q = i*NW + wave) fills RI LDS rows of a tile; lane l writes
   // row q*RI + l / CH, slot l % CH, so it reads the row's chunk
   // (l % CH) ^ swz(row).
-  auto swz = [](int r) { return BK == 128 ? swz_row(r) : (r >> 2) & 3; };
   uint32_t aoff[AP], boff[BP];
-  const int chunk = (lane % CH) ^ swz(RI * wave + lane / CH);
+  const int chunk = (lane % CH) ^ swz_row(RI * wave + lane / CH);
 #pragma unroll
   for (int i = 0; i < AP; ++i) {
     const int r = RI * (i * NW + wave) + lane / CH;
@@ -800,14 +784,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, BK, STAGES
     if (i < AP) lds_dma16(rA, aoff[i < AP ? i : 0] - sub, k * BK, base + 1024 * (i * NW + wave));
     else lds_dma16(rB, boff[i < AP ? 0 : i - AP] - sub, k * BK, base + A_BYTES + 1024 * ((i - AP) * NW + wave));
   };
-  // A step's refill is spread over SPREAD slices, the last one of the step
-  // that frees the slot and the first ones of the step after it: load q goes
-  // out behind MFMA number q * SPREAD * IB * JB / LPS of those.  LPS0 of them
-  // belong to the first part.
+  // A step's refill is spread over two slices, the last one of the step that
+  // frees the slot and the first one of the step after it, LPS0 loads behind
+  // the MFMAs of the one and LPS - LPS0 behind those of the other.
   constexpr int NM = IB * JB;
-  constexpr int LPS0 = (LPS + SPREAD - 1) / SPREAD;
+  constexpr int LPS0 = (LPS + 1) / 2;
   // Slice s of row block b: this lane's 16 bytes.
-  const int frow = lane & 31, fh = lane >> 5, fsw = swz(frow);
+  const int frow = lane & 31, fh = lane >> 5, fsw = swz_row(frow);
   auto frag = [&](int slot, int off, int row0, int s) {
     return *reinterpret_cast<const v4i*>(smem + slot * SLOT + off + BK * (row0 + frow) + 16 * ((2 * s + fh) ^ fsw));
   };
@@ -900,9 +883,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, (TileLds<BM, BN, BK, STAGES
           }
 #pragma unroll
           for (int q = 0; q < LPS; ++q) {
-            const int at = q < LPS0 ? q * NM / LPS0 : NM + (q - LPS0) * ((SPREAD - 1) * NM) / (LPS - LPS0 > 0 ? LPS - LPS0 : 1);
-            if (kRefill && s == SL - 1 && at == t) load_one(k + STAGES, slot, q, sub);
-            if (kPrev && s < SL - 1 && at == (s + 1) * NM + t) load_one(k - 1 + STAGES, before, q, sub_prev);
+            const int at = q < LPS0 ? q * NM / LPS0 : (q - LPS0) * NM / (LPS - LPS0);
+            if (kRefill && s == SL - 1 && q < LPS0 && at == t) load_one(k + STAGES, slot, q, sub);
+            if (kPrev && s == 0 && q >= LPS0 && at == t) load_one(k - 1 + STAGES, before, q, sub_prev);
           }
         }
     }
@@ -1004,12 +987,12 @@ hipError_t launch_ANY(const I8Args& a, unsigned grid) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM_, int WN_, int BK, int ST, int SP>
+template <int BM, int BN, int WM_, int WN_, int ST>
 hipError_t launch_TILE(const I8Args& a, unsigned grid) {
   if (!fast_rows(a)) return hipErrorInvalidValue;
   const dim3 g(grid), b(64 * WM_ * WN_);
-  if (a.offsets) hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 1>), g, b, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, BK, ST, SP, 0>), g, b, 0, a.stream, a);
+  if (a.offsets) hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, ST, 1>), g, b, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_i8_tile<BM, BN, WM_, WN_, ST, 0>), g, b, 0, a.stream, a);
   return hipGetLastError();
 }
 

@@ -11,21 +11,20 @@ namespace fbg {
 //   SKINNY: rows x columns, waves, K slices per group, whether 16-byte rows
 //           have a form of their own (else it takes them like any others)
 //   SLIM: rows x columns tile, steps per round, ring slots (16-byte rows)
-//   TILE: rows x columns tile, waves of each, K bytes per step, ring slots,
-//         slices a refill is spread over (16-byte rows)
-#define FBG_I8_CFGS(X)                   \
-  X(0, ANY, 64, 64, 2)                   \
-  X(1, ANY, 32, 64, 4)                   \
-  X(2, SKINNY, 8, 16, 8, 4, true)        \
-  X(3, SKINNY, 16, 16, 8, 4, true)       \
-  X(4, SKINNY, 16, 32, 4, 4, false)      \
-  X(5, TILE, 32, 64, 1, 2, 128, 4, 2)    \
-  X(6, TILE, 64, 64, 2, 2, 128, 4, 2)    \
-  X(7, TILE, 64, 128, 2, 2, 128, 3, 2)   \
-  X(8, TILE, 128, 128, 2, 2, 128, 2, 2)  \
-  X(9, TILE, 128, 256, 2, 2, 128, 3, 2)  \
-  X(10, TILE, 256, 256, 2, 2, 128, 2, 2) \
-  X(11, SLIM, 32, 32, 2, 4)              \
+//   TILE: rows x columns tile, waves of each, ring slots (16-byte rows)
+#define FBG_I8_CFGS(X)              \
+  X(0, ANY, 64, 64, 2)              \
+  X(1, ANY, 32, 64, 4)              \
+  X(2, SKINNY, 8, 16, 8, 4, true)   \
+  X(3, SKINNY, 16, 16, 8, 4, true)  \
+  X(4, SKINNY, 16, 32, 4, 4, false) \
+  X(5, TILE, 32, 64, 1, 2, 4)       \
+  X(6, TILE, 64, 64, 2, 2, 4)       \
+  X(7, TILE, 64, 128, 2, 2, 3)      \
+  X(8, TILE, 128, 128, 2, 2, 2)     \
+  X(9, TILE, 128, 256, 2, 2, 3)     \
+  X(10, TILE, 256, 256, 2, 2, 2)    \
+  X(11, SLIM, 32, 32, 2, 4)         \
   X(12, SLIM, 32, 32, 1, 6)
 
 constexpr int kNumI8Cfgs = 13;
