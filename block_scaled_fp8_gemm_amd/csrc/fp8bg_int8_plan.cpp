@@ -17,9 +17,10 @@ enum Kind { ANY, SKINNY, SLIM, TILE };
 // Least-squares fits in the logarithm to 167 dense shapes of M 1 .. 16384, N
 // 64 .. 8192 and K 256, 1024 and 4096 (configurations 2-12, 16-byte rows; the
 // fits' own deviation is 4-11%) and to 79 of the same range with odd K (any
-// rows; 9-22%), `per_cu` being the count that fits best, not an occupancy.
-// Choosing by it costs 0.9% over the best configuration of each shape on
-// average and 11% at worst (any rows: 1.8% and 18%).
+// rows, contiguous, from before the output stores took any alignment; 9-22%),
+// `per_cu` being the count that fits best, not an occupancy.  Choosing by it
+// costs 1.4% over the best configuration of each shape on average and 13% at
+// worst, as the kernels are now (any rows: 1.9% and 19%).
 struct Cost {
   Kind kind;
   int rows, cols, per_cu, waves;
@@ -70,10 +71,10 @@ int int8_cfg_for(int64_t E, int64_t M, int64_t N, int64_t K, bool fast, int cus)
     // 8 of 256 experts of 512 x 4096: 79 us, 5.8 TB/s, skinny 83, 32 x 64 tile
     // 97; 8 rows to an expert on average 88 us, 105 and 110), and the skinny one
     // while that makes at most two workgroups per compute unit (8 experts of
-    // 1-8 rows: 5.0-5.6 us, slim 6.7, the tile 10.4); over a short K the tile
+    // 1-8 rows: 5.5-6.1 us, slim 8.5, the tile 10.7); over a short K the tile
     // does (of 1536 x 1024: 64 us, slim 79, skinny 71).  Any rows: the
     // 32-column skinny form up to a few workgroups per compute unit (64 rows
-    // over 8 experts of 515 x 776: 4.0 us, the 32 x 64 tile 5.1), else the
+    // over 8 experts of 515 x 776: 3.8 us, the 32 x 64 tile 5.1), else the
     // 32 x 64 tile (256 experts: 27.7 us against 32.9).
     if (!fast) return E * ceil_div(N, 32) <= 4 * cus ? 4 : 1;
     if (K < 2048) return 5;
