@@ -98,7 +98,8 @@ struct Chunk {
 // STREAM: the non-temporal hint, for the tensors that are read once (16384 x
 // 4096: norm to int8 132 -> 113 us, quantiser 36.8 -> 35.3 us in the same
 // shapes); the weights and a gate per channel, which every row reads, go without
-// it (the gate with it: 16384 x 8192 204 against 191 us, 1024 x 4096 10.4 and 9.7).
+// it (the gate with it: 16384 x 8192 202 against 185 us, 1024 x 4096 10.4 and 9.8,
+// 16384 x 256 11.7 and 11.2).
 template <bool STREAM, typename T>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int at, int n) {
   Chunk<T> c;
@@ -270,12 +271,13 @@ __global__ __launch_bounds__(threads(TPR)) void k_block_norm(NormArgs a) {
     for (int i = 0; i < ITEMS; ++i) cx[i] = load_chunk<true>(x, (i * TPR + t) * VE, a.D);
   }
   if (a.gate) {
-    if (a.gate_col == 1 && a.gate_row == 0) {
+    if (a.gate_col == 1) {
+      // Every row reads it.  (Few rows, one chunk per thread in a wave or more:
+      // the hint says nothing there.)
+      const bool shared = (ITEMS > 1 || TPR == 32) && a.gate_row == 0;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) cg[i] = load_chunk<false>(gate, (i * TPR + t) * VE, a.D);
-    } else if (a.gate_col == 1) {
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) cg[i] = load_chunk<true>(gate, (i * TPR + t) * VE, a.D);
+      for (int i = 0; i < ITEMS; ++i)
+        cg[i] = shared ? load_chunk<false>(gate, (i * TPR + t) * VE, a.D) : load_chunk<true>(gate, (i * TPR + t) * VE, a.D);
     } else {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
