@@ -8,7 +8,7 @@
 //
 // All arithmetic is fp32 whatever the tensors' type; r and y are rounded
 // once, and the second norm takes r as it was before its rounding.  The
-// quotients x / s are correctly rounded divisions.
+// codes are those of correctly rounded divisions x / s.
 #include <type_traits>
 
 #include "fp8bg_device.hpp"
@@ -159,8 +159,9 @@ __device__ __forceinline__ void load_weights(const void* w, bool f32, int at, in
 // Int8 codes of VE values with scale s.  EXACT: by division.  Else the
 // quotient is t = v * (1/s) and one correction step, t + (v - t*s) * (1/s):
 // its code is that of the correctly rounded v / s for every bf16 or fp16
-// value in a row with any bf16 or fp16 maximum (checked for all pairs), at 3
-// operations where the division takes about 10.
+// value in a row with any bf16 or fp16 maximum (checked for all pairs), and for
+// the fp32 values of a norm next to every boundary between two codes (checked
+// for random maxima), at 3 operations where the division takes about 10.
 template <bool EXACT, int VE>
 __device__ __forceinline__ void int8_codes(const float (&v)[VE], float s, float y, int8_t (&q)[VE]) {
 #pragma unroll
