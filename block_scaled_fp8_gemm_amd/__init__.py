@@ -85,6 +85,22 @@ def load():
     lib.fbg_block_norm.restype = _int
     lib.fbg_block_norm.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _int, _int, _i64, _i64, _f32,
                                    _f32, _f32, _vp, _i64, _vp, _i64, _vp, _int, _vp]
+    lib.fbg_route_experts.restype = _int
+    lib.fbg_route_experts.argtypes = [_vp, _i64, _int, _i64, _i64, _i64, _int, _vp, _i64, _i64, _int, _int, _f32, _vp,
+                                      _vp, _vp, _vp]
+    lib.fbg_dispatch_tokens.restype = _int
+    lib.fbg_dispatch_tokens.argtypes = [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp,
+                                        _vp, _vp, _vp, _sz, _vp]
+    lib.fbg_dispatch_workspace_size.restype = _sz
+    lib.fbg_dispatch_workspace_size.argtypes = [_i64, _i64, _i64]
+    lib.fbg_combine_experts.restype = _int
+    lib.fbg_combine_experts.argtypes = [_vp, _i64, _int, _i64, _vp, _vp, _vp, _i64, _int, _vp, _i64, _int, _i64, _i64,
+                                        _i64, _vp]
+    lib.fbg_add_adapters.restype = _int
+    lib.fbg_add_adapters.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
+                                     _int, _int, _vp, _sz, _vp]
+    lib.fbg_add_adapters_workspace_size.restype = _sz
+    lib.fbg_add_adapters_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
     lib.fp8_block_gemm_version.restype = _int
     lib.fp8_block_gemm_version.argtypes = []
     _lib = lib
@@ -403,3 +419,67 @@ def block_norm(h: torch.Tensor, x: torch.Tensor = None, post_weight: torch.Tenso
     (r, None).  See fbg_block_norm in include/fp8bg.h."""
     return (_native or _load_native()).block_norm(h, x, post_weight, gate, pre_weight, residual_scale, eps,
                                                   weight_offset, quantize, stream)
+
+
+# ---------------------------------------------------------------------------
+# Every token picks its weights: experts, and low-rank adapters.  Declared in
+# include/fp8bg_tokens.h; checks and calls compiled as above.  Index tensors are
+# int32 and never read by the host.
+# ---------------------------------------------------------------------------
+def route_experts(logits: torch.Tensor, topk: int, score: str = "softmax", bias: torch.Tensor = None, groups: int = 1,
+                  topk_groups: int = 1, group_score: str = "max", renormalize: bool = True, scale: float = 1.0,
+                  mask: torch.Tensor = None, weights: torch.Tensor = None, experts: torch.Tensor = None,
+                  stream: torch.cuda.Stream = None):
+    """The `topk` experts of each row of logits [T,E] (bf16, fp16 or fp32, rows
+    any distance apart) and their weights: (weights [T,topk] float32, experts
+    [T,topk] int32), largest first, of equals the lowest expert.
+
+    score: "softmax" or "sigmoid" of the logits; bias [E] float32 is added to
+    the scores for the choice, not to the weights.  Of `groups` equal runs of
+    experts the topk_groups stay whose largest (group_score "max") or two largest
+    summed ("top2") are largest.  The chosen scores are divided by their sum
+    (renormalize) and times `scale`.  mask [T] bool: such a token gets experts
+    -1 and weights 0.  See fbg_route_experts in include/fp8bg_tokens.h."""
+    return (_native or _load_native()).route_experts(logits, topk, score, bias, groups, topk_groups, group_score,
+                                                     renormalize, scale, mask, weights, experts, stream)
+
+
+def dispatch_tokens(experts: torch.Tensor, E: int, x: torch.Tensor, x_scale: torch.Tensor = None,
+                    first_expert: int = 0, rows: torch.Tensor = None, row_scale: torch.Tensor = None,
+                    stream: torch.cuda.Stream = None):
+    """Copies the rows of x [T,K] (codes or values of 1, 2 or 4 bytes, rows any
+    distance apart) and of x_scale ([T] or [T,S] float32) to each of their
+    experts [T,topk] int32, in the order that grouped_gemm and int8_grouped_gemm
+    want: expert by expert, in one by token.  The E experts held here are
+    first_expert .. first_expert + E - 1; choices of others get no row.
+
+    Returns (rows [T*topk,K], row_scale or None, offsets [E+1] int32, slots
+    [T,topk] int32): slots holds each choice's row, or -1.  Rows behind
+    offsets[E] are left as they are (in `rows` and `row_scale`, if given).  See
+    fbg_dispatch_tokens in include/fp8bg_tokens.h."""
+    return (_native or _load_native()).dispatch_tokens(experts, E, x, x_scale, first_expert, rows, row_scale, stream)
+
+
+def combine_experts(rows: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, base: torch.Tensor = None,
+                    out_dtype=None, out: torch.Tensor = None, stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """out[t] = base[t] + sum_j weights[t,j] * rows[slots[t,j]] in fp32, rounded
+    once: rows [R,D] (bf16, fp16 or fp32) as the grouped products leave them, slots
+    [T,topk] int32 from dispatch_tokens (outside 0 .. R-1: left out), weights
+    [T,topk] float32, base [T,D] of the rows' or the output's type, or None.
+    out_dtype: that of `out`, or else the rows'.  `out` may be base.  See
+    fbg_combine_experts in include/fp8bg_tokens.h."""
+    return (_native or _load_native()).combine_experts(rows, slots, weights, base, out_dtype, out, stream)
+
+
+def add_adapters(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapters: torch.Tensor,
+                 scales: torch.Tensor = None, out: torch.Tensor = None,
+                 stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """Adds low-rank adapters to y [M,N], the output of a projection of x [M,K]
+    that all tokens share: y[m] + scales[a] * B[a] (A[a] x[m]) with
+    a = adapters[m], and y[m] where that is outside 0 .. L-1.
+
+    x, A [L,R,K] and B [L,N,R] bf16 or fp16, y of any output type, adapters [M]
+    int32, scales [L] float32 or None; rows of x, y and `out` any distance apart.
+    In place where out is None; returns the tensor written.  See
+    fbg_add_adapters in include/fp8bg_tokens.h."""
+    return (_native or _load_native()).add_adapters(y, x, A, B, adapters, scales, out, stream)

@@ -11,6 +11,7 @@
 #include "fp8bg.h"
 #include "fp8bg_int8_configs.h"
 #include "fp8bg_internal.h"
+#include "fp8bg_tokens.h"
 
 namespace {
 
@@ -566,4 +567,253 @@ extern "C" int fbg_block_norm(const void* h, int64_t ldh, const void* x, int64_t
   args.weight_offset = weight_offset;
   args.stream = static_cast<hipStream_t>(stream);
   return fbg::launch_block_norm(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}
+
+// ---------------------------------------------------------------------------
+// Operators by which every token picks its weights (fp8bg_tokens.h).
+// ---------------------------------------------------------------------------
+namespace {
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+
+// Whether an output overlaps an input or another output.
+template <int O, int I>
+bool any_overlap(const Range (&out)[O], const Range (&in)[I]) {
+  for (int i = 0; i < O; ++i) {
+    for (const Range& r : in)
+      if (overlaps(out[i].p, out[i].bytes, r.p, r.bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+  }
+  return false;
+}
+
+constexpr int64_t kMaxRouted = 1024;  // experts
+constexpr int64_t kMaxTopk = 64;
+constexpr int64_t kMaxRank = 256;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 35;  // workgroups of a grid of two dimensions
+
+}  // namespace
+
+extern "C" int fbg_route_experts(const void* logits, int64_t ld, int dtype, int64_t T, int64_t E, int64_t topk,
+                                 int score, const float* bias, int64_t groups, int64_t topk_groups, int group_score,
+                                 int renormalize, float scale, const uint8_t* mask, float* weights, int32_t* experts,
+                                 void* stream) {
+  if (T < 0 || E < 0 || topk < 0 || !known_dtype(dtype) || (score != FBG_SCORE_SOFTMAX && score != FBG_SCORE_SIGMOID) ||
+      (group_score != FBG_GROUP_MAX && group_score != FBG_GROUP_TOP2) || groups < 1 || topk_groups < 1 ||
+      topk_groups > groups || E % groups != 0)
+    return FBG_ERROR_INVALID_VALUE;
+  if (T > kMaxExtent || E > kMaxRouted || topk > kMaxTopk || groups > kMaxTopk) return FBG_ERROR_UNSUPPORTED;
+  if (topk > E / groups * topk_groups || (T > 1 && ld < E)) return FBG_ERROR_INVALID_VALUE;
+  if (T <= 1) ld = E;
+  const int64_t es = elem_size(dtype);
+  int64_t bytesL = 0;
+  if (!extent(T, E, ld, es, &bytesL)) return FBG_ERROR_UNSUPPORTED;
+  if (T == 0 || topk == 0) return FBG_SUCCESS;
+  if (!logits || !weights || !experts) return FBG_ERROR_INVALID_VALUE;
+  const Range out[] = {{weights, T * topk * 4}, {experts, T * topk * 4}};
+  const Range in[] = {{logits, bytesL}, {bias, E * 4}, {mask, T}};
+  if (any_overlap(out, in)) return FBG_ERROR_INVALID_VALUE;
+  if (!aligned(logits, (uintptr_t)es) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(experts, 4))
+    return FBG_ERROR_UNSUPPORTED;
+  fbg::RouteArgs args;
+  args.logits = logits;
+  args.bias = bias;
+  args.mask = mask;
+  args.weights = weights;
+  args.experts = experts;
+  args.ld = ld;
+  args.T = (int)T;
+  args.E = (int)E;
+  args.topk = (int)topk;
+  args.groups = topk_groups == groups ? 1 : (int)groups;  // all groups stay: none to choose
+  args.topk_groups = (int)topk_groups;
+  args.dtype = dtype;
+  args.score = score;
+  args.group_score = group_score;
+  args.renormalize = renormalize != 0;
+  args.scale = scale;
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_route(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}
+
+extern "C" size_t fbg_dispatch_workspace_size(int64_t T, int64_t topk, int64_t E) {
+  if (T < 0 || topk < 0 || E < 0 || T > kMaxExtent || topk > kMaxTopk || E > kMaxRouted || T * topk > kMaxExtent)
+    return (size_t)-1;
+  return (size_t)fbg::dispatch_workspace(T * topk, E);
+}
+
+extern "C" int fbg_dispatch_tokens(const int32_t* experts, int64_t T, int64_t topk, int64_t first_expert, int64_t E,
+                                   const void* x, int64_t ldx, int64_t K, int size, const float* x_scale, int64_t S,
+                                   void* rows, int64_t ldrows, float* row_scale, int32_t* offsets, int32_t* slots,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x_scale) S = 0, row_scale = nullptr;
+  if (T < 0 || topk < 0 || E < 0 || K < 0 || S < 0 || (size != 1 && size != 2 && size != 4))
+    return FBG_ERROR_INVALID_VALUE;
+  if (T > kMaxExtent || topk > kMaxTopk || E > kMaxRouted || K > kMaxExtent || S > kMaxExtent || T * topk > kMaxExtent)
+    return FBG_ERROR_UNSUPPORTED;
+  const int64_t n = T * topk;
+  if ((T > 1 && ldx < K) || (n > 1 && ldrows < K)) return FBG_ERROR_INVALID_VALUE;
+  if (T <= 1) ldx = K;
+  if (n <= 1) ldrows = K;
+  int64_t bytesX = 0, bytesR = 0, bytesXs = 0, bytesRs = 0;
+  if (!extent(T, K, ldx, size, &bytesX) || !extent(n, K, ldrows, size, &bytesR) || !extent(T, S, S, 4, &bytesXs) ||
+      !extent(n, S, S, 4, &bytesRs))
+    return FBG_ERROR_UNSUPPORTED;
+  if (!offsets || (n > 0 && (!experts || !slots)) || (n > 0 && bytesX > 0 && (!x || !rows)) || (bytesRs > 0 && !row_scale))
+    return FBG_ERROR_INVALID_VALUE;
+  const int64_t need = fbg::dispatch_workspace(n, E);
+  if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return FBG_ERROR_OUT_OF_MEMORY;
+  if (n == 0) x = nullptr, rows = nullptr;
+  const Range out[] = {{rows, bytesR}, {row_scale, bytesRs}, {offsets, (E + 1) * 4}, {slots, n * 4}, {workspace, need}};
+  const Range in[] = {{experts, n * 4}, {x, bytesX}, {x_scale, bytesXs}};
+  if (any_overlap(out, in)) return FBG_ERROR_INVALID_VALUE;
+  if (!aligned(experts, 4) || !aligned(x, (uintptr_t)size) || !aligned(x_scale, 4) || !aligned(rows, (uintptr_t)size) ||
+      !aligned(row_scale, 4) || !aligned(offsets, 4) || !aligned(slots, 4) || (need > 0 && !aligned(workspace, 4)))
+    return FBG_ERROR_UNSUPPORTED;
+  fbg::DispatchArgs args;
+  args.experts = experts;
+  args.x = static_cast<const uint8_t*>(x);
+  args.x_scale = bytesXs > 0 ? reinterpret_cast<const uint8_t*>(x_scale) : nullptr;
+  args.rows = static_cast<uint8_t*>(rows);
+  args.row_scale = reinterpret_cast<uint8_t*>(row_scale);
+  args.offsets = offsets;
+  args.slots = slots;
+  args.counts = static_cast<int32_t*>(workspace);
+  args.x_pitch = ldx * size;
+  args.row_bytes = K * size;
+  args.rows_pitch = ldrows * size;
+  args.scale_bytes = S * 4;
+  args.first = first_expert;
+  args.blocks = 0;
+  args.T = (int)T;
+  args.topk = (int)topk;
+  args.n = (int)n;
+  args.E = (int)E;
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_dispatch(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}
+
+extern "C" int fbg_combine_experts(const void* rows, int64_t ldrows, int dtype, int64_t R, const int32_t* slots,
+                                   const float* weights, const void* base, int64_t ldbase, int base_dtype, void* out,
+                                   int64_t ldout, int out_dtype, int64_t T, int64_t topk, int64_t D, void* stream) {
+  if (R < 0 || T < 0 || topk < 0 || D < 0 || !known_dtype(dtype) || !known_dtype(out_dtype) ||
+      (base && base_dtype != dtype && base_dtype != out_dtype))
+    return FBG_ERROR_INVALID_VALUE;
+  if (R > kMaxExtent || T > kMaxExtent || topk > kMaxTopk || D > kMaxExtent) return FBG_ERROR_UNSUPPORTED;
+  if ((R > 1 && ldrows < D) || (T > 1 && (ldout < D || (base && ldbase < D)))) return FBG_ERROR_INVALID_VALUE;
+  if (R <= 1) ldrows = D;
+  if (T <= 1) ldbase = ldout = D;
+  const int64_t es = elem_size(dtype), os = elem_size(out_dtype), bs = elem_size(base ? base_dtype : dtype);
+  int64_t bytesR = 0, bytesB = 0, bytesO = 0;
+  if (!extent(R, D, ldrows, es, &bytesR) || !extent(T, D, base ? ldbase : D, bs, &bytesB) ||
+      !extent(T, D, ldout, os, &bytesO) || T * ((D + 255) / 256) > kMaxBlocks)
+    return FBG_ERROR_UNSUPPORTED;
+  if (T == 0 || D == 0) return FBG_SUCCESS;
+  if ((bytesR > 0 && !rows) || !out || (topk > 0 && (!slots || !weights))) return FBG_ERROR_INVALID_VALUE;
+  const bool in_place = base == out && ldbase == ldout && base_dtype == out_dtype;
+  const Range o[] = {{out, bytesO}};
+  const Range in[] = {{rows, bytesR}, {slots, T * topk * 4}, {weights, T * topk * 4}, {in_place ? nullptr : base, bytesB}};
+  if (any_overlap(o, in)) return FBG_ERROR_INVALID_VALUE;
+  if (!aligned(rows, (uintptr_t)es) || !aligned(slots, 4) || !aligned(weights, 4) || !aligned(base, (uintptr_t)bs) ||
+      !aligned(out, (uintptr_t)os))
+    return FBG_ERROR_UNSUPPORTED;
+  fbg::CombineArgs args;
+  args.rows = rows;
+  args.slots = slots;
+  args.weights = weights;
+  args.base = base;
+  args.out = out;
+  args.ldrows = ldrows;
+  args.ldbase = ldbase;
+  args.ldout = ldout;
+  args.R = (int)R;
+  args.T = (int)T;
+  args.topk = (int)topk;
+  args.D = (int)D;
+  args.dtype = dtype;
+  args.out_dtype = out_dtype;
+  args.base_is_out = base && base_dtype == out_dtype;
+  args.splits = 1;
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_combine(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
+}
+
+namespace {
+
+int adapter_pitch(int64_t R) { return (int)((R + 15) / 16 * 16); }
+
+// Bytes of h; false if that overflows.
+bool adapter_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes) {
+  return !__builtin_mul_overflow(M * fbg::adapter_splits(M, K), (int64_t)adapter_pitch(R) * 4, bytes);
+}
+
+}  // namespace
+
+extern "C" size_t fbg_add_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R) {
+  int64_t bytes = 0;
+  if (M < 0 || N < 0 || K < 0 || R < 0 || M > kMaxExtent || N > kMaxExtent || K > kMaxK || R > kMaxRank ||
+      !adapter_workspace(M, K, R, &bytes))
+    return (size_t)-1;
+  return M == 0 || N == 0 || K == 0 || R == 0 ? 0 : (size_t)bytes;
+}
+
+extern "C" int fbg_add_adapters(const void* y, int64_t ldy, const void* x, int64_t ldx, const void* A, const void* B,
+                                const int32_t* adapters, const float* scales, void* out, int64_t ldout, int64_t M,
+                                int64_t N, int64_t K, int64_t R, int64_t L, int dtype, int out_dtype, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || R < 0 || L < 0 || (dtype != FBG_OUT_BF16 && dtype != FBG_OUT_FP16) ||
+      !known_dtype(out_dtype))
+    return FBG_ERROR_INVALID_VALUE;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxK || R > kMaxRank || L > kMaxExtent) return FBG_ERROR_UNSUPPORTED;
+  if (M > 1 && (ldy < N || ldx < K || ldout < N)) return FBG_ERROR_INVALID_VALUE;
+  if (M <= 1) ldy = ldout = N, ldx = K;
+  const int64_t os = elem_size(out_dtype);
+  int64_t bytesX = 0, bytesY = 0, bytesO = 0, bytesA = 0, bytesB = 0, need = 0;
+  if (!extent(M, K, ldx, 2, &bytesX) || !extent(M, N, ldy, os, &bytesY) || !extent(M, N, ldout, os, &bytesO) ||
+      __builtin_mul_overflow(L * R, K * 2, &bytesA) || __builtin_mul_overflow(L * R, N * 2, &bytesB) ||
+      !adapter_workspace(M, K, R, &need) || (M + 15) / 16 * ((N + 127) / 128) > kMaxBlocks)
+    return FBG_ERROR_UNSUPPORTED;
+  if (M == 0 || N == 0) return FBG_SUCCESS;
+  const bool any = K > 0 && R > 0 && L > 0;
+  if (!y || !out || (any && (!x || !A || !B || !adapters))) return FBG_ERROR_INVALID_VALUE;
+  if (!any) x = A = B = nullptr, adapters = nullptr, scales = nullptr, need = 0, L = 0;
+  if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return FBG_ERROR_OUT_OF_MEMORY;
+  const bool in_place = y == out && ldy == ldout;
+  const Range o[] = {{out, bytesO}, {workspace, need}};
+  const Range in[] = {{in_place ? nullptr : y, bytesY}, {x, bytesX}, {A, bytesA}, {B, bytesB}, {adapters, M * 4},
+                      {scales, L * 4}};
+  if (any_overlap(o, in)) return FBG_ERROR_INVALID_VALUE;
+  if (!aligned(y, (uintptr_t)os) || !aligned(out, (uintptr_t)os) || !aligned(x, 2) || !aligned(A, 2) || !aligned(B, 2) ||
+      !aligned(adapters, 4) || !aligned(scales, 4) || (need > 0 && !aligned(workspace, 16)))
+    return FBG_ERROR_UNSUPPORTED;
+  if (!any && in_place) return FBG_SUCCESS;
+  fbg::AdapterArgs args;
+  args.y = y;
+  args.x = x;
+  args.A = A;
+  args.B = B;
+  args.adapters = adapters;
+  args.scales = scales;
+  args.out = out;
+  args.h = static_cast<float*>(workspace);
+  args.ldy = ldy;
+  args.ldx = ldx;
+  args.ldout = ldout;
+  args.M = (int)M;
+  args.N = (int)N;
+  args.K = (int)K;
+  args.R = (int)R;
+  args.L = (int)L;
+  args.pitch = adapter_pitch(R);
+  args.splits = fbg::adapter_splits(M, K);
+  args.in_place = in_place;
+  args.dtype = dtype;
+  args.out_dtype = out_dtype;
+  args.col_blocks = 0;
+  args.stream = static_cast<hipStream_t>(stream);
+  return fbg::launch_add_adapters(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }

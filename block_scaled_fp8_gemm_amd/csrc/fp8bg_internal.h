@@ -38,6 +38,12 @@ int int8_grouped_gemm(const void* A, int64_t lda, const float* a_s, const void* 
                       void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t K,
                       int out_dtype, void* stream);
 
+// Workspace of the two-step operators (fp8bg_experts.hip, fp8bg_adapters.hip):
+// bytes for n choices over E experts; over how many workgroups the adapters'
+// first product splits K.
+int64_t dispatch_workspace(int64_t n, int64_t E);
+int adapter_splits(int64_t M, int64_t K);
+
 #ifdef __HIPCC__
 struct GemmArgs {
   const uint8_t* A;
@@ -111,6 +117,73 @@ struct NormArgs {
   hipStream_t stream;
 };
 hipError_t launch_block_norm(const NormArgs& a);
+
+// Between a router's logits and the grouped products (fp8bg_experts.hip).
+struct RouteArgs {
+  const void* logits;
+  const float* bias;    // [E], or null
+  const uint8_t* mask;  // [T], or null
+  float* weights;
+  int32_t* experts;
+  int64_t ld;
+  int T, E, topk;
+  int groups, topk_groups;
+  int dtype, score, group_score, renormalize;
+  float scale;
+  hipStream_t stream;
+};
+hipError_t launch_route(const RouteArgs& a);
+
+struct DispatchArgs {
+  const int32_t* experts;
+  const uint8_t* x;
+  const uint8_t* x_scale;  // null: none
+  uint8_t* rows;
+  uint8_t* row_scale;
+  int32_t* offsets;
+  int32_t* slots;
+  int32_t* counts;  // workspace
+  int64_t x_pitch, row_bytes, rows_pitch, scale_bytes;  // bytes
+  int64_t first;   // the first expert held here
+  int64_t blocks;  // launch_dispatch sets it
+  int T, topk, n, E;  // n = T * topk
+  hipStream_t stream;
+};
+hipError_t launch_dispatch(DispatchArgs a);
+
+struct CombineArgs {
+  const void* rows;
+  const int32_t* slots;
+  const float* weights;
+  const void* base;  // null: none
+  void* out;
+  int64_t ldrows, ldbase, ldout;
+  int R, T, topk, D;
+  int dtype, out_dtype;
+  int base_is_out;  // base's type: out's, or the rows'
+  int splits;       // workgroups per token (launch_combine sets it)
+  hipStream_t stream;
+};
+hipError_t launch_combine(const CombineArgs& a);
+
+// Low-rank adapters (fp8bg_adapters.hip).
+struct AdapterArgs {
+  const void* y;
+  const void* x;
+  const void* A;
+  const void* B;
+  const int32_t* adapters;
+  const float* scales;  // [L], or null
+  void* out;
+  float* h;  // workspace: [splits][M][pitch]
+  int64_t ldy, ldx, ldout;
+  int M, N, K, R, L;
+  int pitch, splits, in_place;
+  int dtype, out_dtype;
+  int col_blocks;  // launch_add_adapters sets it
+  hipStream_t stream;
+};
+hipError_t launch_add_adapters(const AdapterArgs& a);
 #endif
 
 }  // namespace fbg

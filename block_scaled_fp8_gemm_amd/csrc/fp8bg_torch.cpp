@@ -1,4 +1,4 @@
-// The int8 and row operators for torch tensors: checks of the arguments,
+// The int8, row and token operators for torch tensors: checks of the arguments,
 // allocation of the outputs and the call of the C entry point, in one step.
 //
 // Compiled because these operators take a few microseconds on the GPU at
@@ -21,6 +21,7 @@
 
 #include "fp8bg.h"
 #include "fp8bg_internal.h"
+#include "fp8bg_tokens.h"
 
 namespace {
 
@@ -290,6 +291,181 @@ PyObject* block_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+int64_t integer(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+// Which of two words `o` is.
+int one_of(PyObject* o, const char* name, const char* zero, const char* one) {
+  const char* s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : "";
+  if (!s) throw python_error();
+  if (std::string(s) == zero) return 0;
+  if (std::string(s) == one) return 1;
+  value_error(std::string(name) + " must be \"" + zero + "\" or \"" + one + "\"");
+}
+
+// (logits, topk, score, bias, groups, topk_groups, group_score, renormalize,
+//  scale, mask, weights, experts, stream) -> (weights, experts)
+PyObject* route_experts(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 13);
+  const at::Tensor& logits = matrix(v[0], "logits");
+  const int64_t T = logits.size(0), E = logits.size(1), topk = integer(v[1]);
+  const at::Device dev = logits.device();
+  const int in_code = code(logits.scalar_type(), "logits");
+  const int64_t ld = pitch(logits, "logits", logits.scalar_type(), T, E, dev);
+  if (topk < 0) value_error("topk must not be negative");
+  const int score = one_of(v[2], "score", "softmax", "sigmoid") ? FBG_SCORE_SIGMOID : FBG_SCORE_SOFTMAX;
+  const auto* bias =
+      v[3] == Py_None ? nullptr : static_cast<const float*>(whole(tensor(v[3], "bias"), "bias", at::kFloat, {E}, dev));
+  const int64_t groups = integer(v[4]), topk_groups = integer(v[5]);
+  const int group_score = one_of(v[6], "group_score", "max", "top2") ? FBG_GROUP_TOP2 : FBG_GROUP_MAX;
+  const int renormalize = PyObject_IsTrue(v[7]);
+  const double scale = PyFloat_AsDouble(v[8]);
+  if (PyErr_Occurred()) throw python_error();
+  const uint8_t* mask = nullptr;
+  if (v[9] != Py_None) {
+    const at::Tensor& m = tensor(v[9], "mask");
+    const at::ScalarType type = m.scalar_type() == at::kByte ? at::kByte : at::kBool;
+    mask = static_cast<const uint8_t*>(whole(m, "mask", type, {T}, dev));
+  }
+  const Launch launch(v[12], dev);
+  const at::Tensor w = v[10] == Py_None ? make({T, topk}, at::kFloat, dev) : tensor(v[10], "weights");
+  auto* weights = static_cast<float*>(whole(w, "weights", at::kFloat, {T, topk}, dev));
+  const at::Tensor e = v[11] == Py_None ? make({T, topk}, at::kInt, dev) : tensor(v[11], "experts");
+  auto* experts = static_cast<int32_t*>(whole(e, "experts", at::kInt, {T, topk}, dev));
+  check_status(fbg_route_experts(logits.data_ptr(), ld, in_code, T, E, topk, score, bias, groups, topk_groups,
+                                 group_score, renormalize, (float)scale, mask, weights, experts, launch.get()),
+               "fbg_route_experts");
+  return Py_BuildValue("(NN)", THPVariable_Wrap(w), THPVariable_Wrap(e));
+  END_HANDLE_TH_ERRORS
+}
+
+// (experts, E, x, x_scale, first_expert, rows, row_scale, stream)
+//  -> (rows, row_scale or None, offsets, slots)
+PyObject* dispatch_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 8);
+  const at::Tensor &experts = matrix(v[0], "experts"), &x = matrix(v[2], "x");
+  const int64_t T = experts.size(0), topk = experts.size(1), E = integer(v[1]), K = x.size(1);
+  const at::Device dev = x.device();
+  if (E < 0) value_error("E must not be negative");
+  const auto* ids = static_cast<const int32_t*>(whole(experts, "experts", at::kInt, {T, topk}, dev));
+  const at::ScalarType type = x.scalar_type();
+  const int64_t ldx = pitch(x, "x", type, T, K, dev);
+  const int64_t size = x.element_size();
+  if (size != 1 && size != 2 && size != 4) type_error("x: elements of 1, 2 or 4 bytes expected");
+  const float* x_scale = nullptr;
+  int64_t S = 0;
+  at::DimVector scale_shape;
+  if (v[3] != Py_None) {
+    const at::Tensor& t = tensor(v[3], "x_scale");
+    if (t.dim() != 1 && t.dim() != 2) value_error("x_scale must be [T] or [T, S]");
+    S = t.dim() == 1 ? 1 : t.size(1);
+    scale_shape.push_back(T);
+    if (t.dim() == 2) scale_shape.push_back(S);
+    x_scale = static_cast<const float*>(whole(t, "x_scale", at::kFloat, scale_shape, dev));
+    scale_shape[0] = T * topk;
+  }
+  const int64_t first = integer(v[4]);
+  const size_t need = fbg_dispatch_workspace_size(T, topk, E);
+  if (need == (size_t)-1) check_status(FBG_ERROR_UNSUPPORTED, "fbg_dispatch_tokens");
+  const Launch launch(v[7], dev);
+  const at::Tensor rows = v[5] != Py_None      ? tensor(v[5], "rows")
+                          : type == at::kChar ? make_codes(T * topk, K, dev)
+                                              : make({T * topk, K}, type, dev);
+  const int64_t ldrows = pitch(rows, "rows", type, T * topk, K, dev);
+  at::Tensor row_scale;
+  if (v[3] != Py_None) {
+    row_scale = v[6] == Py_None ? make(scale_shape, at::kFloat, dev) : tensor(v[6], "row_scale");
+    whole(row_scale, "row_scale", at::kFloat, scale_shape, dev);
+  } else if (v[6] != Py_None) {
+    value_error("row_scale needs x_scale");
+  }
+  const at::Tensor offsets = make({E + 1}, at::kInt, dev), slots = make({T, topk}, at::kInt, dev);
+  const at::Tensor work = need ? make({(int64_t)need}, at::kByte, dev) : at::Tensor();
+  check_status(fbg_dispatch_tokens(ids, T, topk, first, E, x.data_ptr(), ldx, K, (int)size, x_scale, S,
+                                   rows.data_ptr(), ldrows,
+                                   row_scale.defined() ? static_cast<float*>(row_scale.data_ptr()) : nullptr,
+                                   static_cast<int32_t*>(offsets.data_ptr()), static_cast<int32_t*>(slots.data_ptr()),
+                                   need ? work.data_ptr() : nullptr, need, launch.get()),
+               "fbg_dispatch_tokens");
+  PyObject* so = row_scale.defined() ? THPVariable_Wrap(row_scale) : Py_NewRef(Py_None);
+  return Py_BuildValue("(NNNN)", THPVariable_Wrap(rows), so, THPVariable_Wrap(offsets), THPVariable_Wrap(slots));
+  END_HANDLE_TH_ERRORS
+}
+
+// (rows, slots, weights, base, out_dtype, out, stream)
+PyObject* combine_experts(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 7);
+  const at::Tensor &rows = matrix(v[0], "rows"), &slots = matrix(v[1], "slots");
+  const int64_t R = rows.size(0), D = rows.size(1), T = slots.size(0), topk = slots.size(1);
+  const at::Device dev = rows.device();
+  const at::ScalarType type = rows.scalar_type();
+  const int in_code = code(type, "rows");
+  const int64_t ldrows = pitch(rows, "rows", type, R, D, dev);
+  const auto* at_slots = static_cast<const int32_t*>(whole(slots, "slots", at::kInt, {T, topk}, dev));
+  const auto* weights =
+      static_cast<const float*>(whole(tensor(v[2], "weights"), "weights", at::kFloat, {T, topk}, dev));
+  const at::ScalarType out_type = v[4] == Py_None ? v[5] == Py_None ? type : tensor(v[5], "out").scalar_type() : dtype_arg(v[4]);
+  const int out_code = code(out_type, "out_dtype");
+  const void* base = nullptr;
+  int64_t ldbase = 0;
+  int base_code = in_code;
+  if (v[3] != Py_None) {
+    const at::Tensor& t = tensor(v[3], "base");
+    const at::ScalarType bt = t.scalar_type();
+    if (bt != type && bt != out_type)
+      type_error(std::string("base: dtype ") + c10::toString(bt) + ", expected " + c10::toString(type) + " or " +
+                 c10::toString(out_type));
+    ldbase = pitch(t, "base", bt, T, D, dev);
+    base = t.data_ptr();
+    base_code = code(bt, "base");
+  }
+  const Launch launch(v[6], dev);
+  const at::Tensor out = v[5] == Py_None ? make({T, D}, out_type, dev) : tensor(v[5], "out");
+  const int64_t ldout = pitch(out, "out", out_type, T, D, dev);
+  check_status(fbg_combine_experts(rows.data_ptr(), ldrows, in_code, R, at_slots, weights, base, ldbase, base_code,
+                                   out.data_ptr(), ldout, out_code, T, topk, D, launch.get()),
+               "fbg_combine_experts");
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// (y, x, A, B, adapters, scales, out, stream)
+PyObject* add_adapters(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 8);
+  const at::Tensor &y = matrix(v[0], "y"), &x = matrix(v[1], "x"), &A = tensor(v[2], "A"), &B = tensor(v[3], "B");
+  if (A.dim() != 3 || B.dim() != 3) value_error("A must be [L, R, K] and B [L, N, R]");
+  const int64_t M = y.size(0), N = y.size(1), K = x.size(1), L = A.size(0), R = A.size(1);
+  const at::Device dev = y.device();
+  const at::ScalarType type = x.scalar_type(), out_type = y.scalar_type();
+  const int in_code = code(type, "x"), out_code = code(out_type, "y");
+  if (in_code == FBG_OUT_FP32) type_error("x: dtype Float, expected BFloat16 or Half");
+  const int64_t ldy = pitch(y, "y", out_type, M, N, dev), ldx = pitch(x, "x", type, M, K, dev);
+  const void* pa = whole(A, "A", type, {L, R, K}, dev);
+  const void* pb = whole(B, "B", type, {L, N, R}, dev);
+  const auto* ids = static_cast<const int32_t*>(whole(tensor(v[4], "adapters"), "adapters", at::kInt, {M}, dev));
+  const auto* scales = v[5] == Py_None
+                           ? nullptr
+                           : static_cast<const float*>(whole(tensor(v[5], "scales"), "scales", at::kFloat, {L}, dev));
+  const size_t need = fbg_add_adapters_workspace_size(M, N, K, R);
+  if (need == (size_t)-1) check_status(FBG_ERROR_UNSUPPORTED, "fbg_add_adapters");
+  const Launch launch(v[7], dev);
+  const at::Tensor out = v[6] == Py_None ? y : tensor(v[6], "out");
+  const int64_t ldout = pitch(out, "out", out_type, M, N, dev);
+  const at::Tensor work = need ? make({(int64_t)need}, at::kByte, dev) : at::Tensor();
+  check_status(fbg_add_adapters(y.data_ptr(), ldy, x.data_ptr(), ldx, pa, pb, ids, scales, out.data_ptr(), ldout, M, N,
+                                K, R, L, in_code, out_code, need ? work.data_ptr() : nullptr, need, launch.get()),
+               "fbg_add_adapters");
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XDECREF(g_error);
@@ -302,6 +478,10 @@ PyMethodDef methods[] = {{"int8_gemm", FAST(int8_gemm), nullptr},
                          {"int8_grouped_gemm", FAST(int8_grouped_gemm), nullptr},
                          {"quantize_tokens", FAST(quantize_tokens), nullptr},
                          {"block_norm", FAST(block_norm), nullptr},
+                         {"route_experts", FAST(route_experts), nullptr},
+                         {"dispatch_tokens", FAST(dispatch_tokens), nullptr},
+                         {"combine_experts", FAST(combine_experts), nullptr},
+                         {"add_adapters", FAST(add_adapters), nullptr},
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8bg_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
