@@ -775,7 +775,7 @@ extern "C" int fbg_add_adapters(const void* y, int64_t ldy, const void* x, int64
   int64_t bytesX = 0, bytesY = 0, bytesO = 0, bytesA = 0, bytesB = 0, need = 0;
   if (!extent(M, K, ldx, 2, &bytesX) || !extent(M, N, ldy, os, &bytesY) || !extent(M, N, ldout, os, &bytesO) ||
       __builtin_mul_overflow(L * R, K * 2, &bytesA) || __builtin_mul_overflow(L * R, N * 2, &bytesB) ||
-      !adapter_workspace(M, K, R, &need) || (M + 15) / 16 * ((N + 127) / 128) > kMaxBlocks)
+      !adapter_workspace(M, K, R, &need) || (M + 15) / 16 * ((N + 63) / 64) > kMaxBlocks)
     return FBG_ERROR_UNSUPPORTED;
   if (M == 0 || N == 0) return FBG_SUCCESS;
   const bool any = K > 0 && R > 0 && L > 0;
@@ -813,7 +813,7 @@ extern "C" int fbg_add_adapters(const void* y, int64_t ldy, const void* x, int64
   args.in_place = in_place;
   args.dtype = dtype;
   args.out_dtype = out_dtype;
-  args.col_blocks = 0;
+  args.workers = args.cols = args.col_blocks = 0;
   args.stream = static_cast<hipStream_t>(stream);
   return fbg::launch_add_adapters(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }
