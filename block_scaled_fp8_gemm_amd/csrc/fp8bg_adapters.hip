@@ -16,11 +16,21 @@ namespace {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr int64_t kGridX = 1 << 20;
-inline dim3 wide_grid(int64_t blocks) {
-  return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+constexpr int kMaxSplits = 4;
+constexpr int kFewTiles = 64;  // tiles of 16 tokens
+
+// Grids: splits of K or blocks of columns along x, tiles of 16 tokens along y
+// and, past kGridY of them, z; with several workers per tile they stand along z.
+// (No flat index: its 64-bit divisions took longer than a decode tile's loads.)
+constexpr int kGridY = 1 << 15;
+inline dim3 tile_grid(int64_t x, int64_t tiles, int workers) {
+  const int64_t y = tiles < kGridY ? tiles : kGridY;
+  return dim3((unsigned)x, (unsigned)y, workers > 1 ? (unsigned)workers : (unsigned)((tiles + y - 1) / y));
 }
-__device__ __forceinline__ int64_t block_of_grid() { return (int64_t)blockIdx.y * kGridX + blockIdx.x; }
+__device__ __forceinline__ int64_t first_token(int workers) {
+  return ((workers > 1 ? 0 : (int64_t)blockIdx.z * kGridY) + blockIdx.y) * 16;
+}
+__device__ __forceinline__ int worker_of(int workers) { return workers > 1 ? blockIdx.z : 0; }
 
 template <typename T> struct Vec8;
 template <> struct Vec8<__bf16> { typedef v8bf type; };
@@ -45,8 +55,8 @@ __device__ __forceinline__ void load_some(const T* row, int at, int n, T (&v)[N]
 }
 template <typename T>
 __device__ __forceinline__ typename Vec8<T>::type load8(const T* row, int at, int n) {
-  T v[8];
-  load_some(row, at, n, v);
+  T v[8] = {};
+  if (at < n) load_some(row, at, n, v);
   typename Vec8<T>::type r;
   __builtin_memcpy(&r, v, sizeof(r));
   return r;
@@ -59,37 +69,33 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs& a, int64_t m) {
 }
 
 // The passes of a tile of 16 tokens: one for each different adapter among them.
-// Worker `first` of `count` calls pass(adapter) for its share.
+// One worker does them all; of several (as many as a tile can have passes)
+// number `worker` does the one of that number.
 template <typename F>
-__device__ __forceinline__ void for_passes(int id, int first, int count, const F& pass) {
+__device__ __forceinline__ void for_passes(int id, int worker, int workers, const F& pass) {
   uint64_t todo = __ballot(id >= 0) & 0xffff;
   for (int p = 0; todo; ++p) {
     const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     todo &= ~__ballot(id == cur);
-    if (p % count == first) pass(cur);
+    if (workers == 1 || p == worker) pass(cur);
   }
 }
 
 // h of 16 tokens over one slice of K for one adapter of theirs, or each in
-// turn; the four waves split the slice, and their sums meet in LDS.  RT tiles
+// turn; the W waves split the slice, and their sums meet in LDS.  RT tiles
 // of 16 ranks at a time; the loads of U steps are in flight together.
-template <typename T, int RT>
-__global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
+template <typename T, int RT, int W>
+__global__ __launch_bounds__(64 * W) void k_shrink(AdapterArgs a) {
   constexpr int U = RT == 1 ? 8 : 4;
   typedef typename Vec8<T>::type V;
-  __shared__ v4f part[RT][4][64];  // [tile of 16 ranks][wave][lane]
-  int64_t block = block_of_grid();
-  const int split = (int)(block % a.splits);
-  block /= a.splits;
-  const int worker = (int)(block % a.workers);
-  const int64_t m0 = block / a.workers * 16;
+  __shared__ v4f part[RT][W][64];  // [tile of 16 ranks][wave][lane]
+  const int split = blockIdx.x, worker = worker_of(a.workers);
+  const int64_t m0 = first_token(a.workers);
   if (m0 >= a.M) return;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
   const int id = adapter_of(a, m0 + j);
-  // A wave's share: whole steps of 32.
-  const int steps = (a.K + 31) / 32, per = (steps + a.splits * 4 - 1) / (a.splits * 4);
-  const int first = (split * 4 + w) * per * 32;
-  const int last = first + per * 32 < a.K ? first + per * 32 : a.K;
+  const int first = (split * W + w) * a.share;
+  const int last = first + a.share < a.K ? first + a.share : a.K;
   float* h = a.h + ((int64_t)split * a.M + m0 + j) * a.pitch;
   for_passes(id, worker, a.workers, [&](int cur) {
     const bool mine = id == cur;
@@ -111,6 +117,7 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
 #pragma unroll
           for (int i = 0; i < RT; ++i) __builtin_memcpy(&af[u][i], row[i] + k + 32 * u + 8 * g, 16);
         }
+        __builtin_amdgcn_sched_barrier(0);  // all loads before the first use of one
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -128,7 +135,7 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
         const int r = r0 + 16 * w + 4 * g;
         v4f s = part[w][0][lane];
 #pragma unroll
-        for (int i = 1; i < 4; ++i) s += part[w][i][lane];
+        for (int i = 1; i < W; ++i) s += part[w][i][lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (r + i >= a.R) s[i] = 0.0f;
@@ -139,109 +146,211 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
   });
 }
 
-// 16 tokens by blocks of 64 columns per wave.  Row i of the first operand's
-// tile t is column 32 (t / 2) + 8 (i / 4) + 4 (t % 2) + i % 4 of the block, so that a
-// lane's results are of one token and 8 columns next to one another, twice.  h stays in
-// fp32: the fp32 MFMA takes it and the weights as they are.  Each token
-// belongs to one pass, which alone writes its row; the first worker writes the
-// rows without an adapter.  DEEP: more than 64 ranks, h read again for each
-// block of columns.
-template <typename T, typename O, int RT, bool DEEP>
+// How k_expand reads the ranks of a weight row: RT * 16 of them in whole chunks,
+// up to 16 in chunks of four, or any number one by one.
+enum Ranks { kWhole, kFours, kAny };
+
+// 16 tokens by blocks of 64 columns, four blocks next to one another on the
+// four waves.  Row i of the first operand's tile t is column 32 (t / 2) + 8 (i / 4) +
+// 4 (t % 2) + i % 4 of the block, so that a lane's results are of one token and 8
+// columns next to one another, twice.  h stays in fp32: the fp32 MFMA takes it
+// and the weights as they are.  Each token belongs to one pass, which alone
+// writes its row; the first worker writes the rows without an adapter.  DEEP:
+// the ranks in steps of 16 RT, h read again for each block of columns.
+//
+// The loads of the next block are in flight while one is computed: they stay
+// raw dwords until they are used, and have no branch between lanes (a lane of
+// another token reads the row of one that is meant), since the compiler waits
+// for a load where it unpacks its value or where the lanes meet again.  A last
+// block that N cuts goes element by element.
+template <typename T, typename O, int RT, bool DEEP, Ranks RANKS>
 __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
-  int64_t block = block_of_grid();
-  const int64_t n_first = block % a.col_blocks * a.cols;
-  block /= a.col_blocks;
-  const int worker = (int)(block % a.workers);
+  constexpr int YC = 2 * (int)sizeof(O) / 4;  // 16-byte chunks of 8 outputs
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+  typedef O O8 __attribute__((ext_vector_type(8)));
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int64_t m0 = (block / a.workers * 4 + (threadIdx.x >> 6)) * 16;
-  if (m0 >= a.M) return;  // whole waves, which meet at no barrier
-  const int64_t n_last = n_first + a.cols < a.N ? n_first + a.cols : a.N;
-  const int64_t m = m0 + j;
-  const int id = adapter_of(a, m);
-  const O* yrow = reinterpret_cast<const O*>(a.y) + m * a.ldy;
-  O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
-  const auto store = [&](int64_t n, const O (&v)[8]) {
-    if (n + 8 <= a.N) {
-      __builtin_memcpy(orow + n, v, sizeof(v));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n + i < a.N) orow[n + i] = v[i];
-    }
+  const int worker = worker_of(a.workers);
+  const int64_t m0 = first_token(a.workers), n_block = (int64_t)blockIdx.x * a.cols;
+  const int64_t n_first = n_block + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 64, n_end = n_block + a.cols;
+  if (m0 >= a.M || n_first >= a.N) return;  // whole waves, which meet at no barrier
+  const int64_t n_last = n_end < a.N ? n_end : a.N;
+  const int id = adapter_of(a, m0 + j);
+  const int column = 8 * (j >> 2) + (j & 3);
+  struct Weights {
+    U2 v[RT][4];
   };
-  const auto load_h = [&](int r0, float scale, v4f (&h)[RT]) {
+  struct Outputs {
+    U4 v[2][YC];
+  };
+  const auto load_y = [&](const O* row, int64_t n0) {
+    Outputs y;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      h[i] = v4f{};
-      if (r0 + 16 * i < a.pitch) {
-        const float* p = a.h + m * a.pitch + r0 + 16 * i + 4 * g;
-        for (int s = 0; s < a.splits; ++s) h[i] += *reinterpret_cast<const v4f*>(p + (int64_t)s * a.M * a.pitch);
-        h[i] *= scale;
-      }
-    }
+    for (int q = 0; q < 2; ++q) __builtin_memcpy(y.v[q], row + n0 + 32 * q + 8 * g, sizeof(y.v[q]));
+    return y;
   };
   for_passes(id, worker, a.workers, [&](int cur) {
+    const uint64_t meant = __ballot(id == cur);
     const bool mine = id == cur;
-    const float scale = a.scales ? a.scales[cur] : 1.0f;
+    const int64_t m = m0 + (mine ? j : __builtin_ctzll(meant));
+    const O* yrow = reinterpret_cast<const O*>(a.y) + m * a.ldy;
+    O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
     const T* B = reinterpret_cast<const T*>(a.B) + (int64_t)cur * a.N * a.R;
-    v4f h[RT] = {};
-    if (!DEEP && mine) load_h(0, scale, h);
-    for (int64_t n0 = n_first; n0 < n_last; n0 += 64) {
-      O y[2][8];
-      if (mine) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) load_some(yrow, (int)n0 + 32 * q + 8 * g, a.N, y[q]);
-      }
-      const T* row[4];
+    const float* hrow = a.h + m * a.pitch + 4 * g;
+    const int64_t h_split = (int64_t)a.M * a.pitch;
+    const auto load_b = [&](int64_t n0, int r0) {
+      Weights b;
+      const T* base = B + n0 * a.R;
+      const int most = a.N - n0 < 64 ? (int)(a.N - n0) - 1 : 63;  // a column past the last one: the last one's
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int64_t n = n0 + 32 * (t >> 1) + 8 * (j >> 2) + 4 * (t & 1) + (j & 3);
-        row[t] = B + (n < a.N ? n : a.N - 1) * a.R;
-      }
-      v4f acc[4] = {};
-      for (int r0 = 0; r0 < (DEEP ? a.R : 1); r0 += 16 * RT) {
-        if (DEEP && mine) load_h(r0, scale, h);
+        const int n = 32 * (t >> 1) + 4 * (t & 1) + column;
+        const T* row = base + (n < most ? n : most) * a.R;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          T b[4][4];
+          const int r = r0 + 16 * i + 4 * g;
+          if constexpr (RANKS == kAny) {
+            T4 v;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) load_some(row[t], r0 + 16 * i + 4 * g, a.R, b[t]);
+            for (int k = 0; k < 4; ++k) v[k] = row[r + k < a.R ? r + k : a.R - 1];
+            b.v[i][t] = __builtin_bit_cast(U2, v);
+          } else {
+            __builtin_memcpy(&b.v[i][t], row + (RANKS == kWhole || r < a.R ? r : 0), 8);
+          }
+        }
+      }
+      return b;
+    };
+    const auto load_h = [&](int r0, float scale, v4f (&h)[RT]) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        v4f part[kMaxSplits];
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+          if (s < a.splits) part[s] = *reinterpret_cast<const v4f*>(hrow + s * h_split + r0 + 16 * i);
+        h[i] = part[0];
+#pragma unroll
+        for (int s = 1; s < kMaxSplits; ++s)
+          if (s < a.splits) h[i] += part[s];
+        h[i] *= scale;
+      }
+    };
+    const auto multiply = [&](const Weights& b, int r0, const v4f (&h)[RT], v4f (&acc)[4]) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float w[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const T4 v = __builtin_bit_cast(T4, b.v[i][t]);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)b[t][u], h[i][u], acc[t], 0, 0, 0);
+            w[t][u] = RANKS == kWhole || r0 + 16 * i + 4 * g + u < a.R ? (float)v[u] : 0.0f;
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t][u], h[i][u], acc[t], 0, 0, 0);
       }
-      // A lane's results are of its own token: those of the others' adapters,
-      // which may hold infinities, go nowhere.
-      if (mine) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int64_t n = n0 + 32 * q + 8 * g;
-          if (n >= a.N) continue;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[q][i] = (O)((float)y[q][i] + acc[2 * q + (i >> 2)][i & 3]);
-          store(n, y[q]);
+    };
+    const float scale = a.scales ? a.scales[cur] : 1.0f;
+    v4f h[RT];
+    // The products of one block, the weights of its first ranks in hand.
+    const auto block = [&](int64_t n0, const Weights& b, v4f (&acc)[4]) {
+      if constexpr (DEEP) {
+        Weights now = b;
+        for (int r0 = 0; r0 < a.R; r0 += 16 * RT) {
+          load_h(r0, scale, h);
+          const Weights then = load_b(n0, r0 + 16 * RT < a.R ? r0 + 16 * RT : r0);
+          multiply(now, r0, h, acc);
+          now = then;
         }
+      } else {
+        multiply(b, 0, h, acc);
       }
+    };
+    Weights b = load_b(n_first, 0);
+    Outputs y;
+    int64_t n0 = n_first;
+    if (n0 + 64 <= n_last) y = load_y(yrow, n0);
+    if constexpr (!DEEP) load_h(0, scale, h);
+    // A lane's results are of its own token: those of the others' adapters,
+    // which may hold infinities, go nowhere.
+    for (; n0 + 64 <= n_last; n0 += 256) {
+      const int64_t next = n0 + 320 <= n_last ? n0 + 256 : n0;
+      const Weights b_next = load_b(next, 0);
+      const Outputs y_next = load_y(yrow, next);
+      __builtin_amdgcn_sched_barrier(0);  // on their way before the products
+      v4f acc[4] = {};
+      block(n0, b, acc);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        O8 v = __builtin_bit_cast(O8, y.v[q]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (O)((float)v[i] + acc[2 * q + (i >> 2)][i & 3]);
+        if (mine) __builtin_memcpy(orow + n0 + 32 * q + 8 * g, &v, sizeof(v));
+      }
+      b = b_next;
+      y = y_next;
+    }
+    if (n0 < n_last) {
+      O v[2][8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t n = n0 + 32 * q + 8 * g + i;
+          v[q][i] = yrow[n < a.N ? n : a.N - 1];
+        }
+      if (n0 > n_first) b = load_b(n0, 0);
+      v4f acc[4] = {};
+      block(n0, b, acc);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t n = n0 + 32 * q + 8 * g + i;
+          if (mine && n < a.N) orow[n] = (O)((float)v[q][i] + acc[2 * q + (i >> 2)][i & 3]);
+        }
     }
   });
-  if (worker == 0 && !a.in_place && m < a.M && id < 0)
-    for (int64_t n = n_first + 8 * g; n < n_last; n += 32) {
-      O y[8];
-      load_some(yrow, (int)n, a.N, y);
-      store(n, y);
+  const int64_t m = m0 + j;
+  if (worker == 0 && !a.in_place && m < a.M && id < 0) {
+    const O* yrow = reinterpret_cast<const O*>(a.y) + m * a.ldy;
+    O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
+    for (int64_t n0 = n_first; n0 < n_last; n0 += 256) {
+      if (n0 + 64 <= n_last) {
+        const Outputs y = load_y(yrow, n0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) __builtin_memcpy(orow + n0 + 32 * q + 8 * g, y.v[q], sizeof(y.v[q]));
+      } else {
+        for (int64_t n = n0 + 8 * g; n < n0 + 64; n += 32)
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) orow[n + i] = yrow[n + i];
+      }
     }
+  }
 }
 
 template <typename T, typename O>
 void expand(const AdapterArgs& a, dim3 g) {
   const dim3 b(256);
-  if (a.R <= 16) hipLaunchKernelGGL((k_expand<T, O, 1, false>), g, b, 0, a.stream, a);
-  else if (a.R <= 32) hipLaunchKernelGGL((k_expand<T, O, 2, false>), g, b, 0, a.stream, a);
-  else if (a.R <= 64) hipLaunchKernelGGL((k_expand<T, O, 4, false>), g, b, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_expand<T, O, 4, true>), g, b, 0, a.stream, a);
+  if (a.R % 16 == 0) {
+    if (a.R == 16) hipLaunchKernelGGL((k_expand<T, O, 1, false, kWhole>), g, b, 0, a.stream, a);
+    else if (a.R == 32) hipLaunchKernelGGL((k_expand<T, O, 2, false, kWhole>), g, b, 0, a.stream, a);
+    else if (a.R == 64) hipLaunchKernelGGL((k_expand<T, O, 4, false, kWhole>), g, b, 0, a.stream, a);
+    else hipLaunchKernelGGL((k_expand<T, O, 1, true, kWhole>), g, b, 0, a.stream, a);
+  } else if (a.R < 16 && a.R % 4 == 0) {
+    hipLaunchKernelGGL((k_expand<T, O, 1, false, kFours>), g, b, 0, a.stream, a);
+  } else {
+    hipLaunchKernelGGL((k_expand<T, O, 1, true, kAny>), g, b, 0, a.stream, a);
+  }
+}
+
+template <typename T, int RT>
+void shrink(const AdapterArgs& a, dim3 g, bool wide) {
+  if (wide) hipLaunchKernelGGL((k_shrink<T, RT, 16>), g, dim3(1024), 0, a.stream, a);
+  else hipLaunchKernelGGL((k_shrink<T, RT, 4>), g, dim3(256), 0, a.stream, a);
 }
 
 template <typename T>
@@ -249,21 +358,24 @@ hipError_t add(AdapterArgs a) {
   const int64_t tiles = ((int64_t)a.M + 15) / 16;
   // Few tokens: a worker for each adapter that a tile may hold.  Many: the
   // tiles cover the device, and their tokens come in runs.
-  a.workers = tiles > 64 ? 1 : a.M < 16 ? a.M : 16;
+  const bool few = tiles <= kFewTiles;
+  a.workers = !few ? 1 : a.M < 16 ? a.M : 16;
   if (a.R > 0 && a.L > 0 && a.K > 0) {
-    const dim3 g = wide_grid(tiles * a.workers * a.splits), b(256);
-    if (a.R <= 16) hipLaunchKernelGGL((k_shrink<T, 1>), g, b, 0, a.stream, a);
-    else if (a.R <= 32) hipLaunchKernelGGL((k_shrink<T, 2>), g, b, 0, a.stream, a);
-    else hipLaunchKernelGGL((k_shrink<T, 4>), g, b, 0, a.stream, a);
+    const dim3 g = tile_grid(a.splits, tiles, a.workers);
+    const int waves = a.splits * (few ? 16 : 4);
+    a.share = ((a.K + 31) / 32 + waves - 1) / waves * 32;  // a wave's: whole steps of 32
+    if (a.R <= 16) shrink<T, 1>(a, g, few);
+    else if (a.R <= 32) shrink<T, 2>(a, g, few);
+    else shrink<T, 4>(a, g, few);
   } else {
     a.L = 0;  // no adapter at all
   }
-  const int64_t groups = (tiles + 3) / 4 * a.workers, blocks = ((int64_t)a.N + 63) / 64;
-  int64_t per = groups * blocks / 2048;
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
-  a.cols = (int)per * 64;
-  a.col_blocks = (int)((blocks + per - 1) / per);
-  const dim3 g = wide_grid(groups * a.col_blocks);
+  // Blocks of columns one after the other where there are many tokens.
+  const int64_t blocks = ((int64_t)a.N + 255) / 256;
+  int64_t per = tiles * a.workers * blocks / 2048;
+  per = per < 1 ? 1 : per > 4 ? 4 : per;
+  a.cols = (int)per * 256;
+  const dim3 g = tile_grid((blocks + per - 1) / per, tiles, a.workers);
   switch (a.out_dtype) {
     case kOutBF16: expand<T, __bf16>(a, g); break;
     case kOutFP16: expand<T, _Float16>(a, g); break;
@@ -276,10 +388,11 @@ hipError_t add(AdapterArgs a) {
 
 // How many workgroups split K: enough that few tokens still cover the device.
 int adapter_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + 15) / 16, most = (K + 511) / 512;
-  int64_t s = 512 / (tiles > 0 ? tiles : 1);
-  s = s < most ? s : most;
-  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
+  const int64_t tiles = (M + 15) / 16;
+  int64_t most = tiles <= kFewTiles ? (K + 1023) / 1024 : (K + 511) / 512;
+  most = most < kMaxSplits ? most : kMaxSplits;
+  const int64_t s = 512 / (tiles > 0 ? tiles : 1);
+  return (int)(s < 1 ? 1 : s < most ? s : most);
 }
 
 hipError_t launch_add_adapters(const AdapterArgs& a) {

@@ -813,7 +813,7 @@ extern "C" int fbg_add_adapters(const void* y, int64_t ldy, const void* x, int64
   args.in_place = in_place;
   args.dtype = dtype;
   args.out_dtype = out_dtype;
-  args.workers = args.cols = args.col_blocks = 0;
+  args.workers = args.share = args.cols = 0;
   args.stream = static_cast<hipStream_t>(stream);
   return fbg::launch_add_adapters(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }

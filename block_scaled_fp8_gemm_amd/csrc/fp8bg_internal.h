@@ -180,7 +180,7 @@ struct AdapterArgs {
   int M, N, K, R, L;
   int pitch, splits, in_place;
   int dtype, out_dtype;
-  int workers, cols, col_blocks;  // launch_add_adapters sets them
+  int workers, share, cols;  // launch_add_adapters sets them
   hipStream_t stream;
 };
 hipError_t launch_add_adapters(const AdapterArgs& a);
