@@ -82,10 +82,11 @@ __device__ __forceinline__ void for_passes(int id, int worker, int workers, cons
 }
 
 // h of 16 tokens over one slice of K for one adapter of theirs, or each in
-// turn; the W waves split the slice, and their sums meet in LDS.  RT tiles
+// turn; the waves split the slice, and their sums meet in LDS.  RT tiles
 // of 16 ranks at a time; the loads of U steps are in flight together.
-template <typename T, int RT, int W>
-__global__ __launch_bounds__(64 * W) void k_shrink(AdapterArgs a) {
+template <typename T, int RT>
+__global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
+  constexpr int W = 4;
   constexpr int U = RT == 1 ? 8 : 4;
   typedef typename Vec8<T>::type V;
   __shared__ v4f part[RT][W][64];  // [tile of 16 ranks][wave][lane]
@@ -123,6 +124,20 @@ __global__ __launch_bounds__(64 * W) void k_shrink(AdapterArgs a) {
 #pragma unroll
           for (int i = 0; i < RT; ++i) acc[i] = mfma32(af[u][i], xf[u], acc[i]);
       }
+      for (; k + 64 <= last; k += 64) {
+        V xf[2], af[2][RT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          __builtin_memcpy(&xf[u], x + k + 32 * u + 8 * g, 16);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) __builtin_memcpy(&af[u][i], row[i] + k + 32 * u + 8 * g, 16);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[i] = mfma32(af[u][i], xf[u], acc[i]);
+      }
       for (; k < last; k += 32) {
         const V xf = load8(x, k + 8 * g, a.K);
 #pragma unroll
@@ -146,9 +161,10 @@ __global__ __launch_bounds__(64 * W) void k_shrink(AdapterArgs a) {
   });
 }
 
-// How k_expand reads the ranks of a weight row: RT * 16 of them in whole chunks,
-// up to 16 in chunks of four, or any number one by one.
-enum Ranks { kWhole, kFours, kAny };
+// How k_expand reads the ranks of a weight row: all of RT * 16 in chunks of four,
+// any number from four on in such chunks (the last one taken from the row's
+// end and shifted), or fewer than four one by one.
+enum Ranks { kWhole, kPart, kTiny };
 
 // 16 tokens by blocks of 64 columns, four blocks next to one another on the
 // four waves.  Row i of the first operand's tile t is column 32 (t / 2) + 8 (i / 4) +
@@ -210,13 +226,13 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const int r = r0 + 16 * i + 4 * g;
-          if constexpr (RANKS == kAny) {
+          if constexpr (RANKS == kTiny) {
             T4 v;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = row[r + k < a.R ? r + k : a.R - 1];
+            for (int k = 0; k < 4; ++k) v[k] = row[k < a.R ? k : 0];
             b.v[i][t] = __builtin_bit_cast(U2, v);
           } else {
-            __builtin_memcpy(&b.v[i][t], row + (RANKS == kWhole || r < a.R ? r : 0), 8);
+            __builtin_memcpy(&b.v[i][t], row + (RANKS == kWhole || r < a.R - 4 ? r : a.R - 4), 8);
           }
         }
       }
@@ -242,10 +258,17 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
         float w[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const T4 v = __builtin_bit_cast(T4, b.v[i][t]);
+          uint64_t bits = __builtin_bit_cast(uint64_t, b.v[i][t]);
+          const int r = r0 + 16 * i + 4 * g;
+          if constexpr (RANKS == kPart) {  // zeros come in behind the last rank
+            const int past = r > a.R - 4 ? r - (a.R - 4) : 0;
+            bits = past < 4 ? bits >> (16 * past) : 0;
+          } else if constexpr (RANKS == kTiny) {
+            bits = r == 0 ? bits & ((1ull << (16 * a.R)) - 1) : 0;
+          }
+          const T4 v = __builtin_bit_cast(T4, bits);
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            w[t][u] = RANKS == kWhole || r0 + 16 * i + 4 * g + u < a.R ? (float)v[u] : 0.0f;
+          for (int u = 0; u < 4; ++u) w[t][u] = (float)v[u];
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -277,9 +300,12 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
     // A lane's results are of its own token: those of the others' adapters,
     // which may hold infinities, go nowhere.
     for (; n0 + 64 <= n_last; n0 += 256) {
-      const int64_t next = n0 + 320 <= n_last ? n0 + 256 : n0;
-      const Weights b_next = load_b(next, 0);
-      const Outputs y_next = load_y(yrow, next);
+      Weights b_next;
+      Outputs y_next;
+      if (n0 + 320 <= n_last) {
+        b_next = load_b(n0 + 256, 0);
+        y_next = load_y(yrow, n0 + 256);
+      }
       __builtin_amdgcn_sched_barrier(0);  // on their way before the products
       v4f acc[4] = {};
       block(n0, b, acc);
@@ -340,17 +366,13 @@ void expand(const AdapterArgs& a, dim3 g) {
     else if (a.R == 32) hipLaunchKernelGGL((k_expand<T, O, 2, false, kWhole>), g, b, 0, a.stream, a);
     else if (a.R == 64) hipLaunchKernelGGL((k_expand<T, O, 4, false, kWhole>), g, b, 0, a.stream, a);
     else hipLaunchKernelGGL((k_expand<T, O, 1, true, kWhole>), g, b, 0, a.stream, a);
-  } else if (a.R < 16 && a.R % 4 == 0) {
-    hipLaunchKernelGGL((k_expand<T, O, 1, false, kFours>), g, b, 0, a.stream, a);
+  } else if (a.R < 4) {
+    hipLaunchKernelGGL((k_expand<T, O, 1, false, kTiny>), g, b, 0, a.stream, a);
+  } else if (a.R < 16) {
+    hipLaunchKernelGGL((k_expand<T, O, 1, false, kPart>), g, b, 0, a.stream, a);
   } else {
-    hipLaunchKernelGGL((k_expand<T, O, 1, true, kAny>), g, b, 0, a.stream, a);
+    hipLaunchKernelGGL((k_expand<T, O, 1, true, kPart>), g, b, 0, a.stream, a);
   }
-}
-
-template <typename T, int RT>
-void shrink(const AdapterArgs& a, dim3 g, bool wide) {
-  if (wide) hipLaunchKernelGGL((k_shrink<T, RT, 16>), g, dim3(1024), 0, a.stream, a);
-  else hipLaunchKernelGGL((k_shrink<T, RT, 4>), g, dim3(256), 0, a.stream, a);
 }
 
 template <typename T>
@@ -362,11 +384,11 @@ hipError_t add(AdapterArgs a) {
   a.workers = !few ? 1 : a.M < 16 ? a.M : 16;
   if (a.R > 0 && a.L > 0 && a.K > 0) {
     const dim3 g = tile_grid(a.splits, tiles, a.workers);
-    const int waves = a.splits * (few ? 16 : 4);
-    a.share = ((a.K + 31) / 32 + waves - 1) / waves * 32;  // a wave's: whole steps of 32
-    if (a.R <= 16) shrink<T, 1>(a, g, few);
-    else if (a.R <= 32) shrink<T, 2>(a, g, few);
-    else shrink<T, 4>(a, g, few);
+    const dim3 b(256);
+    a.share = ((a.K + 31) / 32 + a.splits * 4 - 1) / (a.splits * 4) * 32;  // a wave's: whole steps of 32
+    if (a.R <= 16) hipLaunchKernelGGL((k_shrink<T, 1>), g, b, 0, a.stream, a);
+    else if (a.R <= 32) hipLaunchKernelGGL((k_shrink<T, 2>), g, b, 0, a.stream, a);
+    else hipLaunchKernelGGL((k_shrink<T, 4>), g, b, 0, a.stream, a);
   } else {
     a.L = 0;  // no adapter at all
   }
@@ -389,9 +411,9 @@ hipError_t add(AdapterArgs a) {
 // How many workgroups split K: enough that few tokens still cover the device.
 int adapter_splits(int64_t M, int64_t K) {
   const int64_t tiles = (M + 15) / 16;
-  int64_t most = tiles <= kFewTiles ? (K + 1023) / 1024 : (K + 511) / 512;
+  int64_t most = (K + 255) / 256;
   most = most < kMaxSplits ? most : kMaxSplits;
-  const int64_t s = 512 / (tiles > 0 ? tiles : 1);
+  const int64_t s = 2048 / (tiles > 0 ? tiles : 1);
   return (int)(s < 1 ? 1 : s < most ? s : most);
 }
 
