@@ -90,9 +90,7 @@ def load():
                                       _vp, _vp, _vp]
     lib.fbg_dispatch_tokens.restype = _int
     lib.fbg_dispatch_tokens.argtypes = [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp,
-                                        _vp, _vp, _vp, _sz, _vp]
-    lib.fbg_dispatch_workspace_size.restype = _sz
-    lib.fbg_dispatch_workspace_size.argtypes = [_i64, _i64, _i64]
+                                        _vp, _vp, _vp]
     lib.fbg_combine_experts.restype = _int
     lib.fbg_combine_experts.argtypes = [_vp, _i64, _int, _i64, _vp, _vp, _vp, _i64, _int, _vp, _i64, _int, _i64, _i64,
                                         _i64, _vp]

@@ -591,7 +591,7 @@ bool any_overlap(const Range (&out)[O], const Range (&in)[I]) {
   return false;
 }
 
-constexpr int64_t kMaxRouted = 1024;  // experts
+using fbg::kMaxRouted;
 constexpr int64_t kMaxTopk = 64;
 constexpr int64_t kMaxRank = 256;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 35;  // workgroups of a grid of two dimensions
@@ -640,20 +640,15 @@ extern "C" int fbg_route_experts(const void* logits, int64_t ld, int dtype, int6
   return fbg::launch_route(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }
 
-extern "C" size_t fbg_dispatch_workspace_size(int64_t T, int64_t topk, int64_t E) {
-  if (T < 0 || topk < 0 || E < 0 || T > kMaxExtent || topk > kMaxTopk || E > kMaxRouted || T * topk > kMaxExtent)
-    return (size_t)-1;
-  return (size_t)fbg::dispatch_workspace(T * topk, E);
-}
-
 extern "C" int fbg_dispatch_tokens(const int32_t* experts, int64_t T, int64_t topk, int64_t first_expert, int64_t E,
                                    const void* x, int64_t ldx, int64_t K, int size, const float* x_scale, int64_t S,
                                    void* rows, int64_t ldrows, float* row_scale, int32_t* offsets, int32_t* slots,
-                                   void* workspace, size_t workspace_bytes, void* stream) {
+                                   void* stream) {
   if (!x_scale) S = 0, row_scale = nullptr;
-  if (T < 0 || topk < 0 || E < 0 || K < 0 || S < 0 || (size != 1 && size != 2 && size != 4))
+  if (T < 0 || topk < 0 || E < 0 || first_expert < 0 || K < 0 || S < 0 || (size != 1 && size != 2 && size != 4))
     return FBG_ERROR_INVALID_VALUE;
-  if (T > kMaxExtent || topk > kMaxTopk || E > kMaxRouted || K > kMaxExtent || S > kMaxExtent || T * topk > kMaxExtent)
+  if (T > kMaxExtent || topk > kMaxTopk || E > kMaxRouted || K > kMaxExtent || S > kMaxExtent || T * topk > kMaxExtent ||
+      first_expert > kMaxExtent)
     return FBG_ERROR_UNSUPPORTED;
   const int64_t n = T * topk;
   if ((T > 1 && ldx < K) || (n > 1 && ldrows < K)) return FBG_ERROR_INVALID_VALUE;
@@ -665,14 +660,12 @@ extern "C" int fbg_dispatch_tokens(const int32_t* experts, int64_t T, int64_t to
     return FBG_ERROR_UNSUPPORTED;
   if (!offsets || (n > 0 && (!experts || !slots)) || (n > 0 && bytesX > 0 && (!x || !rows)) || (bytesRs > 0 && !row_scale))
     return FBG_ERROR_INVALID_VALUE;
-  const int64_t need = fbg::dispatch_workspace(n, E);
-  if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return FBG_ERROR_OUT_OF_MEMORY;
   if (n == 0) x = nullptr, rows = nullptr;
-  const Range out[] = {{rows, bytesR}, {row_scale, bytesRs}, {offsets, (E + 1) * 4}, {slots, n * 4}, {workspace, need}};
+  const Range out[] = {{rows, bytesR}, {row_scale, bytesRs}, {offsets, (E + 1) * 4}, {slots, n * 4}};
   const Range in[] = {{experts, n * 4}, {x, bytesX}, {x_scale, bytesXs}};
   if (any_overlap(out, in)) return FBG_ERROR_INVALID_VALUE;
   if (!aligned(experts, 4) || !aligned(x, (uintptr_t)size) || !aligned(x_scale, 4) || !aligned(rows, (uintptr_t)size) ||
-      !aligned(row_scale, 4) || !aligned(offsets, 4) || !aligned(slots, 4) || (need > 0 && !aligned(workspace, 4)))
+      !aligned(row_scale, 4) || !aligned(offsets, 4) || !aligned(slots, 4))
     return FBG_ERROR_UNSUPPORTED;
   fbg::DispatchArgs args;
   args.experts = experts;
@@ -682,13 +675,12 @@ extern "C" int fbg_dispatch_tokens(const int32_t* experts, int64_t T, int64_t to
   args.row_scale = reinterpret_cast<uint8_t*>(row_scale);
   args.offsets = offsets;
   args.slots = slots;
-  args.counts = static_cast<int32_t*>(workspace);
   args.x_pitch = ldx * size;
   args.row_bytes = K * size;
   args.rows_pitch = ldrows * size;
   args.scale_bytes = S * 4;
-  args.first = first_expert;
-  args.blocks = 0;
+  args.first = (int)first_expert;
+  args.own = 0;
   args.T = (int)T;
   args.topk = (int)topk;
   args.n = (int)n;

@@ -170,123 +170,240 @@ hipError_t route(const RouteArgs& a) {
 
 // ---------------------------------------------------------------------------
 // Into expert order: a stable counting sort of the T * topk choices by expert.
-// Each workgroup ranks kSortBlock choices among themselves and counts its
-// experts'; one workgroup turns the counts into starts; then every choice knows
-// its row, and a workgroup per token copies the token's row to all of them.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 256, kSortItems = 4, kSortBlock = kSortThreads * kSortItems;
 
-// Where a choice's expert is held here, its number, else -1.
-__device__ __forceinline__ int local_expert(int id, int64_t first, int E) {
-  const int64_t e = (int64_t)id - first;
-  return e >= 0 && e < E ? (int)e : -1;
+// Where a choice's expert is held here, its number, else kNoExpert.  (first and
+// first + E are within 0 .. 2^31 - 1, so a negative id wraps to a number past E.)
+constexpr int kNoExpert = 0x7fffffff;
+__device__ __forceinline__ int local_expert(int id, int first, int E) {
+  const uint32_t e = (uint32_t)id - (uint32_t)first;
+  return e < (uint32_t)E ? (int)e : kNoExpert;
 }
 
-__global__ __launch_bounds__(kSortThreads) void k_rank(DispatchArgs a) {
-  extern __shared__ int counts[];  // [waves][E]
-  constexpr int kWaves = kSortThreads / 64;
+typedef unsigned int U4 __attribute__((ext_vector_type(4), aligned(1)));
+
+// The bytes of one token, row and scales, to `slots` (in LDS, -1 for none) by
+// TPT threads.  The first 16 bytes of each thread are loaded before the slots
+// are known (`head`).
+template <int TPT>
+struct Mover {
+  const uint8_t* x;
+  int64_t bytes;
+  int t;
+  U4 head;
+  __device__ __forceinline__ Mover(const DispatchArgs& a, int64_t token, int t_)
+      : x(a.x + token * a.x_pitch), bytes(a.row_bytes), t(t_) {
+    if ((int64_t)t * 16 + 16 <= bytes) head = *reinterpret_cast<const U4*>(x + t * 16);
+  }
+  __device__ __forceinline__ void put(const DispatchArgs& a, int64_t token, const int* slots) const {
+    for (int64_t at = (int64_t)t * 16; at < bytes; at += TPT * 16) {
+      if (at + 16 <= bytes) {
+        const U4 v = at < TPT * 16 ? head : *reinterpret_cast<const U4*>(x + at);
+        for (int j = 0; j < a.topk; ++j)
+          if (slots[j] >= 0) *reinterpret_cast<U4*>(a.rows + slots[j] * a.rows_pitch + at) = v;
+      } else {
+        for (int64_t i = at; i < bytes; ++i) {
+          const uint8_t v = x[i];
+          for (int j = 0; j < a.topk; ++j)
+            if (slots[j] >= 0) a.rows[slots[j] * a.rows_pitch + i] = v;
+        }
+      }
+    }
+    if (a.x_scale) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(a.x_scale + token * a.scale_bytes);
+      for (int64_t i = t; i < a.scale_bytes / 4; i += TPT) {
+        const uint32_t v = from[i];
+        for (int j = 0; j < a.topk; ++j)
+          if (slots[j] >= 0) reinterpret_cast<uint32_t*>(a.row_scale + slots[j] * a.scale_bytes)[i] = v;
+      }
+    }
+  }
+};
+
+// Exclusive sums of values[0 .. 1024) over a workgroup of THREADS threads,
+// 1024 / THREADS next to one another each; sums: THREADS / 64 words of LDS.
+template <int THREADS>
+__device__ __forceinline__ void exclusive_sums(int (&v)[1024 / THREADS], int* sums) {
+  constexpr int N = 1024 / THREADS;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  if (block_of_grid() >= a.blocks) return;  // a whole workgroup
-  for (int i = threadIdx.x; i < kWaves * a.E; i += kSortThreads) counts[i] = 0;
-  __syncthreads();
-  int* mine = counts + w * a.E;
-  const int64_t base = block_of_grid() * kSortBlock + w * 64 * kSortItems;
-  int expert[kSortItems], rank[kSortItems];
+  int total = 0;
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
-    const int64_t i = base + r * 64 + lane;
-    expert[r] = i < a.n ? local_expert(a.experts[i], a.first, a.E) : -1;
-    // The lanes that hold the same expert, found bit by bit.
-    uint64_t same = __ballot(expert[r] >= 0);
+  for (int i = 0; i < N; ++i) {
+    const int c = v[i];
+    v[i] = total;
+    total += c;
+  }
+  int run = total;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(run, o, 64);
+    if (lane >= o) run += u;
+  }
+  if (lane == 63) sums[w] = run;
+  __syncthreads();
+  int before = run - total;
+  for (int i = 0; i < w; ++i) before += sums[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] += before;
+}
+
+// Few choices: one launch.  A workgroup per token finds the rows of its choices
+// by counting, over all choices, those of lower experts and the earlier ones of
+// the same: the lanes' comparisons are masks in scalar registers, whose bits
+// the scalar unit counts.  The first workgroup makes the offsets.
+__global__ __launch_bounds__(256) void k_dispatch_few(DispatchArgs a) {
+  __shared__ int shared[1024];
+  __shared__ int sums[4];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (blockIdx.x == 0) {
+    for (int i = tid; i < 1024; i += 256) shared[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.n; i += 256) {
+      const int e = local_expert(a.experts[i], a.first, a.E);
+      if (e != kNoExpert) atomicAdd(&shared[e], 1);
+    }
+    __syncthreads();
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = shared[tid * 4 + i];
+    exclusive_sums<256>(v, sums);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tid * 4 + i <= a.E) a.offsets[tid * 4 + i] = v[i];
+    if (tid == 255 && a.E == 1024) a.offsets[1024] = v[3] + shared[1023];
+    return;
+  }
+  const int t = blockIdx.x - 1, i0 = t * a.topk;
+  const Mover<256> mover(a, t, tid);
+  int* counts = shared;  // [wave][choice]
+  for (int j0 = 0; j0 < a.topk; j0 += 8) {
+    const int targets = a.topk - j0 < 8 ? a.topk - j0 : 8;
+    int target[8], count[8] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      target[j] = j < targets ? local_expert(a.experts[i0 + j0 + j], a.first, a.E) : kNoExpert;
+    for (int c = w * 64; c < a.n; c += 256) {
+      const int e = c + lane < a.n ? local_expert(a.experts[c + lane], a.first, a.E) : kNoExpert;
+      const int earlier = i0 + j0 - c;  // how many of these 64 come before the first choice
+      if (earlier >= 64 || earlier <= -8) {
+        const int bound = earlier >= 64;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < targets) count[j] += __popcll(__ballot(e < target[j] + bound && e != kNoExpert));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t before = earlier + j >= 64 ? ~0ull : earlier + j <= 0 ? 0 : (1ull << (earlier + j)) - 1;
+          count[j] += __popcll(__ballot(e < target[j])) + __popcll(__ballot(e == target[j]) & before);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (lane == j && j < targets) counts[w * 64 + j0 + j] = target[j] == kNoExpert ? -1 : count[j];
+  }
+  __syncthreads();
+  if (tid < a.topk) {
+    int s = counts[tid];
+    if (s >= 0) s += counts[64 + tid] + counts[128 + tid] + counts[192 + tid];
+    counts[256 + tid] = s;
+    a.slots[i0 + tid] = s;
+  }
+  __syncthreads();
+  mover.put(a, t, counts + 256);
+}
+
+// Many choices, two launches: the choices' rows, and then the rows themselves.
+// Each workgroup counts all choices by expert, those before its own apart (LDS
+// atomics on integers: their order changes nothing), which gives its starts without a
+// word from the others, and ranks its own, 1024 at a time: a wave finds the lanes
+// of each expert bit by bit, and the waves' counts are summed in their order.
+__global__ __launch_bounds__(1024) void k_slots(DispatchArgs a) {
+  extern __shared__ int wave_counts[];  // [16][E]
+  __shared__ int counts[2048], sums[16];  // choices before its own by expert, and the others
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t own = blockIdx.x * a.own, end = own + a.own < a.n ? own + a.own : a.n;
+  counts[tid] = counts[1024 + tid] = 0;
+  __syncthreads();
+  // A wave takes 256 choices at a time, which lie on one side of its own.
+  typedef int I4 __attribute__((ext_vector_type(4), aligned(4)));
+  constexpr int kStep = 4096, kAhead = 2;
+  for (int64_t c = (int64_t)w * 256; c < a.n; c += kStep * kAhead) {
+    I4 id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t i = c + u * kStep + lane * 4;
+      if (i + 4 <= a.n) {
+        id[u] = *reinterpret_cast<const I4*>(a.experts + i);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) id[u][k] = i + k < a.n ? a.experts[i + k] : -1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      int* side = counts + (c + u * kStep < own ? 0 : 1024);
+      const int lead = __builtin_amdgcn_readfirstlane(id[u][0]);
+      if (__ballot(id[u][0] != lead || id[u][1] != lead || id[u][2] != lead || id[u][3] != lead) == 0) {
+        const int e = local_expert(lead, a.first, a.E);  // a popular expert's run: one addition
+        if (lane == 0 && e != kNoExpert) atomicAdd(&side[e], 256);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = local_expert(id[u][k], a.first, a.E);
+          if (e != kNoExpert) atomicAdd(&side[e], 1);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  int all[1] = {counts[tid] + counts[1024 + tid]};
+  const int count = all[0];
+  exclusive_sums<1024>(all, sums);
+  if (blockIdx.x == 0) {
+    if (tid <= a.E) a.offsets[tid] = all[0];
+    if (tid == a.E - 1) a.offsets[a.E] = all[0] + count;
+  }
+  int start = all[0] + counts[tid];  // of expert tid's next choice here
+  int* mine = wave_counts + w * a.E;
+  for (int64_t base = own; base < end; base += 1024) {
+    const int64_t at = base + tid;
+    const int e = at < end ? local_expert(a.experts[at], a.first, a.E) : kNoExpert;
+    for (int k = lane; k < a.E; k += 64) mine[k] = 0;
+    uint64_t same = __ballot(e != kNoExpert);
     for (int bit = 1; bit < a.E; bit <<= 1) {
-      const uint64_t set = __ballot((expert[r] & bit) != 0);
-      same &= (expert[r] & bit) ? set : ~set;
+      const uint64_t set = __ballot((e & bit) != 0);
+      same &= (e & bit) ? set : ~set;
     }
-    const int before = __popcll(same & ((1ull << lane) - 1));
-    rank[r] = 0;
-    if (expert[r] >= 0) {
-      const int start = mine[expert[r]];
-      rank[r] = start + before;
-    }
+    const int ahead = __popcll(same & ((1ull << lane) - 1));
     wave_sync();
-    if (expert[r] >= 0 && before == 0) mine[expert[r]] += __popcll(same);
-    wave_sync();
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int run = 0;
-    for (int i = 0; i < kWaves; ++i) {
-      const int c = counts[i * a.E + e];
-      counts[i * a.E + e] = run;
-      run += c;
-    }
-    a.counts[block_of_grid() * a.E + e] = run;
-  }
-  __syncthreads();
+    if (e != kNoExpert && ahead == 0) mine[e] = __popcll(same);
+    __syncthreads();
+    if (tid < a.E) {
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
-    const int64_t i = base + r * 64 + lane;
-    if (i < a.n) a.slots[i] = expert[r] >= 0 ? mine[expert[r]] + rank[r] : -1;
-  }
-}
-
-// counts[b][e] becomes the first row of block b's choices of expert e.
-__global__ __launch_bounds__(1024) void k_starts(DispatchArgs a) {
-  __shared__ int sums[1024];
-  const int e = threadIdx.x;
-  int run = 0;
-  if (e < a.E)
-    for (int64_t b = 0; b < a.blocks; ++b) {
-      const int c = a.counts[b * a.E + e];
-      a.counts[b * a.E + e] = run;
-      run += c;
+      for (int k = 0; k < 16; ++k) {
+        const int c = wave_counts[k * a.E + tid];
+        wave_counts[k * a.E + tid] = start;
+        start += c;
+      }
     }
-  sums[e] = run;
-  __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const int u = e >= o ? sums[e - o] : 0;
     __syncthreads();
-    sums[e] += u;
-    __syncthreads();
-  }
-  if (e < a.E) a.offsets[e + 1] = sums[e];
-  if (e == 0) a.offsets[0] = 0;
-}
-
-// Copies `bytes` bytes from any address to any other, by `threads` threads.
-__device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64_t bytes, int t, int threads) {
-  typedef unsigned int U4 __attribute__((ext_vector_type(4), aligned(1)));
-  for (int64_t at = (int64_t)t * 16; at < bytes; at += (int64_t)threads * 16) {
-    if (at + 16 <= bytes) {
-      *reinterpret_cast<U4*>(to + at) = *reinterpret_cast<const U4*>(from + at);
-    } else {
-      for (int64_t i = at; i < bytes; ++i) to[i] = from[i];
-    }
+    if (at < end) a.slots[at] = e != kNoExpert ? mine[e] + ahead : -1;
+    wave_sync();  // a wave's counts are its own again
   }
 }
 
+// TPT threads per token.
+template <int TPT>
 __global__ __launch_bounds__(256) void k_move(DispatchArgs a) {
-  const int64_t t = block_of_grid();
-  if (t >= a.T) return;
-  const uint8_t* x = a.x + t * a.x_pitch;
-  for (int j = 0; j < a.topk; ++j) {
-    const int64_t i = t * a.topk + j;
-    const int rank = a.slots[i];
-    if (rank < 0) continue;
-    const int e = local_expert(a.experts[i], a.first, a.E);
-    const int64_t slot = (int64_t)a.offsets[e] + a.counts[i / kSortBlock * a.E + e] + rank;
-    copy_row(x, a.rows + slot * a.rows_pitch, a.row_bytes, threadIdx.x, 256);
-    if (a.x_scale)
-      copy_row(a.x_scale + t * a.scale_bytes, a.row_scale + slot * a.scale_bytes, a.scale_bytes, threadIdx.x, 256);
-  }
-  __syncthreads();  // every thread has read the ranks
-  for (int j = threadIdx.x; j < a.topk; j += 256) {
-    const int64_t i = t * a.topk + j;
-    const int rank = a.slots[i];
-    if (rank < 0) continue;
-    const int e = local_expert(a.experts[i], a.first, a.E);
-    a.slots[i] = a.offsets[e] + a.counts[i / kSortBlock * a.E + e] + rank;
-  }
+  __shared__ int shared[256 / TPT][64];
+  const int t = threadIdx.x % TPT, which = threadIdx.x / TPT;
+  const int64_t token = block_of_grid() * (256 / TPT) + which;
+  const bool here = token < a.T;
+  const Mover<TPT> mover(a, here ? token : 0, t);
+  if (here && t < a.topk) shared[which][t] = a.slots[token * a.topk + t];
+  __syncthreads();
+  if (here) mover.put(a, token, shared[which]);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,14 +486,22 @@ hipError_t launch_route(const RouteArgs& a) {
   }
 }
 
-int64_t dispatch_workspace(int64_t n, int64_t E) { return (n + kSortBlock - 1) / kSortBlock * E * 4; }
+// Up to this many comparisons of a token's choices with all of them the kernel
+// that makes them is the faster one (64 tokens of 8 choices 5.1 us against 7.3,
+// 256 of 8 8.3 against 8.6, 512 of 8 13.4 against 10.9, 2048 of 2 17 against 8.1).
+constexpr int64_t kFewComparisons = (int64_t)1 << 19;
 
 hipError_t launch_dispatch(DispatchArgs a) {
-  a.blocks = (a.n + kSortBlock - 1) / kSortBlock;
-  if (a.blocks > 0)
-    hipLaunchKernelGGL(k_rank, wide_grid(a.blocks), dim3(kSortThreads), kSortThreads / 64 * a.E * sizeof(int), a.stream, a);
-  hipLaunchKernelGGL(k_starts, dim3(1), dim3(1024), 0, a.stream, a);
-  if (a.blocks > 0) hipLaunchKernelGGL(k_move, wide_grid(a.T), dim3(256), 0, a.stream, a);
+  if ((int64_t)a.T * a.n <= kFewComparisons) {
+    hipLaunchKernelGGL(k_dispatch_few, dim3(a.n > 0 ? a.T + 1 : 1), dim3(256), 0, a.stream, a);
+    return hipGetLastError();
+  }
+  a.own = ((int64_t)a.n + 256 * 1024 - 1) / (256 * 1024) * 1024;  // at most a workgroup per compute unit
+  hipLaunchKernelGGL(k_slots, dim3((unsigned)((a.n + a.own - 1) / a.own)), dim3(1024), 16 * a.E * sizeof(int), a.stream, a);
+  if (a.row_bytes <= 2048)
+    hipLaunchKernelGGL(k_move<64>, wide_grid(((int64_t)a.T + 3) / 4), dim3(256), 0, a.stream, a);
+  else
+    hipLaunchKernelGGL(k_move<256>, wide_grid(a.T), dim3(256), 0, a.stream, a);
   return hipGetLastError();
 }
 

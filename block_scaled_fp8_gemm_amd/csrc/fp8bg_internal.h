@@ -38,10 +38,9 @@ int int8_grouped_gemm(const void* A, int64_t lda, const float* a_s, const void* 
                       void* C, int64_t ldc, const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t K,
                       int out_dtype, void* stream);
 
-// Workspace of the two-step operators (fp8bg_experts.hip, fp8bg_adapters.hip):
-// bytes for n choices over E experts; over how many workgroups the adapters'
-// first product splits K.
-int64_t dispatch_workspace(int64_t n, int64_t E);
+constexpr int64_t kMaxRouted = 1024;  // most experts of fbg_route_experts and fbg_dispatch_tokens
+
+// Over how many workgroups the adapters' first product splits K (fp8bg_adapters.hip).
 int adapter_splits(int64_t M, int64_t K);
 
 #ifdef __HIPCC__
@@ -142,10 +141,9 @@ struct DispatchArgs {
   uint8_t* row_scale;
   int32_t* offsets;
   int32_t* slots;
-  int32_t* counts;  // workspace
   int64_t x_pitch, row_bytes, rows_pitch, scale_bytes;  // bytes
-  int64_t first;   // the first expert held here
-  int64_t blocks;  // launch_dispatch sets it
+  int first;    // the first expert held here
+  int64_t own;  // choices per workgroup (launch_dispatch sets it)
   int T, topk, n, E;  // n = T * topk
   hipStream_t stream;
 };

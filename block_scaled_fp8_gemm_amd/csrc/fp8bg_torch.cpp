@@ -370,8 +370,7 @@ PyObject* dispatch_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
     scale_shape[0] = T * topk;
   }
   const int64_t first = integer(v[4]);
-  const size_t need = fbg_dispatch_workspace_size(T, topk, E);
-  if (need == (size_t)-1) check_status(FBG_ERROR_UNSUPPORTED, "fbg_dispatch_tokens");
+  if (E > fbg::kMaxRouted) check_status(FBG_ERROR_UNSUPPORTED, "fbg_dispatch_tokens");
   const Launch launch(v[7], dev);
   const at::Tensor rows = v[5] != Py_None      ? tensor(v[5], "rows")
                           : type == at::kChar ? make_codes(T * topk, K, dev)
@@ -385,12 +384,11 @@ PyObject* dispatch_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
     value_error("row_scale needs x_scale");
   }
   const at::Tensor offsets = make({E + 1}, at::kInt, dev), slots = make({T, topk}, at::kInt, dev);
-  const at::Tensor work = need ? make({(int64_t)need}, at::kByte, dev) : at::Tensor();
   check_status(fbg_dispatch_tokens(ids, T, topk, first, E, x.data_ptr(), ldx, K, (int)size, x_scale, S,
                                    rows.data_ptr(), ldrows,
                                    row_scale.defined() ? static_cast<float*>(row_scale.data_ptr()) : nullptr,
                                    static_cast<int32_t*>(offsets.data_ptr()), static_cast<int32_t*>(slots.data_ptr()),
-                                   need ? work.data_ptr() : nullptr, need, launch.get()),
+                                   launch.get()),
                "fbg_dispatch_tokens");
   PyObject* so = row_scale.defined() ? THPVariable_Wrap(row_scale) : Py_NewRef(Py_None);
   return Py_BuildValue("(NNNN)", THPVariable_Wrap(rows), so, THPVariable_Wrap(offsets), THPVariable_Wrap(slots));

@@ -70,17 +70,12 @@ int fbg_route_experts(const void *logits, int64_t ld, int dtype, int64_t T, int6
  * contiguous, or NULL (then S and row_scale mean nothing).  rows [T*topk, K] and
  * row_scale [T*topk, S] contiguous: those behind offsets[E] are left as they
  * are.  experts and slots [T,topk], offsets [E+1].  x and rows aligned to
- * `size`, the others to 4 bytes.  E <= 1024, topk <= 64, T * topk <= INT32_MAX - 1024.
- * workspace: 4-byte aligned device memory of at least
- * fbg_dispatch_workspace_size(T, topk, E) bytes (0 for up to a few thousand
- * choices), of any content; too small -> OUT_OF_MEMORY.  Calls that overlap in
- * time must not share one.
+ * `size`, the others to 4 bytes.  E <= 1024, topk <= 64, T * topk and
+ * first_expert <= INT32_MAX - 1024.
  */
 int fbg_dispatch_tokens(const int32_t *experts, int64_t T, int64_t topk, int64_t first_expert, int64_t E,
                         const void *x, int64_t ldx, int64_t K, int size, const float *x_scale, int64_t S, void *rows,
-                        int64_t ldrows, float *row_scale, int32_t *offsets, int32_t *slots, void *workspace,
-                        size_t workspace_bytes, void *stream);
-size_t fbg_dispatch_workspace_size(int64_t T, int64_t topk, int64_t E);
+                        int64_t ldrows, float *row_scale, int32_t *offsets, int32_t *slots, void *stream);
 
 /*
  * fbg_combine_experts -- the way back, each token's rows summed by weight:

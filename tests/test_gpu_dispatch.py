@@ -79,11 +79,11 @@ def test_rows(gpu, K, dtype, pad, lead, tokens):
     _check(gpu, _ids(tokens, 8, 16, K, "some"), 16, _x(tokens, K, dtype, K, pad, lead), scale, first=1)
 
 
-@pytest.mark.parametrize("first", [0, 16, 240, 250, 300, -5, 2 ** 31, -2 ** 31, 2 ** 40])
+@pytest.mark.parametrize("first", [0, 16, 240, 250, 300, 2 ** 31 - 1 - 1024])
 def test_share_of_the_experts(gpu, first):
     """Experts held elsewhere, and ids that no expert has, get no row."""
     ids = _ids(100, 4, 256, 3)
-    ids[3, 0], ids[4, 1], ids[5, 2] = -1, 2 ** 31 - 1, -2 ** 31
+    ids[3, 0], ids[4, 1], ids[5, 2], ids[6, 3] = -1, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1024
     for tokens in (100, 3000):
         _check(gpu, ids.repeat(tokens // 100, 1), 16, _x(tokens, 64, torch.int8, 2), torch.rand(tokens, 3), first=first)
 

@@ -23,10 +23,9 @@ def _route(logits=P, ld=256, dtype=0, T=16, E=256, topk=8, score=0, bias=2 * P, 
 
 
 def _dispatch(experts=P, T=16, topk=8, first=0, E=64, x=2 * P, ldx=256, K=256, size=1, xs=3 * P, S=2, rows=4 * P,
-              ldr=256, rs=5 * P, off=6 * P, slots=7 * P, ws=8 * P, wn=None):
-    wn = 1 << 30 if wn is None else wn
+              ldr=256, rs=5 * P, off=6 * P, slots=7 * P):
     return fbg.load().fbg_dispatch_tokens(experts, T, topk, first, E, x, ldx, K, size, xs, S, rows, ldr, rs, off, slots,
-                                          ws, wn, None)
+                                          None)
 
 
 def _combine(rows=P, ldr=256, dtype=0, R=128, slots=2 * P, weights=3 * P, base=4 * P, ldb=256, bdtype=0, out=5 * P,
@@ -45,7 +44,7 @@ def _adapters(y=P, ldy=256, x=2 * P, ldx=128, A=3 * P, B=4 * P, ids=5 * P, scale
 def test_every_declared_function_is_exported():
     text = open(os.path.join(ROOT, "include", "fp8bg_tokens.h")).read()
     names = set(re.findall(r"^(?:int|size_t) (fbg_\w+)\(", text, re.M))
-    assert names == {"fbg_route_experts", "fbg_dispatch_tokens", "fbg_dispatch_workspace_size", "fbg_combine_experts",
+    assert names == {"fbg_route_experts", "fbg_dispatch_tokens", "fbg_combine_experts",
                      "fbg_add_adapters", "fbg_add_adapters_workspace_size"}
     for n in names:
         assert isinstance(getattr(fbg.load(), n), ctypes._CFuncPtr)
@@ -77,22 +76,15 @@ def test_route_refusals():
 
 def test_dispatch_refusals():
     for kw in ({"experts": None}, {"x": None}, {"rows": None}, {"rs": None}, {"off": None}, {"slots": None}, {"T": -1},
-               {"topk": -1}, {"E": -1}, {"K": -1}, {"S": -1}, {"size": 3}, {"size": 8}, {"ldx": 255}, {"ldr": 255}):
+               {"topk": -1}, {"E": -1}, {"first": -1}, {"K": -1}, {"S": -1}, {"size": 3}, {"size": 8}, {"ldx": 255}, {"ldr": 255}):
         assert _dispatch(**kw) == BAD, kw
-    for kw in ({"T": TOP + 1}, {"topk": 65}, {"E": 1025}, {"T": 2 ** 26, "topk": 33}, {"K": TOP + 1, "ldx": 2 ** 32, "ldr": 2 ** 32}):
+    for kw in ({"T": TOP + 1}, {"topk": 65}, {"E": 1025}, {"first": TOP + 1}, {"T": 2 ** 26, "topk": 33}, {"K": TOP + 1, "ldx": 2 ** 32, "ldr": 2 ** 32}):
         assert _dispatch(**kw) == UNSUP, kw
     assert _dispatch(experts=P + 2) == UNSUP and _dispatch(x=2 * P + 1, size=2) == UNSUP
     assert _dispatch(rows=4 * P + 2, size=4) == UNSUP and _dispatch(xs=3 * P + 1) == UNSUP
     assert _dispatch(rs=5 * P + 1) == UNSUP and _dispatch(off=6 * P + 2) == UNSUP and _dispatch(slots=7 * P + 3) == UNSUP
     assert _dispatch(rows=2 * P + 256) == BAD and _dispatch(rows=P) == BAD and _dispatch(rs=3 * P) == BAD
     assert _dispatch(off=7 * P + 8) == BAD and _dispatch(slots=P) == BAD and _dispatch(off=4 * P) == BAD
-    big = {"T": 1 << 20, "rows": 16 * P, "rs": 32 * P, "slots": 64 * P}
-    need = fbg.load().fbg_dispatch_workspace_size(1 << 20, 8, 64)
-    assert need > 0
-    assert _dispatch(ws=None, **big) == MEM and _dispatch(wn=need - 1, **big) == MEM
-    assert _dispatch(ws=128 * P + 2, **big) == UNSUP and _dispatch(ws=6 * P, **big) == BAD
-    assert fbg.load().fbg_dispatch_workspace_size(-1, 8, 64) == ctypes.c_size_t(-1).value
-    assert fbg.load().fbg_dispatch_workspace_size(1, 8, 1025) == ctypes.c_size_t(-1).value
 
 
 def test_combine_refusals():
