@@ -702,7 +702,7 @@ extern "C" int fbg_combine_experts(const void* rows, int64_t ldrows, int dtype, 
   const int64_t es = elem_size(dtype), os = elem_size(out_dtype), bs = elem_size(base ? base_dtype : dtype);
   int64_t bytesR = 0, bytesB = 0, bytesO = 0;
   if (!extent(R, D, ldrows, es, &bytesR) || !extent(T, D, base ? ldbase : D, bs, &bytesB) ||
-      !extent(T, D, ldout, os, &bytesO) || T * ((D + 255) / 256) > kMaxBlocks)
+      !extent(T, D, ldout, os, &bytesO))
     return FBG_ERROR_UNSUPPORTED;
   if (T == 0 || D == 0) return FBG_SUCCESS;
   if ((bytesR > 0 && !rows) || !out || (topk > 0 && (!slots || !weights))) return FBG_ERROR_INVALID_VALUE;
@@ -729,7 +729,6 @@ extern "C" int fbg_combine_experts(const void* rows, int64_t ldrows, int dtype, 
   args.dtype = dtype;
   args.out_dtype = out_dtype;
   args.base_is_out = base && base_dtype == out_dtype;
-  args.splits = 1;
   args.stream = static_cast<hipStream_t>(stream);
   return fbg::launch_combine(args) == hipSuccess ? FBG_SUCCESS : FBG_ERROR_HIP;
 }

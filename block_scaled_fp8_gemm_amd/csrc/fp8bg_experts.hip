@@ -18,6 +18,7 @@ constexpr int64_t kGridX = 1 << 20;
 inline dim3 wide_grid(int64_t blocks) {
   return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
 }
+constexpr int kGridY = 1 << 15;
 __device__ __forceinline__ int64_t block_of_grid() { return (int64_t)blockIdx.y * kGridX + blockIdx.x; }
 
 // What the lanes of a wave wrote to LDS before it, all of them read behind it.
@@ -193,14 +194,17 @@ struct Mover {
   U4 head;
   __device__ __forceinline__ Mover(const DispatchArgs& a, int64_t token, int t_)
       : x(a.x + token * a.x_pitch), bytes(a.row_bytes), t(t_) {
-    if ((int64_t)t * 16 + 16 <= bytes) head = *reinterpret_cast<const U4*>(x + t * 16);
+    if ((int64_t)t * 16 < bytes && bytes >= 16) head = *reinterpret_cast<const U4*>(x + start(t * 16));
   }
+  // The last 16 bytes of a row overlap those before them (one by one they took 4 us).
+  __device__ __forceinline__ int64_t start(int64_t at) const { return at + 16 <= bytes ? at : bytes - 16; }
   __device__ __forceinline__ void put(const DispatchArgs& a, int64_t token, const int* slots) const {
     for (int64_t at = (int64_t)t * 16; at < bytes; at += TPT * 16) {
-      if (at + 16 <= bytes) {
-        const U4 v = at < TPT * 16 ? head : *reinterpret_cast<const U4*>(x + at);
+      if (bytes >= 16) {
+        const int64_t s = start(at);
+        const U4 v = at < TPT * 16 ? head : *reinterpret_cast<const U4*>(x + s);
         for (int j = 0; j < a.topk; ++j)
-          if (slots[j] >= 0) *reinterpret_cast<U4*>(a.rows + slots[j] * a.rows_pitch + at) = v;
+          if (slots[j] >= 0) *reinterpret_cast<U4*>(a.rows + slots[j] * a.rows_pitch + s) = v;
       } else {
         for (int64_t i = at; i < bytes; ++i) {
           const uint8_t v = x[i];
@@ -407,7 +411,9 @@ __global__ __launch_bounds__(256) void k_move(DispatchArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Back into token order: a thread sums 16 bytes' worth of a token's columns.
+// Back into token order: a thread sums 16 bytes' worth of a token's columns, the
+// loads of up to kRows rows in flight together (one after the other 82 us at 4096
+// tokens of 8 x 4096 bf16).  A token's slots and weights are in scalar registers.
 // ---------------------------------------------------------------------------
 template <typename T, int VE>
 __device__ __forceinline__ void load_floats(const void* p, int64_t at, int n, float (&v)[VE]) {
@@ -424,46 +430,70 @@ __device__ __forceinline__ void load_floats(const void* p, int64_t at, int n, fl
 }
 
 template <typename T, typename O>
-__global__ __launch_bounds__(64) void k_combine(CombineArgs a) {
-  constexpr int VE = 16 / (int)sizeof(T);
-  const int64_t block = block_of_grid();
-  const int64_t t = block / a.splits;
+__global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
+  constexpr int VE = 16 / (int)sizeof(T), kRows = 8;
+  typedef T Raw __attribute__((ext_vector_type(VE)));
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.z * kGridY + blockIdx.y;
+  int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VE;
   if (t >= a.T) return;
-  const int at = ((int)(block % a.splits) * 64 + (int)threadIdx.x) * VE;
+  const int slot_of = lane < a.topk ? a.slots[t * a.topk + lane] : -1;
+  const float weight_of = lane < a.topk ? a.weights[t * a.topk + lane] : 0.0f;
   if (at >= a.D) return;
-  const int n = a.D - at;
+  // A last chunk that D cuts is taken from the row's end; its first columns are
+  // another thread's, and not stored.
+  const bool whole = a.D >= VE;
+  int cut = 0;
+  if (whole && at + VE > a.D) cut = (int)(at + VE - a.D), at = a.D - VE;
+  const int n = whole ? VE : a.D;
   float acc[VE] = {};
   if (a.base) {
     if (a.base_is_out) load_floats<O>(a.base, t * a.ldbase + at, n, acc);
     else load_floats<T>(a.base, t * a.ldbase + at, n, acc);
   }
-  for (int j = 0; j < a.topk; ++j) {
-    const int slot = a.slots[t * a.topk + j];
-    if (slot < 0 || slot >= a.R) continue;
-    const float w = a.weights[t * a.topk + j];
-    float v[VE];
-    load_floats<T>(a.rows, (int64_t)slot * a.ldrows + at, n, v);
+  const T* rows = reinterpret_cast<const T*>(a.rows) + at;
+  for (int j0 = 0; j0 < a.topk; j0 += kRows) {
+    Raw raw[kRows];
+    int slot[kRows];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+    for (int j = 0; j < kRows; ++j) {
+      slot[j] = j0 + j < a.topk ? __builtin_amdgcn_readlane(slot_of, j0 + j) : -1;
+      if (slot[j] < 0 || slot[j] >= a.R) continue;
+      const T* p = rows + slot[j] * a.ldrows;
+      if (whole) {
+        __builtin_memcpy(&raw[j], p, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) raw[j][i] = p[i < n ? i : 0];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (slot[j] < 0 || slot[j] >= a.R) continue;
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight_of), j0 + j));
+#pragma unroll
+      for (int i = 0; i < VE; ++i) acc[i] = __builtin_fmaf(w, (float)raw[j][i], acc[i]);
+    }
   }
   O* out = reinterpret_cast<O*>(a.out) + t * a.ldout + at;
   O o[VE];
 #pragma unroll
   for (int i = 0; i < VE; ++i) o[i] = (O)acc[i];
-  if (n >= VE) {
+  if (whole && cut == 0) {
     __builtin_memcpy(out, o, sizeof(o));
   } else {
 #pragma unroll
     for (int i = 0; i < VE; ++i)
-      if (i < n) out[i] = o[i];
+      if (i >= cut && i < n) out[i] = o[i];
   }
 }
 
 template <typename T, typename O>
-hipError_t combine(CombineArgs a) {
-  constexpr int kCols = 64 * 16 / (int)sizeof(T);
-  a.splits = (a.D + kCols - 1) / kCols;
-  hipLaunchKernelGGL((k_combine<T, O>), wide_grid((int64_t)a.T * a.splits), dim3(64), 0, a.stream, a);
+hipError_t combine(const CombineArgs& a) {
+  constexpr int kCols = 256 * 16 / (int)sizeof(T);
+  const unsigned y = a.T < kGridY ? a.T : kGridY;
+  const dim3 g((a.D + kCols - 1) / kCols, y, (a.T + y - 1) / y);
+  hipLaunchKernelGGL((k_combine<T, O>), g, dim3(256), 0, a.stream, a);
   return hipGetLastError();
 }
 

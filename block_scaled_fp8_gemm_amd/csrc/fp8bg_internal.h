@@ -159,7 +159,6 @@ struct CombineArgs {
   int R, T, topk, D;
   int dtype, out_dtype;
   int base_is_out;  // base's type: out's, or the rows'
-  int splits;       // workgroups per token (launch_combine sets it)
   hipStream_t stream;
 };
 hipError_t launch_combine(const CombineArgs& a);
