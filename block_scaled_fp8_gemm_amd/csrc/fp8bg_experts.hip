@@ -44,17 +44,58 @@ __device__ __forceinline__ T wave_sum(T v) {
   return v;
 }
 
+// Lanes' exchanges by data-parallel primitives, in rows of 16.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(dpp<CTRL>(__float_as_int(x)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)dpp<CTRL>((int)x);
+}
+constexpr int kRor = 0x120;  // rotation of a row
+constexpr int64_t kNone64 = (int64_t)1 << 63;
+
+// op over the L lanes of a token, in all of them: within a row by rotations, over
+// the four rows through scalar registers.
+template <int L, typename V, typename Op>
+__device__ __forceinline__ V over_lanes(V x, const Op& op) {
+  x = op(x, dpp<kRor + 8>(x));
+  x = op(x, dpp<kRor + 4>(x));
+  x = op(x, dpp<kRor + 2>(x));
+  x = op(x, dpp<kRor + 1>(x));
+  if constexpr (L == 64) {
+    const auto row = [&](int r) {
+      const int v = __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16 * r);
+      return __builtin_bit_cast(V, v);
+    };
+    x = op(op(row(0), row(1)), op(row(2), row(3)));
+  }
+  return x;
+}
+
+// Bits of a float as an integer of the same order, and back.
+__device__ __forceinline__ int ordered(float v) {
+  const int b = __float_as_int(v);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
 // ---------------------------------------------------------------------------
-// Routing.  One wave per token; lane l holds the experts l * VPL .. l * VPL +
-// VPL - 1, so that of equal values the lowest expert is in the lowest lane and
-// first in it.
+// Routing.  What is compared is c = score + bias in 64 bits, or the logits
+// themselves without a bias (the scores' order, exactly).
 // ---------------------------------------------------------------------------
+
+// A token by a whole wave, everything in 64 bits; lane l holds the experts
+// l * VPL .. l * VPL + VPL - 1, so that of equal values the lowest expert is in the
+// lowest lane and first in it.  shared: 64 * VPL values of LDS for this wave.
 template <typename T, int VPL>
-__global__ __launch_bounds__(256) void k_route(RouteArgs a) {
-  __shared__ double shared[4][64 * VPL];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t t = block_of_grid() * 4 + w;
-  if (t >= a.T) return;  // whole waves, which meet at no barrier
+__device__ void route_exactly(const RouteArgs& a, int64_t t, double* shared) {
+  const int lane = threadIdx.x & 63;
   float* wo = a.weights + t * a.topk;
   int* eo = a.experts + t * a.topk;
   if (a.mask && a.mask[t]) {
@@ -74,7 +115,6 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
   }
   top = wave_max(top);
   if (a.score == FBG_SCORE_SOFTMAX) bad |= top == -kInf;
-  // Scores in 64 bits, and what ranks them: the logits themselves without a bias.
   double s[VPL], c[VPL];
   double sum = 0.0;
 #pragma unroll
@@ -110,15 +150,16 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
   }
   if (a.groups > 1) {
     const int size = a.E / a.groups;
-    double* v = shared[w];
+    wave_sync();
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (allowed[i]) v[lane * VPL + i] = a.group_score == FBG_GROUP_MAX || a.bias ? c[i] : s[i];
+      if (allowed[i]) shared[lane * VPL + i] = a.group_score == FBG_GROUP_MAX || a.bias ? c[i] : s[i];
     wave_sync();
     double best = -kInf, second = -kInf;
     if (lane < a.groups) {
+#pragma unroll 8
       for (int i = 0; i < size; ++i) {
-        const double u = v[lane * size + i];
+        const double u = shared[lane * size + i];
         second = u > best ? best : u > second ? u : second;
         best = u > best ? u : best;
       }
@@ -133,25 +174,35 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) allowed[i] = allowed[i] && ((kept >> ((lane * VPL + i) / size)) & 1);
   }
+  // The values as integers of their order; the scores, as weights, to LDS.
+  wave_sync();
+  float* scores = reinterpret_cast<float*>(shared);
+  int64_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    scores[lane * VPL + i] = (float)s[i];
+    const int64_t bits = __builtin_bit_cast(int64_t, c[i] + 0.0);  // of two zeros none is larger
+    key[i] = allowed[i] ? bits ^ ((bits >> 63) & 0x7fffffffffffffff) : kNone64;
+  }
+  wave_sync();
   float mine = 0.0f;
   int expert = 0;
+  const auto more = [](auto x, auto y) { return x > y ? x : y; };
   for (int j = 0; j < a.topk; ++j) {
-    double best = -kInf;
-    int at = 0x7fffffff;
-    float score = 0.0f;
+    int64_t best = key[0];
+    int place = 0;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+      if (key[i] > best) best = key[i], place = i;
+    // The high words' maximum, then the low ones' among those that have it.
+    const int high = (int)(best >> 32), top_high = over_lanes<64>(high, more);
+    const uint32_t low = (uint32_t)best, top_low = over_lanes<64>(high == top_high ? low : 0u, more);
+    const int winner = __builtin_ctzll(__ballot(high == top_high && low == top_low));
+    const int e = winner * VPL + __builtin_amdgcn_readlane(place, winner);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (allowed[i] && (at == 0x7fffffff || c[i] > best)) best = c[i], at = lane * VPL + i, score = (float)s[i];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const double u = __shfl_xor(best, o, 64);
-      const int ua = __shfl_xor(at, o, 64);
-      const float us = __shfl_xor(score, o, 64);
-      if (ua != 0x7fffffff && (at == 0x7fffffff || u > best || (u == best && ua < at))) best = u, at = ua, score = us;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) allowed[i] = allowed[i] && lane * VPL + i != at;
-    if (lane == j) mine = score, expert = at;
+      if (lane * VPL + i == e) key[i] = kNone64;
+    if (lane == j) mine = scores[e], expert = e;
   }
   if (a.renormalize) {
     const float total = wave_sum(mine);
@@ -160,12 +211,278 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
   if (lane < a.topk) wo[lane] = mine * a.scale, eo[lane] = expert;
 }
 
-template <typename T>
+// For whatever the kernel below does not take.
+template <typename T, int VPL>
+__global__ __launch_bounds__(256) void k_route_exactly(RouteArgs a) {
+  __shared__ double shared[4][64 * VPL];
+  const int64_t t = block_of_grid() * 4 + (threadIdx.x >> 6);
+  if (t < a.T) route_exactly<T, VPL>(a, t, shared[threadIdx.x >> 6]);
+}
+
+constexpr int kNone = (int)0x80000000;  // below every value's key
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// L lanes per token, VPL experts each.  The comparisons are of 32-bit integers: the
+// value's bits in order, the lowest ones replaced by the place, inverted, so
+// that a maximum names its expert, and of equal ones the lowest.
+//
+// EXACT (16-bit logits without a bias): the value takes 16 or 19 bits, the
+// expert the last 10, and nothing is lost.  Else the values are c in 32 bits with the
+// lane's place in the last bits, and the choice holds if each of the first topk is
+// above the next by more than both c can be off.  With U = 2^-24: a product for
+// exp2's argument, its constant and its result make exp(x) off by (1.5 |x| + 2) U of
+// itself, so 1 / (1 + exp(-z)), with one sum and a reciprocal, is off by
+// (1.5 |z| + 2) U s (1 - s) + 3 U s < 2^-22, and a softmax, whose sum adds the mean of its
+// terms' errors (2.5 ln E + 2) U and its additions' 22 U, by less than 2^-18 of the
+// largest score.  fp32 logits without a bias are compared as they are.  A row that
+// does not pass (one in 400 for random fp32 logits and biases) is done again in 64 bits.
+//
+// Groups have to be whole lanes (VPL 2^p experts); a group's two best are taken in
+// 32 bits, and the line between the kept and the others is checked likewise (scores
+// without a bias are off by 1.5 |z| U < 2^-16.9 of themselves, or by 2^-126).
+template <typename T, int L, int VPL, bool EXACT>
+__global__ __launch_bounds__(256) void k_route(RouteArgs a) {
+  constexpr int kExact = L == 16 ? VPL < 4 ? 1 : VPL / 4 : VPL;  // experts per lane of a whole wave
+  constexpr int kPlace = EXACT ? 1023 : VPL - 1;
+  constexpr int kChunks = VPL * (int)sizeof(T) / 16;  // of 16 bytes per lane
+  constexpr int kShared = 64 * (kChunks > 1 && 2 * kChunks > kExact ? 2 * kChunks : kExact);
+  __shared__ double shared[4][kShared];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l = lane & (L - 1);
+  const int e0 = l * VPL;
+  const int64_t t0 = (block_of_grid() * 4 + w) * (64 / L);
+  if (t0 >= a.T) return;  // whole waves, which meet at no barrier
+  const int64_t mine = t0 + lane / L, t = mine < a.T ? mine : a.T - 1;
+  const T* row = reinterpret_cast<const T*>(a.logits) + t * a.ld;
+  const bool masked = a.mask && a.mask[t];
+  T raw[VPL];
+  if constexpr (kChunks > 1) {
+    // The token's lanes read it 16 bytes next to one another, and take their own
+    // experts from LDS; chunk q lies where 16 lanes' reads meet 64 banks.
+    typedef uint32_t U4a __attribute__((ext_vector_type(4)));
+    U4a* rows = reinterpret_cast<U4a*>(shared[w]) + lane / L * (L * kChunks);
+    const auto place = [](int q) { return (q & ~(kChunks - 1)) | ((q + (q >> 4)) & (kChunks - 1)); };
+    constexpr int CE = 16 / (int)sizeof(T);
+    U4a got[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int at = (k * L + l) * CE;
+      if (at + CE <= a.E) {
+        __builtin_memcpy(&got[k], row + at, 16);
+      } else {
+        T v[CE];
+#pragma unroll
+        for (int i = 0; i < CE; ++i) v[i] = row[at + i < a.E ? at + i : 0];
+        __builtin_memcpy(&got[k], v, 16);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) rows[place(k * L + l)] = got[k];
+    wave_sync();
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      got[k] = rows[place(l * kChunks + k)];
+      __builtin_memcpy(raw + k * CE, &got[k], 16);
+    }
+  } else if (e0 + VPL <= a.E) {
+    __builtin_memcpy(raw, row + e0, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) raw[i] = row[e0 + i < a.E ? e0 + i : 0];
+  }
+  float b[VPL];
+  if (!EXACT && a.bias) {
+    if (e0 + VPL <= a.E) {
+      __builtin_memcpy(b, a.bias + e0, sizeof(b));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) b[i] = a.bias[e0 + i < a.E ? e0 + i : 0];
+    }
+  }
+  const auto larger = [](float x, float y) { return x > y ? x : y; };
+  const auto plus = [](float x, float y) { return x + y; };
+  const auto more = [](int x, int y) { return x > y ? x : y; };
+  float c[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) c[i] = e0 + i < a.E ? (float)raw[i] + 0.0f : -kInf;  // of two zeros none is larger
+  bool bad = false;
+  float top = -kInf;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    bad |= !(c[i] < kInf);
+    top = larger(c[i], top);
+  }
+  const bool softmax = a.score == FBG_SCORE_SOFTMAX;
+  float total = 1.0f;
+  if (softmax) {
+    top = over_lanes<L>(top, larger);
+    bad |= top == -kInf;
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) total += fast_exp(c[i] - top);
+    total = over_lanes<L>(total, plus);
+  }
+  const float inverse = 1.0f / total;
+  const auto score_of = [&](float z) {
+    return softmax ? fast_exp(z - top) * inverse : __builtin_amdgcn_rcpf(1.0f + fast_exp(-z));
+  };
+  // How far a score may be off, and c by more than its own rounding.
+  const float off = EXACT || !a.bias ? 0.0f : softmax ? 0x1p-18f * inverse : 0x1p-22f;
+  if (!EXACT && a.bias) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      bad |= !(b[i] < kInf);
+      c[i] = score_of(c[i]) + b[i];
+      if (e0 + i >= a.E) c[i] = -kInf;
+    }
+  }
+  bool sure = true;
+  bool kept = true;
+  if (a.groups > 1) {
+    float best = -kInf, second = -kInf;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      second = __builtin_amdgcn_fmed3f(best, second, c[i]);
+      best = larger(best, c[i]);
+    }
+    // Over the lanes of a group; after each step those of half a group agree.
+    const auto join = [&](float u, float v) {
+      second = larger(best < u ? best : u, larger(second, v));
+      best = larger(best, u);
+    };
+    if (a.group_lanes > 1) join(dpp<0xb1>(best), dpp<0xb1>(second));
+    if (a.group_lanes > 2) join(dpp<0x4e>(best), dpp<0x4e>(second));
+    if (a.group_lanes > 4) join(dpp<0x141>(best), dpp<0x141>(second));
+    if (a.group_lanes > 8) join(dpp<0x140>(best), dpp<0x140>(second));
+    if (L == 64 && a.group_lanes > 16) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
+    const bool two = a.group_score == FBG_GROUP_TOP2;
+    float value = best;
+    if (two) {
+      const bool scored = EXACT || !a.bias;
+      value = scored ? score_of(best) : best;
+      if (a.E > a.groups) value += scored ? score_of(second) : second;
+    }
+    if (e0 >= a.E) value = -kInf;
+    int better = 0;  // groups that come before this lane's
+    for (int o = a.group_lanes; o < L; o += a.group_lanes) {
+      const int other = (l + o) & (L - 1);
+      const float u = __shfl(value, other + (lane & ~(L - 1)), 64);
+      better += u > value || (u == value && other < l);
+    }
+    kept = better < a.topk_groups;
+    if (two || off > 0.0f) {
+      // The last that stays and the first that does not.
+      const auto value_at = [&](int rank) {
+        const uint64_t at = __ballot(better == rank) >> (L == 64 ? 0 : lane & 48);
+        return __shfl(value, (int)__builtin_ctzll(at | 1ull << 63) + (lane & ~(L - 1)), 64);
+      };
+      const float low = value_at(a.topk_groups - 1), high = value_at(a.topk_groups);
+      const float relative = off > 0.0f ? 0x1p-22f : 0x1p-16f;
+      sure = low - high > relative * (__builtin_fabsf(low) + __builtin_fabsf(high)) + 4.0f * off + 0x1p-120f || high == -kInf;
+    }
+  }
+  int key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int place = EXACT ? 1023 - (e0 + i) : VPL - 1 - i;
+    key[i] = kept && e0 + i < a.E ? (ordered(c[i]) & ~kPlace) | place : kNone;
+  }
+  int rank_key = kNone, expert = 0;
+  const int rounds = a.topk + (EXACT ? 0 : 1);
+  for (int r = 0; r < rounds; ++r) {
+    int m = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = more(m, key[i]);
+    const int local = m;
+    m = over_lanes<L>(m, more);
+    int e, gone = m;
+    if constexpr (EXACT) {
+      e = 1023 - (m & 1023);
+    } else {
+      const uint64_t holds = __ballot(local == m);
+      int winner;
+      if constexpr (L == 64) winner = __builtin_ctzll(holds);
+      else winner = __builtin_ctz((uint32_t)(holds >> (lane & 48)) & 0xffff);
+      e = winner * VPL + (VPL - 1 - (m & kPlace));
+      gone = l == winner ? m : kNone;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = key[i] == gone ? kNone : key[i];
+    if (l == r) rank_key = m, expert = e;
+  }
+  // Lane l has the token's expert number l, and lane topk the first of the others.
+  expert = expert < a.E ? expert : a.E - 1;
+  const float z = l < rounds ? (float)row[expert] : 0.0f;
+  if constexpr (!EXACT) {
+    float v = z, most = 0.0f;
+    if (a.bias && l < rounds) {
+      v = score_of(z) + a.bias[expert];
+      most = off + 0x1p-24f * __builtin_fabsf(v);
+    }
+    // What is behind the first of the others is at most its key's value and all
+    // that the place took from another's.
+    if (l == a.topk) v = unordered(rank_key | kPlace);
+    const float gap = v - __shfl(v, lane + 1, 64), lim = most + __shfl(most, lane + 1, 64);
+    const bool last = __shfl(rank_key, lane + 1, 64) == kNone;
+    if (l < a.topk && !last) sure = sure && gap > lim;
+  }
+  float weight = 0.0f;
+  if (l < a.topk) {
+    weight = softmax ? expf(z - top) * inverse : z < 0.0f ? expf(z) / (1.0f + expf(z)) : 1.0f / (1.0f + expf(-z));
+  }
+  if (a.renormalize) {
+    const float sum = over_lanes<L>(weight, plus);
+    weight = weight / (sum < 1e-20f ? 1e-20f : sum);
+  }
+  weight *= a.scale;
+  const uint64_t token = L == 64 ? ~0ull : 0xffffull << (lane & 48);
+  if (__ballot(bad) & token) weight = __builtin_nanf(""), expert = l, sure = true;
+  if (masked) weight = 0.0f, expert = -1, sure = true;
+  const uint64_t unsure = __ballot(!sure && mine < a.T);
+  if (mine < a.T && l < a.topk && !(unsure & token)) {
+    a.weights[t * a.topk + l] = weight;
+    a.experts[t * a.topk + l] = expert;
+  }
+  for (int i = 0; i < 64 / L; ++i)
+    if (unsure & ((L == 64 ? ~0ull : 0xffffull) << (i * L & 63))) route_exactly<T, kExact>(a, t0 + i, shared[w]);
+}
+
+template <typename T, int L, int VPL>
 hipError_t route(const RouteArgs& a) {
+  const dim3 g = wide_grid(((int64_t)a.T * L + 255) / 256), b(256);
+  if constexpr (sizeof(T) == 2) {
+    if (!a.bias) {
+      hipLaunchKernelGGL((k_route<T, L, VPL, true>), g, b, 0, a.stream, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_route<T, L, VPL, false>), g, b, 0, a.stream, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t route(RouteArgs a) {
+  // Whether L lanes of vpl experts hold whole groups and a rank for every choice.
+  const auto fits = [&](int L, int vpl) {
+    if (a.E > L * vpl || a.topk >= L) return false;
+    if (a.groups == 1) return true;
+    const int size = a.E / a.groups, lanes = size / vpl;
+    a.group_lanes = lanes;
+    return size % vpl == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 32;
+  };
+  // Many tokens: four to a wave.  Few: a wave each, for its shorter way to an answer.
+  if (a.T > 1024) {
+    if (fits(16, 4)) return route<T, 16, 4>(a);
+    if (fits(16, 16)) return route<T, 16, 16>(a);
+  }
+  if (fits(64, 1)) return route<T, 64, 1>(a);
+  if (fits(64, 4)) return route<T, 64, 4>(a);
+  if (fits(64, 16)) return route<T, 64, 16>(a);
   const dim3 g = wide_grid(((int64_t)a.T + 3) / 4), b(256);
-  if (a.E <= 64) hipLaunchKernelGGL((k_route<T, 1>), g, b, 0, a.stream, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((k_route<T, 4>), g, b, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_route<T, 16>), g, b, 0, a.stream, a);
+  if (a.E <= 64) hipLaunchKernelGGL((k_route_exactly<T, 1>), g, b, 0, a.stream, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((k_route_exactly<T, 4>), g, b, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_route_exactly<T, 16>), g, b, 0, a.stream, a);
   return hipGetLastError();
 }
 

@@ -127,6 +127,7 @@ struct RouteArgs {
   int64_t ld;
   int T, E, topk;
   int groups, topk_groups;
+  int group_lanes;  // lanes that hold a group (launch_route sets it)
   int dtype, score, group_score, renormalize;
   float scale;
   hipStream_t stream;
