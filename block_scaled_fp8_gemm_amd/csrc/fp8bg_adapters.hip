@@ -100,8 +100,9 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
   float* h = a.h + ((int64_t)split * a.M + m0 + j) * a.pitch;
   for_passes(id, worker, a.workers, [&](int cur) {
     const bool mine = id == cur;
+    const uint64_t meant = __ballot(mine);  // asked of all lanes: not inside the choice below
     // Lanes of other tokens read the row of one that is meant.
-    const int64_t m = m0 + (mine ? j : __builtin_ctzll(__ballot(mine)));
+    const int64_t m = m0 + (mine ? j : __builtin_ctzll(meant));
     const T* x = reinterpret_cast<const T*>(a.x) + m * a.ldx;
     const T* A = reinterpret_cast<const T*>(a.A) + (int64_t)cur * a.R * a.K;
     for (int r0 = 0; r0 < a.R; r0 += 16 * RT) {
