@@ -17,7 +17,6 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxSplits = 4;
-constexpr int kFewTiles = 64;  // tiles of 16 tokens
 
 // Grids: splits of K or blocks of columns along x, tiles of 16 tokens along y
 // and, past kGridY of them, z; with several workers per tile they stand along z.
@@ -69,15 +68,14 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs& a, int64_t m) {
 }
 
 // The passes of a tile of 16 tokens: one for each different adapter among them.
-// One worker does them all; of several (as many as a tile can have passes)
-// number `worker` does the one of that number.
+// Of `workers` (a power of two) number `worker` does every workers-th.
 template <typename F>
 __device__ __forceinline__ void for_passes(int id, int worker, int workers, const F& pass) {
   uint64_t todo = __ballot(id >= 0) & 0xffff;
   for (int p = 0; todo; ++p) {
     const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     todo &= ~__ballot(id == cur);
-    if (workers == 1 || p == worker) pass(cur);
+    if ((p & (workers - 1)) == worker) pass(cur);
   }
 }
 
@@ -162,30 +160,45 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
   });
 }
 
-// How k_expand reads the ranks of a weight row: all of RT * 16 in chunks of four,
-// any number from four on in such chunks (the last one taken from the row's
-// end and shifted), or fewer than four one by one.
+// h in the weights' type, as a sum that the MFMA takes term by term: each term
+// is what the ones before it leave, rounded.  bf16 has fp32's range: two terms are
+// off by 2^-18 of a value, which a 16-bit output does not see, three by 2^-26.  fp16
+// goes relative to the largest of a token's ranks (`unit`, a power of two), the second
+// term times 2^11 to stay above its smallest steps, with sums of its own: off
+// by 2^-22.
+template <typename T, typename O> struct Terms;
+template <typename O> struct Terms<__bf16, O> {
+  static constexpr int kCount = sizeof(O) == 4 ? 3 : 2, kSums = 1;
+};
+template <typename O> struct Terms<_Float16, O> {
+  static constexpr int kCount = 2, kSums = 2;
+};
+
+// How the eight ranks of a lane are read: in one piece where R is a multiple of
+// eight; else as two of four, the row's last four shifted to where they belong; fewer
+// than four one by one.
 enum Ranks { kWhole, kPart, kTiny };
 
 // 16 tokens by blocks of 64 columns, four blocks next to one another on the
 // four waves.  Row i of the first operand's tile t is column 32 (t / 2) + 8 (i / 4) +
 // 4 (t % 2) + i % 4 of the block, so that a lane's results are of one token and 8
-// columns next to one another, twice.  h stays in fp32: the fp32 MFMA takes it
-// and the weights as they are.  Each token belongs to one pass, which alone
-// writes its row; the first worker writes the rows without an adapter.  DEEP:
-// the ranks in steps of 16 RT, h read again for each block of columns.
+// columns next to one another, twice.  Each token belongs to one pass, which
+// alone writes its row; the first worker writes the rows without an adapter.  NC
+// chunks of 32 ranks at a time; DEEP: more than those, h read again for each block
+// of columns.
 //
 // The loads of the next block are in flight while one is computed: they stay
 // raw dwords until they are used, and have no branch between lanes (a lane of
 // another token reads the row of one that is meant), since the compiler waits
 // for a load where it unpacks its value or where the lanes meet again.  A last
 // block that N cuts goes element by element.
-template <typename T, typename O, int RT, bool DEEP, Ranks RANKS>
+template <typename T, typename O, int NC, bool DEEP, Ranks RANKS>
 __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   constexpr int YC = 2 * (int)sizeof(O) / 4;  // 16-byte chunks of 8 outputs
-  typedef T T4 __attribute__((ext_vector_type(4)));
-  typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+  constexpr int kTerms = Terms<T, O>::kCount, kSums = Terms<T, O>::kSums;
+  typedef typename Vec8<T>::type V;
   typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+  typedef uint64_t L2 __attribute__((ext_vector_type(2)));
   typedef O O8 __attribute__((ext_vector_type(8)));
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int worker = worker_of(a.workers);
@@ -196,7 +209,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   const int id = adapter_of(a, m0 + j);
   const int column = 8 * (j >> 2) + (j & 3);
   struct Weights {
-    U2 v[RT][4];
+    L2 v[NC][4];
   };
   struct Outputs {
     U4 v[2][YC];
@@ -208,13 +221,13 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
     return y;
   };
   for_passes(id, worker, a.workers, [&](int cur) {
-    const uint64_t meant = __ballot(id == cur);
     const bool mine = id == cur;
+    const uint64_t meant = __ballot(mine);
     const int64_t m = m0 + (mine ? j : __builtin_ctzll(meant));
     const O* yrow = reinterpret_cast<const O*>(a.y) + m * a.ldy;
     O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
     const T* B = reinterpret_cast<const T*>(a.B) + (int64_t)cur * a.N * a.R;
-    const float* hrow = a.h + m * a.pitch + 4 * g;
+    const float* hrow = a.h + m * a.pitch;
     const int64_t h_split = (int64_t)a.M * a.pitch;
     const auto load_b = [&](int64_t n0, int r0) {
       Weights b;
@@ -225,79 +238,138 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
         const int n = 32 * (t >> 1) + 4 * (t & 1) + column;
         const T* row = base + (n < most ? n : most) * a.R;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const int r = r0 + 16 * i + 4 * g;
+        for (int c = 0; c < NC; ++c) {
+          const int r = r0 + 32 * c + 8 * g;
           if constexpr (RANKS == kTiny) {
-            T4 v;
+            T v[8] = {};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = row[k < a.R ? k : 0];
-            b.v[i][t] = __builtin_bit_cast(U2, v);
+            for (int k = 0; k < 3; ++k) v[k] = row[k < a.R ? k : 0];
+            __builtin_memcpy(&b.v[c][t], v, 16);
+          } else if constexpr (RANKS == kWhole) {
+            __builtin_memcpy(&b.v[c][t], row + (r < a.R ? r : 0), 16);
           } else {
-            __builtin_memcpy(&b.v[i][t], row + (RANKS == kWhole || r < a.R - 4 ? r : a.R - 4), 8);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint64_t v;
+              __builtin_memcpy(&v, row + (r + 4 * k < a.R - 4 ? r + 4 * k : a.R - 4), 8);
+              b.v[c][t][k] = v;
+            }
           }
         }
       }
       return b;
     };
-    const auto load_h = [&](int r0, float scale, v4f (&h)[RT]) {
+    // A lane's weights, zeros from rank R on.
+    const auto weights = [&](const L2& raw, int r) {
+      L2 v = raw;
+      if constexpr (RANKS == kWhole) {
+        if (r >= a.R) v = L2{0, 0};
+      } else if constexpr (RANKS == kTiny) {
+        v = r == 0 ? L2{v[0] & ((1ull << (16 * a.R)) - 1), 0} : L2{0, 0};
+      } else {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        v4f part[kMaxSplits];
-#pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-          if (s < a.splits) part[s] = *reinterpret_cast<const v4f*>(hrow + s * h_split + r0 + 16 * i);
-        h[i] = part[0];
-#pragma unroll
-        for (int s = 1; s < kMaxSplits; ++s)
-          if (s < a.splits) h[i] += part[s];
-        h[i] *= scale;
-      }
-    };
-    const auto multiply = [&](const Weights& b, int r0, const v4f (&h)[RT], v4f (&acc)[4]) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float w[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint64_t bits = __builtin_bit_cast(uint64_t, b.v[i][t]);
-          const int r = r0 + 16 * i + 4 * g;
-          if constexpr (RANKS == kPart) {  // zeros come in behind the last rank
-            const int past = r > a.R - 4 ? r - (a.R - 4) : 0;
-            bits = past < 4 ? bits >> (16 * past) : 0;
-          } else if constexpr (RANKS == kTiny) {
-            bits = r == 0 ? bits & ((1ull << (16 * a.R)) - 1) : 0;
-          }
-          const T4 v = __builtin_bit_cast(T4, bits);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) w[t][u] = (float)v[u];
+        for (int k = 0; k < 2; ++k) {
+          const int past = r + 4 * k > a.R - 4 ? r + 4 * k - (a.R - 4) : 0;
+          v[k] = past < 4 ? v[k] >> (16 * past) : 0;
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t][u], h[i][u], acc[t], 0, 0, 0);
       }
+      return __builtin_bit_cast(V, v);
     };
     const float scale = a.scales ? a.scales[cur] : 1.0f;
-    v4f h[RT];
+    V h[NC][kTerms];
+    float unit = 1.0f;
+    const auto load_h = [&](int r0) {
+      float v[NC][8];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int r = r0 + 32 * c + 8 * g;
+        v4f part[kMaxSplits][2];
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+          if (s < a.splits) __builtin_memcpy(part[s], hrow + s * h_split + (r < a.pitch ? r : 0), 32);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int s = 1; s < kMaxSplits; ++s)
+            if (s < a.splits) part[0][k] += part[s][k];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[c][4 * k + i] = r < a.pitch ? part[0][k][i] * scale : 0.0f;
+        }
+      }
+      if constexpr (kSums == 2) {
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(v[c][i]));
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        // The power of two at or below it, kept where it and its inverse are normal.
+        const uint32_t e = __float_as_uint(top) & 0x7f800000u;
+        unit = __uint_as_float(e < 0x01000000u ? 0x01000000u : e > 0x7e000000u ? 0x7e000000u : e);
+        const float inverse = 1.0f / unit;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[c][i] *= inverse;
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float rest = v[c][i];
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) {
+            const T term = (T)rest;
+            h[c][t][i] = term;
+            rest = (rest - (float)term) * (kSums == 2 ? 2048.0f : 1.0f);
+          }
+        }
+    };
+    const auto multiply = [&](const Weights& b, int r0, v4f (&acc)[4]) {
+      v4f sum[kSums][4] = {};
+      if constexpr (kSums == 1) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sum[0][t] = acc[t];
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        V w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = weights(b.v[c][t], r0 + 32 * c + 8 * g);
+#pragma unroll
+        for (int i = kTerms - 1; i >= 0; --i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            v4f& to = sum[kSums == 2 ? i : 0][t];
+            to = mfma32(w[t], h[c][i], to);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (kSums == 1) acc[t] = sum[0][t];
+        else acc[t] += (sum[0][t] + sum[1][t] * 0x1p-11f) * unit;
+      }
+    };
     // The products of one block, the weights of its first ranks in hand.
     const auto block = [&](int64_t n0, const Weights& b, v4f (&acc)[4]) {
       if constexpr (DEEP) {
         Weights now = b;
-        for (int r0 = 0; r0 < a.R; r0 += 16 * RT) {
-          load_h(r0, scale, h);
-          const Weights then = load_b(n0, r0 + 16 * RT < a.R ? r0 + 16 * RT : r0);
-          multiply(now, r0, h, acc);
+        for (int r0 = 0; r0 < a.R; r0 += 32 * NC) {
+          const Weights then = load_b(n0, r0 + 32 * NC < a.R ? r0 + 32 * NC : r0);
+          load_h(r0);
+          multiply(now, r0, acc);
           now = then;
         }
       } else {
-        multiply(b, 0, h, acc);
+        multiply(b, 0, acc);
       }
     };
     Weights b = load_b(n_first, 0);
     Outputs y;
     int64_t n0 = n_first;
     if (n0 + 64 <= n_last) y = load_y(yrow, n0);
-    if constexpr (!DEEP) load_h(0, scale, h);
+    if constexpr (!DEEP) load_h(0);
     // A lane's results are of its own token: those of the others' adapters,
     // which may hold infinities, go nowhere.
     for (; n0 + 64 <= n_last; n0 += 256) {
@@ -359,21 +431,19 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   }
 }
 
-template <typename T, typename O>
+template <typename T, typename O, Ranks RANKS>
 void expand(const AdapterArgs& a, dim3 g) {
   const dim3 b(256);
-  if (a.R % 16 == 0) {
-    if (a.R == 16) hipLaunchKernelGGL((k_expand<T, O, 1, false, kWhole>), g, b, 0, a.stream, a);
-    else if (a.R == 32) hipLaunchKernelGGL((k_expand<T, O, 2, false, kWhole>), g, b, 0, a.stream, a);
-    else if (a.R == 64) hipLaunchKernelGGL((k_expand<T, O, 4, false, kWhole>), g, b, 0, a.stream, a);
-    else hipLaunchKernelGGL((k_expand<T, O, 1, true, kWhole>), g, b, 0, a.stream, a);
-  } else if (a.R < 4) {
-    hipLaunchKernelGGL((k_expand<T, O, 1, false, kTiny>), g, b, 0, a.stream, a);
-  } else if (a.R < 16) {
-    hipLaunchKernelGGL((k_expand<T, O, 1, false, kPart>), g, b, 0, a.stream, a);
-  } else {
-    hipLaunchKernelGGL((k_expand<T, O, 1, true, kPart>), g, b, 0, a.stream, a);
-  }
+  if (a.R <= 32) hipLaunchKernelGGL((k_expand<T, O, 1, false, RANKS>), g, b, 0, a.stream, a);
+  else if (a.R <= 64) hipLaunchKernelGGL((k_expand<T, O, 2, false, RANKS>), g, b, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_expand<T, O, 2, true, RANKS>), g, b, 0, a.stream, a);
+}
+
+template <typename T, typename O>
+void expand(const AdapterArgs& a, dim3 g) {
+  if (a.R < 4) hipLaunchKernelGGL((k_expand<T, O, 1, false, kTiny>), g, dim3(256), 0, a.stream, a);
+  else if (a.R % 8 == 0) expand<T, O, kWhole>(a, g);
+  else expand<T, O, kPart>(a, g);
 }
 
 template <typename T>
@@ -381,8 +451,8 @@ hipError_t add(AdapterArgs a) {
   const int64_t tiles = ((int64_t)a.M + 15) / 16;
   // Few tokens: a worker for each adapter that a tile may hold.  Many: the
   // tiles cover the device, and their tokens come in runs.
-  const bool few = tiles <= kFewTiles;
-  a.workers = !few ? 1 : a.M < 16 ? a.M : 16;
+  a.workers = tiles <= 64 ? 16 : tiles <= 512 ? 4 : 1;
+  while (a.workers / 2 >= a.M) a.workers /= 2;
   if (a.R > 0 && a.L > 0 && a.K > 0) {
     const dim3 g = tile_grid(a.splits, tiles, a.workers);
     const dim3 b(256);
