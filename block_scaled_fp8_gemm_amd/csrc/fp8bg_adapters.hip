@@ -6,6 +6,8 @@
 // with B[a] added to y.  A tile holds 16 tokens whatever their adapters; it
 // goes over the different ones among them, so that tokens share an adapter's
 // reads wherever they stand, and a run of one adapter is one pass.
+#include <type_traits>
+
 #include "fp8bg_device.hpp"
 #include "fp8bg_internal.h"
 
@@ -17,6 +19,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxSplits = 4;
+constexpr int kFewTiles = 200;  // tiles of 16 tokens
 
 // Grids: splits of K or blocks of columns along x, tiles of 16 tokens along y
 // and, past kGridY of them, z; with several workers per tile they stand along z.
@@ -26,8 +29,8 @@ inline dim3 tile_grid(int64_t x, int64_t tiles, int workers) {
   const int64_t y = tiles < kGridY ? tiles : kGridY;
   return dim3((unsigned)x, (unsigned)y, workers > 1 ? (unsigned)workers : (unsigned)((tiles + y - 1) / y));
 }
-__device__ __forceinline__ int64_t first_token(int workers) {
-  return ((workers > 1 ? 0 : (int64_t)blockIdx.z * kGridY) + blockIdx.y) * 16;
+__device__ __forceinline__ int64_t tile_of(int workers) {
+  return (workers > 1 ? 0 : (int64_t)blockIdx.z * kGridY) + blockIdx.y;
 }
 __device__ __forceinline__ int worker_of(int workers) { return workers > 1 ? blockIdx.z : 0; }
 
@@ -67,93 +70,112 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs& a, int64_t m) {
   return id >= 0 && id < a.L ? id : -1;
 }
 
-// The passes of a tile of 16 tokens: one for each different adapter among them.
-// Of `workers` (a power of two) number `worker` does every workers-th.
-template <typename F>
+// The passes of a tile of 16 MT tokens (lane l holds the adapter of token l of
+// them, or l modulo their number): one for each different adapter, with the mask
+// of its tokens.  Of `workers` (a power of two) number `worker` does every
+// workers-th.
+template <int MT, typename F>
 __device__ __forceinline__ void for_passes(int id, int worker, int workers, const F& pass) {
-  uint64_t todo = __ballot(id >= 0) & 0xffff;
+  uint64_t todo = __ballot(id >= 0) & (MT == 4 ? ~0ull : (1ull << (16 * MT & 63)) - 1);
   for (int p = 0; todo; ++p) {
     const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    todo &= ~__ballot(id == cur);
-    if ((p & (workers - 1)) == worker) pass(cur);
+    const uint64_t meant = todo & __ballot(id == cur);
+    todo &= ~meant;
+    if ((p & (workers - 1)) == worker) pass(cur, meant);
   }
 }
 
-// h of 16 tokens over one slice of K for one adapter of theirs, or each in
-// turn; the waves split the slice, and their sums meet in LDS.  RT tiles
-// of 16 ranks at a time; the loads of U steps are in flight together.
-template <typename T, int RT>
+// h of 16 MT tokens over one slice of K for one adapter of theirs, or each in
+// turn; the waves split the slice, and their sums meet in LDS.  RT tiles of 16
+// ranks at a time; the loads of U steps are in flight together.  Many tokens
+// take MT = 4, which reads the adapter's rows from L2 once for 64 tokens (16384
+// tokens of rank 64: 16 tokens' workgroups read 537 MB of them).
+template <typename T, int RT, int MT>
 __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
-  constexpr int W = 4;
-  constexpr int U = RT == 1 ? 8 : 4;
+  constexpr int W = 4, TM = 16 * MT;
+  constexpr int U = MT > 1 ? 2 : RT > 1 ? 4 : 8;
   typedef typename Vec8<T>::type V;
-  __shared__ v4f part[RT][W][64];  // [tile of 16 ranks][wave][lane]
+  __shared__ v4f part[RT * MT][W][64];  // [tile of 16 ranks by 16 tokens][wave][lane]
   const int split = blockIdx.x, worker = worker_of(a.workers);
-  const int64_t m0 = first_token(a.workers);
+  const int64_t m0 = tile_of(a.workers) * TM;
   if (m0 >= a.M) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
-  const int id = adapter_of(a, m0 + j);
+  const int id = adapter_of(a, m0 + (lane & (TM - 1)));
   const int first = (split * W + w) * a.share;
   const int last = first + a.share < a.K ? first + a.share : a.K;
-  float* h = a.h + ((int64_t)split * a.M + m0 + j) * a.pitch;
-  for_passes(id, worker, a.workers, [&](int cur) {
-    const bool mine = id == cur;
-    const uint64_t meant = __ballot(mine);  // asked of all lanes: not inside the choice below
-    // Lanes of other tokens read the row of one that is meant.
-    const int64_t m = m0 + (mine ? j : __builtin_ctzll(meant));
-    const T* x = reinterpret_cast<const T*>(a.x) + m * a.ldx;
+  for_passes<MT>(id, worker, a.workers, [&](int cur, uint64_t meant) {
+    const T* x[MT];
+    bool some[MT];  // a tile of tokens without this adapter is left out
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint32_t bits = (uint32_t)(meant >> (16 * t)) & 0xffff;
+      some[t] = MT == 1 || bits;
+      // Lanes of other tokens read the row of one that is meant.
+      const int at = (bits >> j) & 1 ? j : __builtin_ctz(bits | 0x10000) & 15;
+      const int64_t m = m0 + 16 * t + at < a.M ? m0 + 16 * t + at : a.M - 1;
+      x[t] = reinterpret_cast<const T*>(a.x) + m * a.ldx;
+    }
     const T* A = reinterpret_cast<const T*>(a.A) + (int64_t)cur * a.R * a.K;
     for (int r0 = 0; r0 < a.R; r0 += 16 * RT) {
       const T* row[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) row[i] = A + (int64_t)(r0 + 16 * i + j < a.R ? r0 + 16 * i + j : a.R - 1) * a.K;
-      v4f acc[RT] = {};
-      int k = first;
-      for (; k + 32 * U <= last; k += 32 * U) {
-        V xf[U], af[U][RT];
+      v4f acc[MT][RT] = {};
+      const auto steps = [&](int k, auto count) {
+        constexpr int N = decltype(count)::value;
+        V xf[MT][N], af[N][RT];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          __builtin_memcpy(&xf[u], x + k + 32 * u + 8 * g, 16);
+        for (int u = 0; u < N; ++u) {
 #pragma unroll
           for (int i = 0; i < RT; ++i) __builtin_memcpy(&af[u][i], row[i] + k + 32 * u + 8 * g, 16);
         }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          if (some[t]) {
+#pragma unroll
+            for (int u = 0; u < N; ++u) __builtin_memcpy(&xf[t][u], x[t] + k + 32 * u + 8 * g, 16);
+          }
         __builtin_amdgcn_sched_barrier(0);  // all loads before the first use of one
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int t = 0; t < MT; ++t)
+          if (some[t]) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i) acc[i] = mfma32(af[u][i], xf[u], acc[i]);
-      }
-      for (; k + 64 <= last; k += 64) {
-        V xf[2], af[2][RT];
+            for (int u = 0; u < N; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          __builtin_memcpy(&xf[u], x + k + 32 * u + 8 * g, 16);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) __builtin_memcpy(&af[u][i], row[i] + k + 32 * u + 8 * g, 16);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) acc[i] = mfma32(af[u][i], xf[u], acc[i]);
-      }
+              for (int i = 0; i < RT; ++i) acc[t][i] = mfma32(af[u][i], xf[t][u], acc[t][i]);
+          }
+      };
+      int k = first;
+      for (; k + 32 * U <= last; k += 32 * U) steps(k, std::integral_constant<int, U>{});
+      for (; k + 64 <= last; k += 64) steps(k, std::integral_constant<int, 2>{});
       for (; k < last; k += 32) {
-        const V xf = load8(x, k + 8 * g, a.K);
+        V af[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = mfma32(load8(row[i], k + 8 * g, a.K), xf, acc[i]);
+        for (int i = 0; i < RT; ++i) af[i] = load8(row[i], k + 8 * g, a.K);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          if (some[t]) {
+            const V xf = load8(x[t], k + 8 * g, a.K);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[t][i] = mfma32(af[i], xf, acc[t][i]);
+          }
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) part[i][w][lane] = acc[i];
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) part[t * RT + i][w][lane] = acc[t][i];
       __syncthreads();
-      if (w < RT && r0 + 16 * w < a.R) {  // wave w: ranks r0 + 16 w ..
-        const int r = r0 + 16 * w + 4 * g;
-        v4f s = part[w][0][lane];
+      for (int q = w; q < MT * RT; q += W) {  // a wave: some of the tiles
+        const int t = q / RT, i = q % RT, r = r0 + 16 * i + 4 * g;
+        if (r0 + 16 * i >= a.R) continue;
+        v4f s = part[q][0][lane];
 #pragma unroll
-        for (int i = 1; i < W; ++i) s += part[w][i][lane];
+        for (int k = 1; k < W; ++k) s += part[q][k][lane];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (r + i >= a.R) s[i] = 0.0f;
-        if (mine) *reinterpret_cast<v4f*>(h + r) = s;
+        for (int k = 0; k < 4; ++k)
+          if (r + k >= a.R) s[k] = 0.0f;
+        const int m = 16 * t + j;
+        if ((meant >> m) & 1) *reinterpret_cast<v4f*>(a.h + ((int64_t)split * a.M + m0 + m) * a.pitch + r) = s;
       }
       __syncthreads();
     }
@@ -163,29 +185,134 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
 // h in the weights' type, as a sum that the MFMA takes term by term: each term
 // is what the ones before it leave, rounded.  bf16 has fp32's range: two terms are
 // off by 2^-18 of a value, which a 16-bit output does not see, three by 2^-26.  fp16
-// goes relative to the largest of a token's ranks (`unit`, a power of two), the second
-// term times 2^11 to stay above its smallest steps, with sums of its own: off
-// by 2^-22.
-template <typename T, typename O> struct Terms;
-template <typename O> struct Terms<__bf16, O> {
-  static constexpr int kCount = sizeof(O) == 4 ? 3 : 2, kSums = 1;
-};
-template <typename O> struct Terms<_Float16, O> {
-  static constexpr int kCount = 2, kSums = 2;
-};
+// goes relative to the largest of a token's 32 ranks (a power of two, returned), the
+// second term times 2^11 to stay above its smallest steps, with sums of its own:
+// off by 2^-22.
+template <typename T, typename O>
+constexpr int kTermsOf = std::is_same<T, __bf16>::value && sizeof(O) == 4 ? 3 : 2;
+
+template <typename T, int TERMS>
+__device__ __forceinline__ float split_terms(const float (&v)[8], typename Vec8<T>::type (&h)[TERMS]) {
+  constexpr bool kHalf = std::is_same<T, _Float16>::value;
+  float unit = 1.0f, inverse = 1.0f;
+  if constexpr (kHalf) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(v[i]));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    // The power of two at or below it, kept where it and its inverse are normal.
+    const uint32_t e = __float_as_uint(top) & 0x7f800000u;
+    unit = __uint_as_float(e < 0x01000000u ? 0x01000000u : e > 0x7e000000u ? 0x7e000000u : e);
+    inverse = 1.0f / unit;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float rest = v[i] * inverse;
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      const T term = (T)rest;
+      h[t][i] = term;
+      rest = (rest - (float)term) * (kHalf ? 2048.0f : 1.0f);
+    }
+  }
+  return unit;
+}
+
+// acc[t] += weights w[t] (rows) times h (columns: tokens).
+template <int TERMS, typename V>
+__device__ __forceinline__ void add_products(const V (&w)[4], const V (&h)[TERMS], float unit, v4f (&acc)[4]) {
+  if constexpr (std::is_same<V, v8h>::value) {
+    v4f first[4] = {}, second[4] = {};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) first[t] = mfma32(w[t], h[0], first[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) second[t] = mfma32(w[t], h[1], second[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[t] += (first[t] + second[t] * 0x1p-11f) * unit;
+  } else {
+#pragma unroll
+    for (int i = TERMS - 1; i >= 0; --i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = mfma32(w[t], h[i], acc[t]);
+  }
+}
+
+// h's ranks r .. r + 7 of one token, summed over the parts of K, times scale.
+__device__ __forceinline__ void load_hidden(const AdapterArgs& a, const float* row, int r, float scale, float (&v)[8]) {
+  v4f part[kMaxSplits][2];
+  const int64_t next = (int64_t)a.M * a.pitch;
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s)
+    if (s < a.splits) __builtin_memcpy(part[s], row + s * next + (r < a.pitch ? r : 0), 32);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int s = 1; s < kMaxSplits; ++s)
+      if (s < a.splits) part[0][k] += part[s][k];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * k + i] = r < a.pitch ? part[0][k][i] * scale : 0.0f;
+  }
+}
 
 // How the eight ranks of a lane are read: in one piece where R is a multiple of
 // eight; else as two of four, the row's last four shifted to where they belong; fewer
 // than four one by one.
 enum Ranks { kWhole, kPart, kTiny };
 
+typedef uint64_t L2 __attribute__((ext_vector_type(2)));
+
+// Ranks r .. r + 7 of the weights of a block's 64 columns from n0 on: row i of
+// tile t is column 32 (t / 2) + 8 (i / 4) + 4 (t % 2) + i % 4, so that a lane's results
+// are of one token and 8 columns next to one another, twice.  A column past the
+// last one reads the last one's.
+template <typename T, Ranks RANKS>
+__device__ __forceinline__ void load_weights(const T* B, int64_t n0, int N, int r, int R, int j, L2 (&v)[4]) {
+  const T* base = B + n0 * R;
+  const int most = N - n0 < 64 ? (int)(N - n0) - 1 : 63;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int n = 32 * (t >> 1) + 4 * (t & 1) + 8 * (j >> 2) + (j & 3);
+    const T* row = base + (n < most ? n : most) * R;
+    if constexpr (RANKS == kTiny) {
+      T u[8] = {};
+#pragma unroll
+      for (int k = 0; k < 3; ++k) u[k] = row[k < R ? k : 0];
+      __builtin_memcpy(&v[t], u, 16);
+    } else if constexpr (RANKS == kWhole) {
+      __builtin_memcpy(&v[t], row + (r < R ? r : 0), 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint64_t u;
+        __builtin_memcpy(&u, row + (r + 4 * k < R - 4 ? r + 4 * k : R - 4), 8);
+        v[t][k] = u;
+      }
+    }
+  }
+}
+
+// The same as the MFMA takes them, zeros from rank R on.
+template <typename T, Ranks RANKS>
+__device__ __forceinline__ typename Vec8<T>::type weights_of(L2 v, int r, int R) {
+  if constexpr (RANKS == kWhole) {
+    if (r >= R) v = L2{0, 0};
+  } else if constexpr (RANKS == kTiny) {
+    v = r == 0 ? L2{v[0] & ((1ull << (16 * R)) - 1), 0} : L2{0, 0};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int past = r + 4 * k > R - 4 ? r + 4 * k - (R - 4) : 0;
+      v[k] = past < 4 ? v[k] >> (16 * past) : 0;
+    }
+  }
+  return __builtin_bit_cast(typename Vec8<T>::type, v);
+}
+
 // 16 tokens by blocks of 64 columns, four blocks next to one another on the
-// four waves.  Row i of the first operand's tile t is column 32 (t / 2) + 8 (i / 4) +
-// 4 (t % 2) + i % 4 of the block, so that a lane's results are of one token and 8
-// columns next to one another, twice.  Each token belongs to one pass, which
-// alone writes its row; the first worker writes the rows without an adapter.  NC
-// chunks of 32 ranks at a time; DEEP: more than those, h read again for each block
-// of columns.
+// four waves.  Each token belongs to one pass, which alone writes its row; the
+// first worker writes the rows without an adapter.  NC chunks of 32 ranks at a
+// time; DEEP: more than those, h read again for each block of columns.
 //
 // The loads of the next block are in flight while one is computed: they stay
 // raw dwords until they are used, and have no branch between lanes (a lane of
@@ -195,19 +322,17 @@ enum Ranks { kWhole, kPart, kTiny };
 template <typename T, typename O, int NC, bool DEEP, Ranks RANKS>
 __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   constexpr int YC = 2 * (int)sizeof(O) / 4;  // 16-byte chunks of 8 outputs
-  constexpr int kTerms = Terms<T, O>::kCount, kSums = Terms<T, O>::kSums;
+  constexpr int kTerms = kTermsOf<T, O>;
   typedef typename Vec8<T>::type V;
   typedef uint32_t U4 __attribute__((ext_vector_type(4)));
-  typedef uint64_t L2 __attribute__((ext_vector_type(2)));
   typedef O O8 __attribute__((ext_vector_type(8)));
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int worker = worker_of(a.workers);
-  const int64_t m0 = first_token(a.workers), n_block = (int64_t)blockIdx.x * a.cols;
+  const int64_t m0 = tile_of(a.workers) * 16, n_block = (int64_t)blockIdx.x * a.cols;
   const int64_t n_first = n_block + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 64, n_end = n_block + a.cols;
   if (m0 >= a.M || n_first >= a.N) return;  // whole waves, which meet at no barrier
   const int64_t n_last = n_end < a.N ? n_end : a.N;
   const int id = adapter_of(a, m0 + j);
-  const int column = 8 * (j >> 2) + (j & 3);
   struct Weights {
     L2 v[NC][4];
   };
@@ -220,135 +345,37 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
     for (int q = 0; q < 2; ++q) __builtin_memcpy(y.v[q], row + n0 + 32 * q + 8 * g, sizeof(y.v[q]));
     return y;
   };
-  for_passes(id, worker, a.workers, [&](int cur) {
+  for_passes<1>(id, worker, a.workers, [&](int cur, uint64_t meant) {
     const bool mine = id == cur;
-    const uint64_t meant = __ballot(mine);
     const int64_t m = m0 + (mine ? j : __builtin_ctzll(meant));
     const O* yrow = reinterpret_cast<const O*>(a.y) + m * a.ldy;
     O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
     const T* B = reinterpret_cast<const T*>(a.B) + (int64_t)cur * a.N * a.R;
     const float* hrow = a.h + m * a.pitch;
-    const int64_t h_split = (int64_t)a.M * a.pitch;
     const auto load_b = [&](int64_t n0, int r0) {
       Weights b;
-      const T* base = B + n0 * a.R;
-      const int most = a.N - n0 < 64 ? (int)(a.N - n0) - 1 : 63;  // a column past the last one: the last one's
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int n = 32 * (t >> 1) + 4 * (t & 1) + column;
-        const T* row = base + (n < most ? n : most) * a.R;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int r = r0 + 32 * c + 8 * g;
-          if constexpr (RANKS == kTiny) {
-            T v[8] = {};
-#pragma unroll
-            for (int k = 0; k < 3; ++k) v[k] = row[k < a.R ? k : 0];
-            __builtin_memcpy(&b.v[c][t], v, 16);
-          } else if constexpr (RANKS == kWhole) {
-            __builtin_memcpy(&b.v[c][t], row + (r < a.R ? r : 0), 16);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint64_t v;
-              __builtin_memcpy(&v, row + (r + 4 * k < a.R - 4 ? r + 4 * k : a.R - 4), 8);
-              b.v[c][t][k] = v;
-            }
-          }
-        }
-      }
+      for (int c = 0; c < NC; ++c) load_weights<T, RANKS>(B, n0, a.N, r0 + 32 * c + 8 * g, a.R, j, b.v[c]);
       return b;
-    };
-    // A lane's weights, zeros from rank R on.
-    const auto weights = [&](const L2& raw, int r) {
-      L2 v = raw;
-      if constexpr (RANKS == kWhole) {
-        if (r >= a.R) v = L2{0, 0};
-      } else if constexpr (RANKS == kTiny) {
-        v = r == 0 ? L2{v[0] & ((1ull << (16 * a.R)) - 1), 0} : L2{0, 0};
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int past = r + 4 * k > a.R - 4 ? r + 4 * k - (a.R - 4) : 0;
-          v[k] = past < 4 ? v[k] >> (16 * past) : 0;
-        }
-      }
-      return __builtin_bit_cast(V, v);
     };
     const float scale = a.scales ? a.scales[cur] : 1.0f;
     V h[NC][kTerms];
-    float unit = 1.0f;
+    float unit[NC];
     const auto load_h = [&](int r0) {
-      float v[NC][8];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int r = r0 + 32 * c + 8 * g;
-        v4f part[kMaxSplits][2];
-#pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-          if (s < a.splits) __builtin_memcpy(part[s], hrow + s * h_split + (r < a.pitch ? r : 0), 32);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int s = 1; s < kMaxSplits; ++s)
-            if (s < a.splits) part[0][k] += part[s][k];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[c][4 * k + i] = r < a.pitch ? part[0][k][i] * scale : 0.0f;
-        }
+        float v[8];
+        load_hidden(a, hrow, r0 + 32 * c + 8 * g, scale, v);
+        unit[c] = split_terms<T, kTerms>(v, h[c]);
       }
-      if constexpr (kSums == 2) {
-        float top = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(v[c][i]));
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        // The power of two at or below it, kept where it and its inverse are normal.
-        const uint32_t e = __float_as_uint(top) & 0x7f800000u;
-        unit = __uint_as_float(e < 0x01000000u ? 0x01000000u : e > 0x7e000000u ? 0x7e000000u : e);
-        const float inverse = 1.0f / unit;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] *= inverse;
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float rest = v[c][i];
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            const T term = (T)rest;
-            h[c][t][i] = term;
-            rest = (rest - (float)term) * (kSums == 2 ? 2048.0f : 1.0f);
-          }
-        }
     };
     const auto multiply = [&](const Weights& b, int r0, v4f (&acc)[4]) {
-      v4f sum[kSums][4] = {};
-      if constexpr (kSums == 1) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) sum[0][t] = acc[t];
-      }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         V w[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = weights(b.v[c][t], r0 + 32 * c + 8 * g);
-#pragma unroll
-        for (int i = kTerms - 1; i >= 0; --i)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            v4f& to = sum[kSums == 2 ? i : 0][t];
-            to = mfma32(w[t], h[c][i], to);
-          }
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if constexpr (kSums == 1) acc[t] = sum[0][t];
-        else acc[t] += (sum[0][t] + sum[1][t] * 0x1p-11f) * unit;
+        for (int t = 0; t < 4; ++t) w[t] = weights_of<T, RANKS>(b.v[c][t], r0 + 32 * c + 8 * g, a.R);
+        add_products<kTerms>(w, h[c], unit[c], acc);
       }
     };
     // The products of one block, the weights of its first ranks in hand.
@@ -431,6 +458,164 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   }
 }
 
+// The same for many tokens: 16 MT of them to a workgroup, so that a block's weights
+// come from L2 once for all (rank 64 and 16384 tokens by 4096 columns: 16 tokens'
+// workgroups read 537 MB of them, twice the outputs).  h's terms are made once per pass
+// and stay in LDS; the ranks go in chunks of 32, any number of them.
+template <typename T, typename O, int MT, Ranks RANKS>
+__global__ __launch_bounds__(256) void k_expand_many(AdapterArgs a) {
+  constexpr int YC = 2 * (int)sizeof(O) / 4, TM = 16 * MT, kTerms = kTermsOf<T, O>;
+  typedef typename Vec8<T>::type V;
+  typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+  typedef O O8 __attribute__((ext_vector_type(8)));
+  extern __shared__ v4f staged[];  // [tile of tokens][chunk][term][lane], then the units [tile][chunk][16]
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
+  const int worker = worker_of(a.workers), chunks = (a.R + 31) / 32;
+  float* units = reinterpret_cast<float*>(staged + MT * chunks * kTerms * 64);
+  const int64_t m0 = tile_of(a.workers) * TM, n_block = (int64_t)blockIdx.x * a.cols;
+  if (m0 >= a.M) return;  // a whole workgroup
+  const int64_t n_first = n_block + w * 64, n_end = n_block + a.cols;
+  const int64_t n_last = n_end < a.N ? n_end : a.N;
+  const int id = adapter_of(a, m0 + (lane & (TM - 1)));
+  struct Outputs {
+    U4 v[2][YC];
+  };
+  const auto load_y = [&](const O* row, int64_t n0) {
+    Outputs y;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) __builtin_memcpy(y.v[q], row + n0 + 32 * q + 8 * g, sizeof(y.v[q]));
+    return y;
+  };
+  for_passes<MT>(id, worker, a.workers, [&](int cur, uint64_t meant) {
+    bool some[MT], mine[MT];
+    int64_t row_of[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint32_t bits = (uint32_t)(meant >> (16 * t)) & 0xffff;
+      some[t] = bits != 0;
+      mine[t] = (bits >> j) & 1;
+      // Lanes of other tokens read the row of one that is meant.
+      const int64_t m = m0 + 16 * t + (mine[t] ? j : __builtin_ctz(bits | 0x10000) & 15);
+      row_of[t] = m < a.M ? m : a.M - 1;
+    }
+    const T* B = reinterpret_cast<const T*>(a.B) + (int64_t)cur * a.N * a.R;
+    const float scale = a.scales ? a.scales[cur] : 1.0f;
+    for (int q = w; q < MT * chunks; q += 4) {  // a wave: some of the chunks
+      const int t = q / chunks, c = q % chunks;
+      if (!((meant >> (16 * t)) & 0xffff)) continue;
+      const uint32_t bits = (uint32_t)(meant >> (16 * t)) & 0xffff;
+      const int64_t m = m0 + 16 * t + ((bits >> j) & 1 ? j : __builtin_ctz(bits));
+      float v[8];
+      V h[kTerms];
+      load_hidden(a, a.h + m * a.pitch, 32 * c + 8 * g, scale, v);
+      const float unit = split_terms<T, kTerms>(v, h);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) __builtin_memcpy(&staged[(q * kTerms + i) * 64 + lane], &h[i], 16);
+      if (g == 0) units[q * 16 + j] = unit;
+    }
+    __syncthreads();
+    const auto products = [&](const L2 (&raw)[4], int c, v4f (&acc)[MT][4]) {
+      V wt[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) wt[t] = weights_of<T, RANKS>(raw[t], 32 * c + 8 * g, a.R);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if (some[t]) {
+          const int q = t * chunks + c;
+          V h[kTerms];
+#pragma unroll
+          for (int i = 0; i < kTerms; ++i) __builtin_memcpy(&h[i], &staged[(q * kTerms + i) * 64 + lane], 16);
+          add_products<kTerms>(wt, h, units[q * 16 + j], acc[t]);
+        }
+    };
+    L2 b[4];
+    Outputs y[MT];
+    int64_t n0 = n_first;
+    if (n0 < n_last) load_weights<T, RANKS>(B, n0, a.N, 8 * g, a.R, j, b);
+    if (n0 + 64 <= n_last) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if (some[t]) y[t] = load_y(reinterpret_cast<const O*>(a.y) + row_of[t] * a.ldy, n0);
+    }
+    for (; n0 < n_last; n0 += 256) {
+      const bool whole = n0 + 64 <= n_last, more = n0 + 256 < n_last, next_whole = n0 + 320 <= n_last;
+      v4f acc[MT][4] = {};
+      Outputs y_next[MT];
+      for (int c = 0; c < chunks; ++c) {
+        L2 b_next[4];
+        if (c + 1 < chunks) {
+          load_weights<T, RANKS>(B, n0, a.N, 32 * (c + 1) + 8 * g, a.R, j, b_next);
+        } else if (more) {
+          load_weights<T, RANKS>(B, n0 + 256, a.N, 8 * g, a.R, j, b_next);
+        }
+        if (c == 0 && next_whole) {
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            if (some[t]) y_next[t] = load_y(reinterpret_cast<const O*>(a.y) + row_of[t] * a.ldy, n0 + 256);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // on their way before the products
+        products(b, c, acc);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) b[t] = b_next[t];
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (!some[t]) continue;
+        O* orow = reinterpret_cast<O*>(a.out) + row_of[t] * a.ldout;
+        if (whole) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            O8 v = __builtin_bit_cast(O8, y[t].v[q]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (O)((float)v[i] + acc[t][2 * q + (i >> 2)][i & 3]);
+            if (mine[t]) __builtin_memcpy(orow + n0 + 32 * q + 8 * g, &v, sizeof(v));
+          }
+        } else {
+          const O* yrow = reinterpret_cast<const O*>(a.y) + row_of[t] * a.ldy;
+          O v[2][8];
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t n = n0 + 32 * q + 8 * g + i;
+              v[q][i] = yrow[n < a.N ? n : a.N - 1];
+            }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t n = n0 + 32 * q + 8 * g + i;
+              if (mine[t] && n < a.N) orow[n] = (O)((float)v[q][i] + acc[t][2 * q + (i >> 2)][i & 3]);
+            }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) y[t] = y_next[t];
+    }
+    __syncthreads();  // h is read
+  });
+  if (worker != 0 || a.in_place) return;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t m = m0 + 16 * t + j;
+    const int of = __shfl(id, 16 * t + j, 64);
+    if (m >= a.M || of >= 0) continue;
+    const O* yrow = reinterpret_cast<const O*>(a.y) + m * a.ldy;
+    O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
+    for (int64_t n0 = n_first; n0 < n_last; n0 += 256) {
+      if (n0 + 64 <= n_last) {
+        const Outputs y = load_y(yrow, n0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) __builtin_memcpy(orow + n0 + 32 * q + 8 * g, y.v[q], sizeof(y.v[q]));
+      } else {
+        for (int64_t n = n0 + 8 * g; n < n0 + 64; n += 32)
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) orow[n + i] = yrow[n + i];
+      }
+    }
+  }
+}
+
 template <typename T, typename O, Ranks RANKS>
 void expand(const AdapterArgs& a, dim3 g) {
   const dim3 b(256);
@@ -446,6 +631,24 @@ void expand(const AdapterArgs& a, dim3 g) {
   else expand<T, O, kPart>(a, g);
 }
 
+template <typename T, typename O>
+void expand_many(const AdapterArgs& a, int64_t tiles, int64_t ranges) {
+  constexpr int MT = sizeof(O) == 4 ? 2 : 4;
+  const dim3 b(256), g = tile_grid(ranges, (tiles + MT - 1) / MT, a.workers);
+  const size_t lds = (size_t)MT * ((a.R + 31) / 32) * (kTermsOf<T, O> * 1024 + 64);
+  if (a.R < 4) hipLaunchKernelGGL((k_expand_many<T, O, MT, kTiny>), g, b, lds, a.stream, a);
+  else if (a.R % 8 == 0) hipLaunchKernelGGL((k_expand_many<T, O, MT, kWhole>), g, b, lds, a.stream, a);
+  else hipLaunchKernelGGL((k_expand_many<T, O, MT, kPart>), g, b, lds, a.stream, a);
+}
+
+template <typename T, int MT>
+void shrink(AdapterArgs a, int64_t tiles) {
+  const dim3 b(256), g = tile_grid(a.splits, (tiles + MT - 1) / MT, a.workers);
+  if (a.R <= 16) hipLaunchKernelGGL((k_shrink<T, 1, MT>), g, b, 0, a.stream, a);
+  else if (a.R <= 32) hipLaunchKernelGGL((k_shrink<T, 2, MT>), g, b, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_shrink<T, 4, MT>), g, b, 0, a.stream, a);
+}
+
 template <typename T>
 hipError_t add(AdapterArgs a) {
   const int64_t tiles = ((int64_t)a.M + 15) / 16;
@@ -454,25 +657,24 @@ hipError_t add(AdapterArgs a) {
   a.workers = tiles <= 64 ? 16 : tiles <= 512 ? 4 : 1;
   while (a.workers / 2 >= a.M) a.workers /= 2;
   if (a.R > 0 && a.L > 0 && a.K > 0) {
-    const dim3 g = tile_grid(a.splits, tiles, a.workers);
-    const dim3 b(256);
     a.share = ((a.K + 31) / 32 + a.splits * 4 - 1) / (a.splits * 4) * 32;  // a wave's: whole steps of 32
-    if (a.R <= 16) hipLaunchKernelGGL((k_shrink<T, 1>), g, b, 0, a.stream, a);
-    else if (a.R <= 32) hipLaunchKernelGGL((k_shrink<T, 2>), g, b, 0, a.stream, a);
-    else hipLaunchKernelGGL((k_shrink<T, 4>), g, b, 0, a.stream, a);
+    if (tiles > kFewTiles) shrink<T, 4>(a, tiles);
+    else shrink<T, 1>(a, tiles);
   } else {
     a.L = 0;  // no adapter at all
   }
   // Blocks of columns one after the other where there are many tokens.
-  const int64_t blocks = ((int64_t)a.N + 255) / 256;
-  int64_t per = tiles * a.workers * blocks / 2048;
+  const bool many = tiles > kFewTiles && a.R > 32 && a.L > 0;
+  const int64_t blocks = ((int64_t)a.N + 255) / 256, rows = many ? (tiles + 3) / 4 : tiles;
+  int64_t per = rows * a.workers * blocks / (many ? 1024 : 2048);
   per = per < 1 ? 1 : per > 4 ? 4 : per;
   a.cols = (int)per * 256;
-  const dim3 g = tile_grid((blocks + per - 1) / per, tiles, a.workers);
+  const int64_t ranges = (blocks + per - 1) / per;
+  const dim3 g = tile_grid(ranges, tiles, a.workers);
   switch (a.out_dtype) {
-    case kOutBF16: expand<T, __bf16>(a, g); break;
-    case kOutFP16: expand<T, _Float16>(a, g); break;
-    default: expand<T, float>(a, g); break;
+    case kOutBF16: many ? expand_many<T, __bf16>(a, tiles, ranges) : expand<T, __bf16>(a, g); break;
+    case kOutFP16: many ? expand_many<T, _Float16>(a, tiles, ranges) : expand<T, _Float16>(a, g); break;
+    default: many ? expand_many<T, float>(a, tiles, ranges) : expand<T, float>(a, g); break;
   }
   return hipGetLastError();
 }
@@ -481,10 +683,10 @@ hipError_t add(AdapterArgs a) {
 
 // How many workgroups split K: enough that few tokens still cover the device.
 int adapter_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + 15) / 16;
+  const int64_t tiles = (M + 15) / 16, groups = tiles > kFewTiles ? (tiles + 3) / 4 : tiles;
   int64_t most = (K + 255) / 256;
   most = most < kMaxSplits ? most : kMaxSplits;
-  const int64_t s = 2048 / (tiles > 0 ? tiles : 1);
+  const int64_t s = (tiles > kFewTiles ? 512 : 2048) / (groups > 0 ? groups : 1);
   return (int)(s < 1 ? 1 : s < most ? s : most);
 }
 

@@ -94,10 +94,23 @@ def test_runs_and_alternations(gpu, M):
         _check(gpu, d, "fp32", ids[:4], in_place=True, scales=False)
 
 
+@pytest.mark.parametrize("R", [1, 3, 4, 7, 8, 16, 24, 30, 32, 33, 64, 65, 128, 200, 256])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp16", "fp32")])
+def test_many_tokens(gpu, R, dtype, out):
+    """Prefills: runs of one adapter and tokens that change theirs, columns that no
+    block divides, out of place and in place."""
+    for M, N, K, L in ((3333, 136, 72, 3), (4100, 345, 40, 7)):
+        d = _make(M, N, K, R, L, dtype, out, M + R, pad=3 * (R % 2), lead=R % 2)
+        m = torch.arange(M)
+        for ids in (d["ids"], (m // 100 % (L + 1) - 1), torch.where(m % 1000 < 500, m // 64 % L, -1)):
+            d["ids"] = ids.to(torch.int32)
+            _check(gpu, d, out, (M, R), in_place=R % 2 == 0)
+
+
 def test_infinities_stay_with_their_tokens(gpu):
     """A NaN or infinity in one token, or in an adapter that others use, reaches
     no other token."""
-    for M in (40, 600):
+    for M in (40, 600, 3500):
         d = _make(M, 96, 256, 16, 4, "bf16", "fp32", 1, bare=0.3)
         d["x"][5] = float("nan")
         d["x"][6, 3] = float("inf")
