@@ -631,7 +631,8 @@ extern "C" int fbg_route_experts(const void* logits, int64_t ld, int dtype, int6
   args.topk = (int)topk;
   args.groups = topk_groups == groups ? 1 : (int)groups;  // all groups stay: none to choose
   args.topk_groups = (int)topk_groups;
-  args.group_lanes = 1;
+  args.group_lanes = 0;
+  args.group_inverse = 0;
   args.dtype = dtype;
   args.score = score;
   args.group_score = group_score;

@@ -236,18 +236,21 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // itself, so 1 / (1 + exp(-z)), with one sum and a reciprocal, is off by
 // (1.5 |z| + 2) U s (1 - s) + 3 U s < 2^-22, and a softmax, whose sum adds the mean of its
 // terms' errors (2.5 ln E + 2) U and its additions' 22 U, by less than 2^-18 of the
-// largest score.  fp32 logits without a bias are compared as they are.  A row that
-// does not pass (one in 400 for random fp32 logits and biases) is done again in 64 bits.
+// largest score.  fp32 logits without a bias are compared as they are.
 //
-// Groups have to be whole lanes (VPL 2^p experts); a group's two best are taken in
-// 32 bits, and the line between the kept and the others is checked likewise (scores
-// without a bias are off by 1.5 |z| U < 2^-16.9 of themselves, or by 2^-126).
+// Values that are too near (in one row of 400 for random fp32 logits and biases) are
+// compared in 64 bits, the first topk + 1 of them alone; where that does not settle a row
+// (three in a heap, the line between groups, a softmax with a bias), it is done again by
+// the whole wave, which takes 5 us.  A group's two best are taken in 32
+// bits, by its lanes where it is 2^p of them, else by one lane from LDS, and the line
+// between the kept and the others is checked like the rest (scores without a bias
+// are off by 1.5 |z| U < 2^-16.9 of themselves, or by 2^-126).
 template <typename T, int L, int VPL, bool EXACT>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
   constexpr int kExact = L == 16 ? VPL < 4 ? 1 : VPL / 4 : VPL;  // experts per lane of a whole wave
   constexpr int kPlace = EXACT ? 1023 : VPL - 1;
   constexpr int kChunks = VPL * (int)sizeof(T) / 16;  // of 16 bytes per lane
-  constexpr int kShared = 64 * (kChunks > 1 && 2 * kChunks > kExact ? 2 * kChunks : kExact);
+  constexpr int kShared = 64 * (2 * kChunks > kExact ? 2 * kChunks : VPL / 2 > kExact ? VPL / 2 : kExact);
   __shared__ double shared[4][kShared];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l = lane & (L - 1);
   const int e0 = l * VPL;
@@ -338,58 +341,85 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
     }
   }
   bool sure = true;
-  bool kept = true;
+  uint32_t kept = ~0u;  // which of the lane's experts are of groups that stay
+  const int base = lane & ~(L - 1);
   if (a.groups > 1) {
+    const bool aligned = a.group_lanes > 0;
+    const bool two = a.group_score == FBG_GROUP_TOP2;
     float best = -kInf, second = -kInf;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      second = __builtin_amdgcn_fmed3f(best, second, c[i]);
-      best = larger(best, c[i]);
-    }
-    // Over the lanes of a group; after each step those of half a group agree.
-    const auto join = [&](float u, float v) {
-      second = larger(best < u ? best : u, larger(second, v));
+    const auto take = [&](float u) {
+      second = __builtin_amdgcn_fmed3f(best, second, u);
       best = larger(best, u);
     };
-    if (a.group_lanes > 1) join(dpp<0xb1>(best), dpp<0xb1>(second));
-    if (a.group_lanes > 2) join(dpp<0x4e>(best), dpp<0x4e>(second));
-    if (a.group_lanes > 4) join(dpp<0x141>(best), dpp<0x141>(second));
-    if (a.group_lanes > 8) join(dpp<0x140>(best), dpp<0x140>(second));
-    if (L == 64 && a.group_lanes > 16) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
-    const bool two = a.group_score == FBG_GROUP_TOP2;
+    if (aligned) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) take(c[i]);
+      // Over the lanes of a group; after each step those of half a group agree.
+      const auto join = [&](float u, float v) {
+        second = larger(best < u ? best : u, larger(second, v));
+        best = larger(best, u);
+      };
+      if (a.group_lanes > 1) join(dpp<0xb1>(best), dpp<0xb1>(second));
+      if (a.group_lanes > 2) join(dpp<0x4e>(best), dpp<0x4e>(second));
+      if (a.group_lanes > 4) join(dpp<0x141>(best), dpp<0x141>(second));
+      if (a.group_lanes > 8) join(dpp<0x140>(best), dpp<0x140>(second));
+      if (L == 64 && a.group_lanes > 16) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
+    } else {  // a lane looks at a whole group
+      float* values = reinterpret_cast<float*>(shared[w]) + lane / L * (L * VPL);
+      wave_sync();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) values[e0 + i] = c[i];
+      wave_sync();
+      const int size = a.E / a.groups;
+      if (l < a.groups) {
+#pragma unroll 8
+        for (int i = 0; i < size; ++i) take(values[l * size + i]);
+      }
+    }
     float value = best;
     if (two) {
       const bool scored = EXACT || !a.bias;
       value = scored ? score_of(best) : best;
       if (a.E > a.groups) value += scored ? score_of(second) : second;
     }
-    if (e0 >= a.E) value = -kInf;
+    const int lanes = aligned ? a.group_lanes : 1, last = aligned ? L : a.groups;
+    const bool real = aligned ? e0 < a.E : l < a.groups;
+    if (!real) value = -kInf;
     int better = 0;  // groups that come before this lane's
-    for (int o = a.group_lanes; o < L; o += a.group_lanes) {
-      const int other = (l + o) & (L - 1);
-      const float u = __shfl(value, other + (lane & ~(L - 1)), 64);
+    for (int o = aligned ? lanes : 0; o < last; o += lanes) {
+      const int other = aligned ? (l + o) & (L - 1) : o;
+      const float u = __shfl(value, other + base, 64);
       better += u > value || (u == value && other < l);
     }
-    kept = better < a.topk_groups;
+    const bool stays = real && better < a.topk_groups;
     if (two || off > 0.0f) {
       // The last that stays and the first that does not.
       const auto value_at = [&](int rank) {
         const uint64_t at = __ballot(better == rank) >> (L == 64 ? 0 : lane & 48);
-        return __shfl(value, (int)__builtin_ctzll(at | 1ull << 63) + (lane & ~(L - 1)), 64);
+        return __shfl(value, (int)__builtin_ctzll(at | 1ull << 63) + base, 64);
       };
       const float low = value_at(a.topk_groups - 1), high = value_at(a.topk_groups);
       const float relative = off > 0.0f ? 0x1p-22f : 0x1p-16f;
       sure = low - high > relative * (__builtin_fabsf(low) + __builtin_fabsf(high)) + 4.0f * off + 0x1p-120f || high == -kInf;
+    }
+    if (aligned) {
+      kept = stays ? ~0u : 0;
+    } else {
+      const uint64_t stay = __ballot(stays) >> (L == 64 ? 0 : lane & 48);
+      kept = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)  // the group of an expert by its inverse, exact below 1024
+        kept |= (uint32_t)((stay >> (((uint32_t)(e0 + i) * a.group_inverse >> 20) & 63)) & 1) << i;
     }
   }
   int key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int place = EXACT ? 1023 - (e0 + i) : VPL - 1 - i;
-    key[i] = kept && e0 + i < a.E ? (ordered(c[i]) & ~kPlace) | place : kNone;
+    key[i] = (kept >> i & 1) && e0 + i < a.E ? (ordered(c[i]) & ~kPlace) | place : kNone;
   }
   int rank_key = kNone, expert = 0;
-  const int rounds = a.topk + (EXACT ? 0 : 1);
+  const int rounds = a.topk + (EXACT ? 0 : 2);
   for (int r = 0; r < rounds; ++r) {
     int m = key[0];
 #pragma unroll
@@ -411,21 +441,52 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
     for (int i = 0; i < VPL; ++i) key[i] = key[i] == gone ? kNone : key[i];
     if (l == r) rank_key = m, expert = e;
   }
-  // Lane l has the token's expert number l, and lane topk the first of the others.
+  // Lane l has the token's expert number l; lanes topk and topk + 1 the first two
+  // of the others.
   expert = expert < a.E ? expert : a.E - 1;
-  const float z = l < rounds ? (float)row[expert] : 0.0f;
+  float z = l < rounds ? (float)row[expert] : 0.0f;
   if constexpr (!EXACT) {
+    const int other_key = __shfl(rank_key, base + a.topk + 1, 64);
+    // What the others behind lane topk's are at most: the key's value and all that the
+    // place took from another's.
+    const float rest = other_key == kNone ? -kInf : unordered(other_key | kPlace);
+    const bool there = l <= a.topk && rank_key != kNone;
     float v = z, most = 0.0f;
-    if (a.bias && l < rounds) {
+    if (a.bias && there) {
       v = score_of(z) + a.bias[expert];
       most = off + 0x1p-24f * __builtin_fabsf(v);
     }
-    // What is behind the first of the others is at most its key's value and all
-    // that the place took from another's.
-    if (l == a.topk) v = unordered(rank_key | kPlace);
-    const float gap = v - __shfl(v, lane + 1, 64), lim = most + __shfl(most, lane + 1, 64);
-    const bool last = __shfl(rank_key, lane + 1, 64) == kNone;
-    if (l < a.topk && !last) sure = sure && gap > lim;
+    const float next = __shfl(v, lane + 1, 64), lim = most + __shfl(most, lane + 1, 64);
+    const bool next_there = __shfl((int)there, lane + 1, 64) != 0;
+    bool clear = true;
+    if (l < a.topk && next_there) clear = v - next > lim;
+    if (l == a.topk - 1 && other_key != kNone) clear = clear && v - rest > most + off;
+    const bool again = !clear && !(softmax && a.bias);
+    sure = sure && (clear || again);
+    if (__ballot(again)) {
+      // Lanes 0 .. topk are put in order by their values in 64 bits (softmax with a
+      // bias: their sum is not known to 64); the others are far enough below the last of
+      // them that is chosen, or the row goes the long way.
+      double d = (double)z;
+      if (a.bias && there) d = 1.0 / (1.0 + exp(-(double)z)) + (double)a.bias[expert];
+      int rank = 0;
+      for (int o = 0; o <= a.topk; ++o) {
+        const double u = __shfl(d, base + o, 64);
+        const int ue = __shfl(expert, base + o, 64);
+        const bool ut = __shfl((int)there, base + o, 64) != 0;
+        rank += ut && (u > d || (u == d && ue < expert));
+      }
+      int* order = reinterpret_cast<int*>(shared[w]) + base;
+      wave_sync();
+      if (there) order[rank] = lane;
+      wave_sync();
+      const int from = there ? order[l] : lane;
+      expert = __shfl(expert, from, 64);
+      z = __shfl(z, from, 64);
+      d = __shfl(d, from, 64);
+      const float lim = off > 0.0f ? off + 0x1p-24f * __builtin_fabsf(rest) : 0.0f;
+      if (l == a.topk - 1 && other_key != kNone) sure = sure && d - (double)rest > (double)lim;
+    }
   }
   float weight = 0.0f;
   if (l < a.topk) {
@@ -463,13 +524,15 @@ hipError_t route(const RouteArgs& a) {
 
 template <typename T>
 hipError_t route(RouteArgs a) {
-  // Whether L lanes of vpl experts hold whole groups and a rank for every choice.
+  // Whether L lanes of vpl experts hold them all, a rank for every choice and two
+  // more, and a lane for every group.
   const auto fits = [&](int L, int vpl) {
-    if (a.E > L * vpl || a.topk >= L) return false;
-    if (a.groups == 1) return true;
+    if (a.E > L * vpl || a.topk + 2 > L || a.groups > L) return false;
     const int size = a.E / a.groups, lanes = size / vpl;
-    a.group_lanes = lanes;
-    return size % vpl == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 32;
+    const bool aligned = size % vpl == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 32;
+    a.group_lanes = aligned ? lanes : 0;
+    a.group_inverse = (1u << 20) / size + 1;
+    return true;
   };
   // Many tokens: four to a wave.  Few: a wave each, for its shorter way to an answer.
   if (a.T > 1024) {

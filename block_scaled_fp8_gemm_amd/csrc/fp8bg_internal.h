@@ -127,7 +127,8 @@ struct RouteArgs {
   int64_t ld;
   int T, E, topk;
   int groups, topk_groups;
-  int group_lanes;  // lanes that hold a group (launch_route sets it)
+  int group_lanes;         // lanes that hold a group, 0 where groups cut lanes (launch_route sets these)
+  uint32_t group_inverse;  // 2^20 over a group's experts, rounded up
   int dtype, score, group_score, renormalize;
   float scale;
   hipStream_t stream;

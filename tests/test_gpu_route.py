@@ -141,6 +141,36 @@ def test_scores_next_to_one_another(gpu, E):
                 _check(gpu, z, 8, score=score, bias=bias, groups=groups, topk_groups=groups // 2, group_score="top2")
 
 
+@pytest.mark.parametrize("E", [48, 256])
+def test_many_rows_next_to_one_another(gpu, E):
+    """The same in calls of many tokens: pairs, heaps and exact ties, with and without
+    a bias, in and between groups."""
+    g = torch.Generator().manual_seed(E)
+    for score in ("sigmoid", "softmax"):
+        near = lambda z: torch.sigmoid(z.double()) if score == "sigmoid" else torch.softmax(z.double(), 1)  # noqa: E731
+        z = torch.randn(1500, E, generator=g)
+        bias = 0.75 - near(z[:1])[0].float()
+        z[1:500] = z[:1] * (1 + 2.0 ** -21 * torch.randn(499, 1, generator=g))          # all near
+        z[500:1000, 1::2] = z[500:1000, ::2]                                            # equal pairs
+        z[1000:1200, 1::2] = z[1000:1200, ::2] * (1 + 2.0 ** -23)                       # the next number
+        c = np.sort((near(z) + bias.double()).numpy(), axis=1)
+        clear = torch.from_numpy(np.diff(c, axis=1)[:, -10:].min(axis=1) > 1e-13)
+        assert int(clear[:500].sum()) > 300
+        for groups in (1, 4, 6 if E % 6 == 0 else 8):
+            for group_score in ("max", "top2"):
+                kw = dict(score=score, groups=groups, topk_groups=max(1, groups // 2), group_score=group_score)
+                if groups > 1:   # rows whose groups are as near as their experts are left out
+                    v = np.sort((near(z) + bias.double()).numpy().reshape(1500, groups, -1), axis=2)
+                    v = np.sort(v[:, :, -1] if group_score == "max" else v[:, :, -2:].sum(axis=2), axis=1)
+                    keep = clear & torch.from_numpy(np.diff(v, axis=1).min(axis=1) > 1e-13)
+                else:
+                    keep = clear
+                rows = z[keep].repeat(2, 1)
+                assert len(rows) > 1024
+                _check(gpu, rows, 8, bias=bias, what=(E, kw), **kw)
+                _check(gpu, z if groups == 1 else rows, 8, what=(E, kw, "no bias"), **kw)
+
+
 def test_two_best_without_a_bias(gpu):
     """The groups' values are sums of scores, not of logits."""
     z = torch.tensor([[5.0, -9.0, 4.0, 3.9, -1.0, -1.0, 0.0, 0.0]])
