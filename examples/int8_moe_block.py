@@ -2,11 +2,12 @@
 two attention blocks:
 
     r, q, s = block_norm(attention output, residual, .., quantize="int8")
-    router on r, tokens sorted by expert
-    up   = int8_grouped_gemm(q of the sorted tokens, ..)      [2F per expert]
+    weights, experts = route_experts(logits of r, ..)
+    rows, .. = dispatch_tokens(experts, q, s)                  q, s in expert order
+    up   = int8_grouped_gemm(rows, ..)                         [2F per expert]
     act  = silu(up[:, :F]) * up[:, F:]                         -> quantize_tokens
     down = int8_grouped_gemm(act, ..)                          [D per expert]
-    h    = sum of each token's experts, weighted by the router
+    h    = combine_experts(down, slots, weights)
     r, q, s = block_norm(h, r, .., quantize="int8")
     qkv  = int8_gemm(q, s, next projection)
 
@@ -46,28 +47,15 @@ class Int8MoEBlock:
         self.down, self.down_s = down.view(E, D, F), down_s.view(E, D)
         self.next, self.next_s = fbg.quantize_tokens(self.w_next)
 
-    def route(self, r):
-        """Weights [T, topk], and each token's experts."""
-        weight, expert = torch.topk(torch.softmax(r.float() @ self.router.t(), dim=-1), self.topk, dim=-1)
-        return weight / weight.sum(dim=-1, keepdim=True), expert
-
     def __call__(self, attention, residual):
-        T, D = attention.shape
         r, q, s = fbg.block_norm(attention, residual, post_weight=self.norms[0], gate=self.gates[0],
                                  pre_weight=self.norms[1], residual_scale=self.scale, quantize="int8")
-        weight, expert = self.route(r)
-        order = torch.argsort(expert.reshape(-1), stable=True)
-        token = order // self.topk
-        # offsets[e]: rows whose expert is below e (no atomics, no wait for the GPU)
-        ids = torch.arange(self.E + 1, device=q.device)
-        offsets = torch.searchsorted(expert.reshape(-1)[order], ids).to(torch.int32)
-        up = fbg.int8_grouped_gemm(q[token], s[token], self.up, self.up_s, offsets)
+        weight, expert = fbg.route_experts(r.float() @ self.router.t(), self.topk)
+        rows, rows_s, offsets, slots = fbg.dispatch_tokens(expert, self.E, q, s)
+        up = fbg.int8_grouped_gemm(rows, rows_s, self.up, self.up_s, offsets)
         act = torch.nn.functional.silu(up[:, :self.F]) * up[:, self.F:]
         down = fbg.int8_grouped_gemm(*fbg.quantize_tokens(act), self.down, self.down_s, offsets, out_dtype=torch.float32)
-        # back to token order: row order[i] of the (token, choice) matrix is row i here
-        rows = torch.empty_like(down)
-        rows[order] = down
-        h = (rows.view(T, self.topk, D) * weight[..., None]).sum(dim=1).to(torch.bfloat16)
+        h = fbg.combine_experts(down, slots, weight, out_dtype=torch.bfloat16)
         r, q, s = fbg.block_norm(h, r, post_weight=self.norms[2], gate=self.gates[1], pre_weight=self.norms[3],
                                  residual_scale=self.scale, quantize="int8")
         return r, fbg.int8_gemm(q, s, self.next, self.next_s), expert
@@ -78,7 +66,7 @@ class Int8MoEBlock:
         rms = lambda v, w: v / torch.sqrt((v * v).mean(dim=1, keepdim=True) + 1e-6) * w.double()
         r = self.scale * residual.double() + self.gates[0].double() * rms(attention.double(), self.norms[0])
         y = rms(r, self.norms[1])
-        p = torch.softmax(r @ self.router.double().t(), dim=-1).gather(1, expert)
+        p = torch.softmax(r @ self.router.double().t(), dim=-1).gather(1, expert.long())
         p = p / p.sum(dim=-1, keepdim=True)
         h = torch.zeros_like(r)
         for e in range(self.E):
