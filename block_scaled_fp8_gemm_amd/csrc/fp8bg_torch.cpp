@@ -18,6 +18,7 @@
 
 #include <optional>
 #include <string>
+#include <utility>
 
 #include "fp8bg.h"
 #include "fp8bg_internal.h"
@@ -133,6 +134,20 @@ class Launch {
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+}
+
+// Two int32 outputs in one allocation, each a tensor of its own at a 16-byte
+// boundary (5.3 us a small call, with an allocation each 5.7).
+std::pair<at::Tensor, at::Tensor> make_two(at::IntArrayRef shape0, at::IntArrayRef shape1, at::Device device) {
+  const int64_t n0 = (c10::multiply_integers(shape0) + 3) / 4 * 4, n1 = c10::multiply_integers(shape1);
+  const at::Tensor both = make({n0 + n1}, at::kInt, device);
+  const auto part = [&](at::IntArrayRef shape, int64_t at) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(both.storage()), both.key_set(), both.dtype());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    return t;
+  };
+  return {part(shape0, 0), part(shape1, n0)};
 }
 
 // An int8 matrix whose rows start on 16-byte boundaries: the products read it
@@ -333,8 +348,8 @@ PyObject* route_experts(PyObject*, PyObject* const* v, Py_ssize_t n) {
   }
   const Launch launch(v[12], dev);
   const at::Tensor w = v[10] == Py_None ? make({T, topk}, at::kFloat, dev) : tensor(v[10], "weights");
-  auto* weights = static_cast<float*>(whole(w, "weights", at::kFloat, {T, topk}, dev));
   const at::Tensor e = v[11] == Py_None ? make({T, topk}, at::kInt, dev) : tensor(v[11], "experts");
+  auto* weights = static_cast<float*>(whole(w, "weights", at::kFloat, {T, topk}, dev));
   auto* experts = static_cast<int32_t*>(whole(e, "experts", at::kInt, {T, topk}, dev));
   check_status(fbg_route_experts(logits.data_ptr(), ld, in_code, T, E, topk, score, bias, groups, topk_groups,
                                  group_score, renormalize, (float)scale, mask, weights, experts, launch.get()),
@@ -383,7 +398,7 @@ PyObject* dispatch_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
   } else if (v[6] != Py_None) {
     value_error("row_scale needs x_scale");
   }
-  const at::Tensor offsets = make({E + 1}, at::kInt, dev), slots = make({T, topk}, at::kInt, dev);
+  const auto [offsets, slots] = make_two({E + 1}, {T, topk}, dev);
   check_status(fbg_dispatch_tokens(ids, T, topk, first, E, x.data_ptr(), ldx, K, (int)size, x_scale, S,
                                    rows.data_ptr(), ldrows,
                                    row_scale.defined() ? static_cast<float*>(row_scale.data_ptr()) : nullptr,

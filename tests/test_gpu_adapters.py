@@ -107,6 +107,20 @@ def test_many_tokens(gpu, R, dtype, out):
             _check(gpu, d, out, (M, R), in_place=R % 2 == 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M", [20, 3400])
+@pytest.mark.parametrize("R", [16, 48, 100])
+def test_ranks_of_unlike_sizes(gpu, dtype, M, R):
+    """Ranks whose values differ by up to 2^12, with weights that make up for it: none
+    may lose its small ones, within 32 ranks or between them."""
+    d = _make(M, 72, 128, R, 2, dtype, "fp32", R)
+    size = torch.exp2(-(torch.arange(R) % 13).float())
+    d["A"] = (d["A"].float() * size[None, :, None]).to(d["A"].dtype)
+    d["B"] = (d["B"].float() / size / 64).to(d["B"].dtype)
+    d["x"] *= 16
+    _check(gpu, d, "fp32", (M, R))
+
+
 def test_infinities_stay_with_their_tokens(gpu):
     """A NaN or infinity in one token, or in an adapter that others use, reaches
     no other token."""
