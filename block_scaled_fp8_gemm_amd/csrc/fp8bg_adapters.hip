@@ -87,7 +87,7 @@ __device__ __forceinline__ void for_passes(int id, int worker, int workers, cons
 
 // h of 16 MT tokens over one slice of K for one adapter of theirs, or each in
 // turn; the waves split the slice, and their sums meet in LDS.  RT tiles of 16
-// ranks at a time; the loads of U steps are in flight together.  Many tokens
+// ranks to a workgroup; the loads of U steps are in flight together.  Many tokens
 // take MT = 4, which reads the adapter's rows from L2 once for 64 tokens (16384
 // tokens of rank 64: 16 tokens' workgroups read 537 MB of them).
 template <typename T, int RT, int MT>
@@ -96,7 +96,9 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
   constexpr int U = MT > 1 ? 2 : RT > 1 ? 4 : 8;
   typedef typename Vec8<T>::type V;
   __shared__ v4f part[RT * MT][W][64];  // [tile of 16 ranks by 16 tokens][wave][lane]
-  const int split = blockIdx.x, worker = worker_of(a.workers);
+  // Ranks past 64 are other workgroups'.
+  const int chunk = (int)gridDim.x == a.splits ? 0 : blockIdx.x / a.splits, r0 = chunk * 16 * RT;
+  const int split = blockIdx.x - chunk * a.splits, worker = worker_of(a.workers);
   const int64_t m0 = tile_of(a.workers) * TM;
   if (m0 >= a.M) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
@@ -116,69 +118,67 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
       x[t] = reinterpret_cast<const T*>(a.x) + m * a.ldx;
     }
     const T* A = reinterpret_cast<const T*>(a.A) + (int64_t)cur * a.R * a.K;
-    for (int r0 = 0; r0 < a.R; r0 += 16 * RT) {
-      const T* row[RT];
+    const T* row[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) row[i] = A + (int64_t)(r0 + 16 * i + j < a.R ? r0 + 16 * i + j : a.R - 1) * a.K;
-      v4f acc[MT][RT] = {};
-      const auto steps = [&](int k, auto count) {
-        constexpr int N = decltype(count)::value;
-        V xf[MT][N], af[N][RT];
+    for (int i = 0; i < RT; ++i) row[i] = A + (int64_t)(r0 + 16 * i + j < a.R ? r0 + 16 * i + j : a.R - 1) * a.K;
+    v4f acc[MT][RT] = {};
+    const auto steps = [&](int k, auto count) {
+      constexpr int N = decltype(count)::value;
+      V xf[MT][N], af[N][RT];
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
+      for (int u = 0; u < N; ++u) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i) __builtin_memcpy(&af[u][i], row[i] + k + 32 * u + 8 * g, 16);
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          if (some[t]) {
-#pragma unroll
-            for (int u = 0; u < N; ++u) __builtin_memcpy(&xf[t][u], x[t] + k + 32 * u + 8 * g, 16);
-          }
-        __builtin_amdgcn_sched_barrier(0);  // all loads before the first use of one
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          if (some[t]) {
-#pragma unroll
-            for (int u = 0; u < N; ++u)
-#pragma unroll
-              for (int i = 0; i < RT; ++i) acc[t][i] = mfma32(af[u][i], xf[t][u], acc[t][i]);
-          }
-      };
-      int k = first;
-      for (; k + 32 * U <= last; k += 32 * U) steps(k, std::integral_constant<int, U>{});
-      for (; k + 64 <= last; k += 64) steps(k, std::integral_constant<int, 2>{});
-      for (; k < last; k += 32) {
-        V af[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) af[i] = load8(row[i], k + 8 * g, a.K);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          if (some[t]) {
-            const V xf = load8(x[t], k + 8 * g, a.K);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) acc[t][i] = mfma32(af[i], xf, acc[t][i]);
-          }
+        for (int i = 0; i < RT; ++i) __builtin_memcpy(&af[u][i], row[i] + k + 32 * u + 8 * g, 16);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t)
+        if (some[t]) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) part[t * RT + i][w][lane] = acc[t][i];
-      __syncthreads();
-      for (int q = w; q < MT * RT; q += W) {  // a wave: some of the tiles
-        const int t = q / RT, i = q % RT, r = r0 + 16 * i + 4 * g;
-        if (r0 + 16 * i >= a.R) continue;
-        v4f s = part[q][0][lane];
+          for (int u = 0; u < N; ++u) __builtin_memcpy(&xf[t][u], x[t] + k + 32 * u + 8 * g, 16);
+        }
+      __builtin_amdgcn_sched_barrier(0);  // all loads before the first use of one
 #pragma unroll
-        for (int k = 1; k < W; ++k) s += part[q][k][lane];
+      for (int t = 0; t < MT; ++t)
+        if (some[t]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r + k >= a.R) s[k] = 0.0f;
-        const int m = 16 * t + j;
-        if ((meant >> m) & 1) *reinterpret_cast<v4f*>(a.h + ((int64_t)split * a.M + m0 + m) * a.pitch + r) = s;
-      }
-      __syncthreads();
+          for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[t][i] = mfma32(af[u][i], xf[t][u], acc[t][i]);
+        }
+    };
+    int k = first;
+    for (; k + 32 * U <= last; k += 32 * U) steps(k, std::integral_constant<int, U>{});
+    for (; k + 64 <= last; k += 64) steps(k, std::integral_constant<int, 2>{});
+    for (; k < last; k += 32) {
+      V af[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) af[i] = load8(row[i], k + 8 * g, a.K);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if (some[t]) {
+          const V xf = load8(x[t], k + 8 * g, a.K);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[t][i] = mfma32(af[i], xf, acc[t][i]);
+        }
     }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) part[t * RT + i][w][lane] = acc[t][i];
+    __syncthreads();
+    for (int q = w; q < MT * RT; q += W) {  // a wave: some of the tiles
+      const int t = q / RT, i = q % RT, r = r0 + 16 * i + 4 * g;
+      if (r0 + 16 * i >= a.R) continue;
+      v4f s = part[q][0][lane];
+#pragma unroll
+      for (int k = 1; k < W; ++k) s += part[q][k][lane];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r + k >= a.R) s[k] = 0.0f;
+      const int m = 16 * t + j;
+      if ((meant >> m) & 1) *reinterpret_cast<v4f*>(a.h + ((int64_t)split * a.M + m0 + m) * a.pitch + r) = s;
+    }
+    __syncthreads();
   });
 }
 
@@ -311,15 +311,14 @@ __device__ __forceinline__ typename Vec8<T>::type weights_of(L2 v, int r, int R)
 
 // 16 tokens by blocks of 64 columns, four blocks next to one another on the
 // four waves.  Each token belongs to one pass, which alone writes its row; the
-// first worker writes the rows without an adapter.  NC chunks of 32 ranks at a
-// time; DEEP: more than those, h read again for each block of columns.
+// first worker writes the rows without an adapter.  NC chunks of 32 ranks.
 //
 // The loads of the next block are in flight while one is computed: they stay
 // raw dwords until they are used, and have no branch between lanes (a lane of
 // another token reads the row of one that is meant), since the compiler waits
 // for a load where it unpacks its value or where the lanes meet again.  A last
 // block that N cuts goes element by element.
-template <typename T, typename O, int NC, bool DEEP, Ranks RANKS>
+template <typename T, typename O, int NC, Ranks RANKS>
 __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   constexpr int YC = 2 * (int)sizeof(O) / 4;  // 16-byte chunks of 8 outputs
   constexpr int kTerms = kTermsOf<T, O>;
@@ -352,63 +351,46 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
     O* orow = reinterpret_cast<O*>(a.out) + m * a.ldout;
     const T* B = reinterpret_cast<const T*>(a.B) + (int64_t)cur * a.N * a.R;
     const float* hrow = a.h + m * a.pitch;
-    const auto load_b = [&](int64_t n0, int r0) {
+    const auto load_b = [&](int64_t n0) {
       Weights b;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) load_weights<T, RANKS>(B, n0, a.N, r0 + 32 * c + 8 * g, a.R, j, b.v[c]);
+      for (int c = 0; c < NC; ++c) load_weights<T, RANKS>(B, n0, a.N, 32 * c + 8 * g, a.R, j, b.v[c]);
       return b;
     };
     const float scale = a.scales ? a.scales[cur] : 1.0f;
     V h[NC][kTerms];
     float unit[NC];
-    const auto load_h = [&](int r0) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float v[8];
-        load_hidden(a, hrow, r0 + 32 * c + 8 * g, scale, v);
-        unit[c] = split_terms<T, kTerms>(v, h[c]);
-      }
-    };
-    const auto multiply = [&](const Weights& b, int r0, v4f (&acc)[4]) {
+    const auto products = [&](const Weights& b, v4f (&acc)[4]) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         V w[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = weights_of<T, RANKS>(b.v[c][t], r0 + 32 * c + 8 * g, a.R);
+        for (int t = 0; t < 4; ++t) w[t] = weights_of<T, RANKS>(b.v[c][t], 32 * c + 8 * g, a.R);
         add_products<kTerms>(w, h[c], unit[c], acc);
       }
     };
-    // The products of one block, the weights of its first ranks in hand.
-    const auto block = [&](int64_t n0, const Weights& b, v4f (&acc)[4]) {
-      if constexpr (DEEP) {
-        Weights now = b;
-        for (int r0 = 0; r0 < a.R; r0 += 32 * NC) {
-          const Weights then = load_b(n0, r0 + 32 * NC < a.R ? r0 + 32 * NC : r0);
-          load_h(r0);
-          multiply(now, r0, acc);
-          now = then;
-        }
-      } else {
-        multiply(b, 0, acc);
-      }
-    };
-    Weights b = load_b(n_first, 0);
+    Weights b = load_b(n_first);
     Outputs y;
     int64_t n0 = n_first;
     if (n0 + 64 <= n_last) y = load_y(yrow, n0);
-    if constexpr (!DEEP) load_h(0);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float v[8];
+      load_hidden(a, hrow, 32 * c + 8 * g, scale, v);
+      unit[c] = split_terms<T, kTerms>(v, h[c]);
+    }
     // A lane's results are of its own token: those of the others' adapters,
     // which may hold infinities, go nowhere.
     for (; n0 + 64 <= n_last; n0 += 256) {
       Weights b_next;
       Outputs y_next;
       if (n0 + 320 <= n_last) {
-        b_next = load_b(n0 + 256, 0);
+        b_next = load_b(n0 + 256);
         y_next = load_y(yrow, n0 + 256);
       }
       __builtin_amdgcn_sched_barrier(0);  // on their way before the products
       v4f acc[4] = {};
-      block(n0, b, acc);
+      products(b, acc);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         O8 v = __builtin_bit_cast(O8, y.v[q]);
@@ -428,9 +410,9 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
           const int64_t n = n0 + 32 * q + 8 * g + i;
           v[q][i] = yrow[n < a.N ? n : a.N - 1];
         }
-      if (n0 > n_first) b = load_b(n0, 0);
+      if (n0 > n_first) b = load_b(n0);
       v4f acc[4] = {};
-      block(n0, b, acc);
+      products(b, acc);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -458,12 +440,12 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   }
 }
 
-// The same for many tokens: 16 MT of them to a workgroup, so that a block's weights
-// come from L2 once for all (rank 64 and 16384 tokens by 4096 columns: 16 tokens'
-// workgroups read 537 MB of them, twice the outputs).  h's terms are made once per pass
-// and stay in LDS; the ranks go in chunks of 32, any number of them.
+// The same for any rank, in chunks of 32: h's terms are made once per pass, by all
+// waves, and stay in LDS.  Many tokens take 16 MT of them to a workgroup, so that a
+// block's weights come from L2 once for all (rank 64 and 16384 tokens by 4096 columns:
+// 16 tokens' workgroups read 537 MB of them, twice the outputs).
 template <typename T, typename O, int MT, Ranks RANKS>
-__global__ __launch_bounds__(256) void k_expand_many(AdapterArgs a) {
+__global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
   constexpr int YC = 2 * (int)sizeof(O) / 4, TM = 16 * MT, kTerms = kTermsOf<T, O>;
   typedef typename Vec8<T>::type V;
   typedef uint32_t U4 __attribute__((ext_vector_type(4)));
@@ -619,34 +601,51 @@ __global__ __launch_bounds__(256) void k_expand_many(AdapterArgs a) {
 template <typename T, typename O, Ranks RANKS>
 void expand(const AdapterArgs& a, dim3 g) {
   const dim3 b(256);
-  if (a.R <= 32) hipLaunchKernelGGL((k_expand<T, O, 1, false, RANKS>), g, b, 0, a.stream, a);
-  else if (a.R <= 64) hipLaunchKernelGGL((k_expand<T, O, 2, false, RANKS>), g, b, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_expand<T, O, 2, true, RANKS>), g, b, 0, a.stream, a);
+  if (a.R <= 32) hipLaunchKernelGGL((k_expand<T, O, 1, RANKS>), g, b, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_expand<T, O, 2, RANKS>), g, b, 0, a.stream, a);
 }
 
 template <typename T, typename O>
 void expand(const AdapterArgs& a, dim3 g) {
-  if (a.R < 4) hipLaunchKernelGGL((k_expand<T, O, 1, false, kTiny>), g, dim3(256), 0, a.stream, a);
+  if (a.R < 4) hipLaunchKernelGGL((k_expand<T, O, 1, kTiny>), g, dim3(256), 0, a.stream, a);
   else if (a.R % 8 == 0) expand<T, O, kWhole>(a, g);
   else expand<T, O, kPart>(a, g);
 }
 
-template <typename T, typename O>
-void expand_many(const AdapterArgs& a, int64_t tiles, int64_t ranges) {
-  constexpr int MT = sizeof(O) == 4 ? 2 : 4;
+template <typename T, typename O, int MT>
+void expand_deep(const AdapterArgs& a, int64_t tiles, int64_t ranges) {
   const dim3 b(256), g = tile_grid(ranges, (tiles + MT - 1) / MT, a.workers);
   const size_t lds = (size_t)MT * ((a.R + 31) / 32) * (kTermsOf<T, O> * 1024 + 64);
-  if (a.R < 4) hipLaunchKernelGGL((k_expand_many<T, O, MT, kTiny>), g, b, lds, a.stream, a);
-  else if (a.R % 8 == 0) hipLaunchKernelGGL((k_expand_many<T, O, MT, kWhole>), g, b, lds, a.stream, a);
-  else hipLaunchKernelGGL((k_expand_many<T, O, MT, kPart>), g, b, lds, a.stream, a);
+  if (a.R % 8 == 0) hipLaunchKernelGGL((k_expand_deep<T, O, MT, kWhole>), g, b, lds, a.stream, a);
+  else hipLaunchKernelGGL((k_expand_deep<T, O, MT, kPart>), g, b, lds, a.stream, a);
+}
+
+// Blocks of columns one after the other where there are many tokens.
+template <typename T, typename O>
+void second(AdapterArgs a, int64_t tiles) {
+  constexpr int MT = sizeof(O) == 4 ? 2 : 4;
+  const bool wide = tiles > kFewTiles && a.R > 32 && a.L > 0;
+  const int64_t blocks = ((int64_t)a.N + 255) / 256, rows = wide ? (tiles + 3) / 4 : tiles;
+  int64_t per = rows * a.workers * blocks / (wide ? 1024 : 2048);
+  per = per < 1 ? 1 : per > 4 ? 4 : per;
+  a.cols = (int)per * 256;
+  const int64_t ranges = (blocks + per - 1) / per;
+  if (wide) expand_deep<T, O, MT>(a, tiles, ranges);
+  else if (a.R > 64) expand_deep<T, O, 1>(a, tiles, ranges);
+  else expand<T, O>(a, tile_grid(ranges, tiles, a.workers));
 }
 
 template <typename T, int MT>
 void shrink(AdapterArgs a, int64_t tiles) {
-  const dim3 b(256), g = tile_grid(a.splits, (tiles + MT - 1) / MT, a.workers);
-  if (a.R <= 16) hipLaunchKernelGGL((k_shrink<T, 1, MT>), g, b, 0, a.stream, a);
-  else if (a.R <= 32) hipLaunchKernelGGL((k_shrink<T, 2, MT>), g, b, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_shrink<T, 4, MT>), g, b, 0, a.stream, a);
+  // Tiles of 16 ranks, over as many workgroups as take four each, evenly.
+  const int ranks = (a.R + 15) / 16, chunks = (ranks + 3) / 4;
+  const dim3 b(256), g = tile_grid(a.splits * chunks, (tiles + MT - 1) / MT, a.workers);
+  switch ((ranks + chunks - 1) / chunks) {
+    case 1: hipLaunchKernelGGL((k_shrink<T, 1, MT>), g, b, 0, a.stream, a); break;
+    case 2: hipLaunchKernelGGL((k_shrink<T, 2, MT>), g, b, 0, a.stream, a); break;
+    case 3: hipLaunchKernelGGL((k_shrink<T, 3, MT>), g, b, 0, a.stream, a); break;
+    default: hipLaunchKernelGGL((k_shrink<T, 4, MT>), g, b, 0, a.stream, a); break;
+  }
 }
 
 template <typename T>
@@ -663,18 +662,10 @@ hipError_t add(AdapterArgs a) {
   } else {
     a.L = 0;  // no adapter at all
   }
-  // Blocks of columns one after the other where there are many tokens.
-  const bool many = tiles > kFewTiles && a.R > 32 && a.L > 0;
-  const int64_t blocks = ((int64_t)a.N + 255) / 256, rows = many ? (tiles + 3) / 4 : tiles;
-  int64_t per = rows * a.workers * blocks / (many ? 1024 : 2048);
-  per = per < 1 ? 1 : per > 4 ? 4 : per;
-  a.cols = (int)per * 256;
-  const int64_t ranges = (blocks + per - 1) / per;
-  const dim3 g = tile_grid(ranges, tiles, a.workers);
   switch (a.out_dtype) {
-    case kOutBF16: many ? expand_many<T, __bf16>(a, tiles, ranges) : expand<T, __bf16>(a, g); break;
-    case kOutFP16: many ? expand_many<T, _Float16>(a, tiles, ranges) : expand<T, _Float16>(a, g); break;
-    default: many ? expand_many<T, float>(a, tiles, ranges) : expand<T, float>(a, g); break;
+    case kOutBF16: second<T, __bf16>(a, tiles); break;
+    case kOutFP16: second<T, _Float16>(a, tiles); break;
+    default: second<T, float>(a, tiles); break;
   }
   return hipGetLastError();
 }
