@@ -6,6 +6,12 @@
 // with B[a] added to y.  A tile holds 16 tokens whatever their adapters; it
 // goes over the different ones among them, so that tokens share an adapter's
 // reads wherever they stand, and a run of one adapter is one pass.
+//
+// 16384 tokens of 16 adapters of rank 16, 4096 to 4096 columns, bf16: 37 us for the
+// first product (136 MB read by the counters, 3.6 TB/s) and 60 for the second (146 read
+// and 134 written, 4.7 TB/s); a large copy reaches 5.2.  64 tokens of a request each: 4.3
+// and 4.8 us, bound by latency.  One kernel for both, a workgroup per 16 tokens with h in
+// LDS, took 11.4 us there against 8.9 in a graph, and was no faster for many (104 both).
 #include <type_traits>
 
 #include "fp8bg_device.hpp"
@@ -19,7 +25,15 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxSplits = 4;
-constexpr int kFewTiles = 200;  // tiles of 16 tokens
+// Whether `tiles` tiles of 16 tokens go four to a workgroup: it reads an adapter once for
+// all of its tokens, and fewer workgroups share the work.  K = N = 4096, 16 tokens
+// per workgroup and 64, us, a batch of 8 prompts / of a request per token over 16
+// adapters: rank 64, 256 tokens 14.9 and 20.6 / 37.8 and 27.5, 512 20.3 and 24.6 / 57.5 and
+// 36.6, 2048 39.5 and 30.9 / 198 and 112; rank 128, 256 tokens 17.1 and 24.0 / 54.7 and
+// 36.5, 512 29.2 and 29.3 / 99 and 56; rank 256, 64 tokens 17.3 and 26.4 / 31.0 and 28.0,
+// 256 26.9 and 30.4 / 98.5 and 58.8.  Up to rank 32 the first product alone: 8 prompts of
+// rank 16, 2048 tokens 17.7 and 18.7, 4096 30.4 and 27.1.
+bool many_tokens(int64_t tiles, int64_t R) { return R > 32 ? tiles * R >= 2048 : tiles > 200; }
 
 // Grids: splits of K or blocks of columns along x, tiles of 16 tokens along y
 // and, past kGridY of them, z; with several workers per tile they stand along z.
@@ -443,7 +457,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
 // The same for any rank, in chunks of 32: h's terms are made once per pass, by all
 // waves, and stay in LDS.  Many tokens take 16 MT of them to a workgroup, so that a
 // block's weights come from L2 once for all (rank 64 and 16384 tokens by 4096 columns:
-// 16 tokens' workgroups read 537 MB of them, twice the outputs).
+// 16 tokens' workgroups read 537 MB of them, four times the outputs).
 template <typename T, typename O, int MT, Ranks RANKS>
 __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
   constexpr int YC = 2 * (int)sizeof(O) / 4, TM = 16 * MT, kTerms = kTermsOf<T, O>;
@@ -624,9 +638,9 @@ void expand_deep(const AdapterArgs& a, int64_t tiles, int64_t ranges) {
 template <typename T, typename O>
 void second(AdapterArgs a, int64_t tiles) {
   constexpr int MT = sizeof(O) == 4 ? 2 : 4;
-  const bool wide = tiles > kFewTiles && a.R > 32 && a.L > 0;
+  const bool wide = many_tokens(tiles, a.R) && a.R > 32 && a.L > 0;
   const int64_t blocks = ((int64_t)a.N + 255) / 256, rows = wide ? (tiles + 3) / 4 : tiles;
-  int64_t per = rows * a.workers * blocks / (wide ? 1024 : 2048);
+  int64_t per = rows * a.workers * blocks / 1024;
   per = per < 1 ? 1 : per > 4 ? 4 : per;
   a.cols = (int)per * 256;
   const int64_t ranges = (blocks + per - 1) / per;
@@ -652,12 +666,15 @@ template <typename T>
 hipError_t add(AdapterArgs a) {
   const int64_t tiles = ((int64_t)a.M + 15) / 16;
   // Few tokens: a worker for each adapter that a tile may hold.  Many: the
-  // tiles cover the device, and their tokens come in runs.
-  a.workers = tiles <= 64 ? 16 : tiles <= 512 ? 4 : 1;
+  // tiles cover the device, and their tokens come in runs.  Rank 16, us with 16 workers, 4
+  // and 1, prompts / requests of one token: 400 tokens 11.5 and 10.2 / 21.7 and 24.8 with 16
+  // and 4, 1024 15.8, 13.8, 15.4 / 40.1, 41.0, 51.0, 4096 36.3, 26.8, 29.4 / 101, 91, 125,
+  // 16384 149, 106, 102 / 403, 350, 355.
+  a.workers = tiles <= 32 ? 16 : tiles <= 512 ? 4 : 1;
   while (a.workers / 2 >= a.M) a.workers /= 2;
   if (a.R > 0 && a.L > 0 && a.K > 0) {
     a.share = ((a.K + 31) / 32 + a.splits * 4 - 1) / (a.splits * 4) * 32;  // a wave's: whole steps of 32
-    if (tiles > kFewTiles) shrink<T, 4>(a, tiles);
+    if (many_tokens(tiles, a.R)) shrink<T, 4>(a, tiles);
     else shrink<T, 1>(a, tiles);
   } else {
     a.L = 0;  // no adapter at all
@@ -672,12 +689,13 @@ hipError_t add(AdapterArgs a) {
 
 }  // namespace
 
-// How many workgroups split K: enough that few tokens still cover the device.
-int adapter_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + 15) / 16, groups = tiles > kFewTiles ? (tiles + 3) / 4 : tiles;
+// How many workgroups split K: enough that few tokens still cover the device (64
+// tokens of rank 16: one 12.1 us, four 8.4; 16384 tokens: one 106, four 101).
+int adapter_splits(int64_t M, int64_t K, int64_t R) {
+  const int64_t tiles = (M + 15) / 16, groups = many_tokens(tiles, R) ? (tiles + 3) / 4 : tiles;
   int64_t most = (K + 255) / 256;
   most = most < kMaxSplits ? most : kMaxSplits;
-  const int64_t s = (tiles > kFewTiles ? 512 : 2048) / (groups > 0 ? groups : 1);
+  const int64_t s = 2048 / (groups > 0 ? groups : 1);
   return (int)(s < 1 ? 1 : s < most ? s : most);
 }
 

@@ -741,7 +741,7 @@ int adapter_pitch(int64_t R) { return (int)((R + 15) / 16 * 16); }
 
 // Bytes of h; false if that overflows.
 bool adapter_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes) {
-  return !__builtin_mul_overflow(M * fbg::adapter_splits(M, K), (int64_t)adapter_pitch(R) * 4, bytes);
+  return !__builtin_mul_overflow(M * fbg::adapter_splits(M, K, R), (int64_t)adapter_pitch(R) * 4, bytes);
 }
 
 }  // namespace
@@ -802,7 +802,7 @@ extern "C" int fbg_add_adapters(const void* y, int64_t ldy, const void* x, int64
   args.R = (int)R;
   args.L = (int)L;
   args.pitch = adapter_pitch(R);
-  args.splits = fbg::adapter_splits(M, K);
+  args.splits = fbg::adapter_splits(M, K, R);
   args.in_place = in_place;
   args.dtype = dtype;
   args.out_dtype = out_dtype;

@@ -41,7 +41,7 @@ int int8_grouped_gemm(const void* A, int64_t lda, const float* a_s, const void* 
 constexpr int64_t kMaxRouted = 1024;  // most experts of fbg_route_experts and fbg_dispatch_tokens
 
 // Over how many workgroups the adapters' first product splits K (fp8bg_adapters.hip).
-int adapter_splits(int64_t M, int64_t K);
+int adapter_splits(int64_t M, int64_t K, int64_t R);
 
 #ifdef __HIPCC__
 struct GemmArgs {

@@ -107,6 +107,15 @@ def test_many_tokens(gpu, R, dtype, out):
             _check(gpu, d, out, (M, R), in_place=R % 2 == 0)
 
 
+@pytest.mark.parametrize("M,R", [(496, 64), (497, 64), (240, 128), (250, 128), (112, 256), (113, 256), (816, 40),
+                                 (817, 40), (999, 36), (640, 200), (3200, 16), (3201, 16), (512, 32), (513, 30)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp16", "fp32")])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_both_sides_of_many_tokens(gpu, M, R, dtype, out, in_place):
+    """Tokens of 21 adapters in any order, more of them per workgroup than it has workers."""
+    _check(gpu, _make(M, 328, 264, R, 21, dtype, out, M + R), out, (M, R), in_place=in_place)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("M", [20, 3400])
 @pytest.mark.parametrize("R", [16, 48, 100])

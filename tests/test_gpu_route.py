@@ -171,6 +171,45 @@ def test_many_rows_next_to_one_another(gpu, E):
                 _check(gpu, z if groups == 1 else rows, 8, what=(E, kw, "no bias"), **kw)
 
 
+@pytest.mark.parametrize("E,rows", [(48, 2500), (256, 4500)])
+def test_rows_next_to_one_another_four_to_a_wave(gpu, E, rows):
+    """Calls above the number of tokens from which four share a wave: near sums, pairs
+    and exact ties among ordinary rows, between groups too."""
+    g = torch.Generator().manual_seed(E + 1)
+    for score in ("sigmoid", "softmax"):
+        near = lambda z: torch.sigmoid(z.double()) if score == "sigmoid" else torch.softmax(z.double(), 1)  # noqa: E731
+        z = torch.randn(rows, E, generator=g)
+        bias = 0.75 - near(z[:1])[0].float()
+        z[1:500] = z[:1] * (1 + 2.0 ** -21 * torch.randn(499, 1, generator=g))
+        z[500:1000, 1::2] = z[500:1000, ::2]
+        z[1000:1200, 1::2] = z[1000:1200, ::2] * (1 + 2.0 ** -23)
+        c = (near(z) + bias.double()).numpy()
+        clear = torch.from_numpy(np.diff(np.sort(c, axis=1), axis=1)[:, -10:].min(axis=1) > 1e-13)
+        assert int(clear[:500].sum()) > 300
+        for groups in (1, 4, 6 if E % 6 == 0 else 8):
+            for group_score in ("max", "top2"):
+                kw = dict(score=score, groups=groups, topk_groups=max(1, groups // 2), group_score=group_score)
+                v = np.sort(c.reshape(rows, groups, -1), axis=2)
+                v = np.sort(v[:, :, -1] if group_score == "max" else v[:, :, -2:].sum(axis=2), axis=1)
+                keep = clear if groups == 1 else clear & torch.from_numpy(np.diff(v, axis=1).min(axis=1) > 1e-13)
+                some = z[keep].repeat(2, 1)[:rows]   # as many as before: all near rows, some others twice
+                assert len(some) > (2048 if E <= 64 else 4096)
+                _check(gpu, some, 8, bias=bias, what=(E, kw), **kw)
+                _check(gpu, z if groups == 1 else some, 8, what=(E, kw, "no bias"), **kw)
+
+
+@pytest.mark.parametrize("E,rows", [(64, 2048), (64, 2049), (60, 3001), (65, 4096), (65, 4097), (256, 4099), (250, 5001)])
+def test_both_sides_of_four_to_a_wave(gpu, E, rows):
+    for i, kw in enumerate(CONFIGS):
+        for groups in (1, 4 if E % 4 == 0 else 5):
+            if E % groups:
+                continue
+            group_score = ("max", "top2")[i % 2]
+            mask = torch.rand(rows, generator=torch.Generator().manual_seed(i)) < 0.2 if i % 3 else None
+            _check(gpu, _logits(rows, E, ("fp32", "bf16", "fp16")[i % 3], E + i), 6, pad=i % 2, what=(E, rows, kw, groups),
+                   groups=groups, topk_groups=groups - groups // 2, group_score=group_score, mask=mask, **kw)
+
+
 def test_two_best_without_a_bias(gpu):
     """The groups' values are sums of scores, not of logits."""
     z = torch.tensor([[5.0, -9.0, 4.0, 3.9, -1.0, -1.0, 0.0, 0.0]])
