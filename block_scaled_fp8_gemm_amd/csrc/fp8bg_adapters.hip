@@ -7,10 +7,10 @@
 // goes over the different ones among them, so that tokens share an adapter's
 // reads wherever they stand, and a run of one adapter is one pass.
 //
-// 16384 tokens of 16 adapters of rank 16, 4096 to 4096 columns, bf16: 37 us for the
-// first product (136 MB read by the counters, 3.6 TB/s) and 60 for the second (146 read
-// and 134 written, 4.7 TB/s); a large copy reaches 5.2.  64 tokens of a request each: 4.3
-// and 4.8 us, bound by latency.  One kernel for both, a workgroup per 16 tokens with h in
+// 16384 tokens of 16 adapters of rank 16, 4096 to 4096 columns, bf16: 39 us for the
+// first product (136 MB read by the counters, 3.5 TB/s) and 63 for the second (146 read
+// and 134 written, 4.5 TB/s); a large copy reaches 5.2.  64 tokens of a request each: 4.6
+// and 5.0 us, bound by latency.  One kernel for both, a workgroup per 16 tokens with h in
 // LDS, took 11.4 us there against 8.9 in a graph, and was no faster for many (104 both).
 #include <type_traits>
 
@@ -690,12 +690,16 @@ hipError_t add(AdapterArgs a) {
 }  // namespace
 
 // How many workgroups split K: enough that few tokens still cover the device (64
-// tokens of rank 16: one 12.1 us, four 8.4; 16384 tokens: one 106, four 101).
+// tokens of rank 16: one 12.1 us, four 8.4).  Many tokens take fewer, which
+// halves h, and the second product reads all parts of it: 16384 tokens of rank 16, two
+// and four, the kernels 38.8 + 62.6 and 35.5 + 65.9, a call 97.9 and 99.6.
 int adapter_splits(int64_t M, int64_t K, int64_t R) {
-  const int64_t tiles = (M + 15) / 16, groups = many_tokens(tiles, R) ? (tiles + 3) / 4 : tiles;
+  const int64_t tiles = (M + 15) / 16;
+  const bool many = many_tokens(tiles, R);
+  const int64_t groups = many ? (tiles + 3) / 4 : tiles;
   int64_t most = (K + 255) / 256;
   most = most < kMaxSplits ? most : kMaxSplits;
-  const int64_t s = 2048 / (groups > 0 ? groups : 1);
+  const int64_t s = (many ? 512 : 2048) / (groups > 0 ? groups : 1);
   return (int)(s < 1 ? 1 : s < most ? s : most);
 }
 

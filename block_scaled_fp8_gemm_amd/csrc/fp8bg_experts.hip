@@ -246,10 +246,10 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // between the kept and the others is checked like the rest (scores without a bias
 // are off by 1.5 |z| U < 2^-16.9 of themselves, or by 2^-126).
 //
-// 16384 tokens of 256 fp32 logits, sigmoid, bias, 4 of 8 groups, 8 experts: 14.5 us (18
+// 16384 tokens of 256 fp32 logits, sigmoid, bias, 4 of 8 groups, 8 experts: 15.6 us (18
 // MB, whose copy takes 3.4; every score in 64 bits took 54).  The comparisons bound it:
 // 16-bit logits without bias or groups take 7.1.  Few tokens are bound by latency: 64 of
-// them 5.2 us, one of bf16 logits 2.8.
+// them 6.1 us, one of bf16 logits 2.9.
 template <typename T, int L, int VPL, bool EXACT>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
   constexpr int kExact = L == 16 ? VPL < 4 ? 1 : VPL / 4 : VPL;  // experts per lane of a whole wave
@@ -641,7 +641,7 @@ __device__ __forceinline__ void exclusive_sums(int (&v)[1024 / THREADS], int* su
 // by counting, over all choices, those of lower experts and the earlier ones of
 // the same: the lanes' comparisons are masks in scalar registers, whose bits
 // the scalar unit counts.  The first workgroup makes the offsets.  64 tokens of 8
-// choices and 4096 bytes: 5.2 us, bound by latency.
+// choices and 4096 bytes: 5.4 us, bound by latency.
 __global__ __launch_bounds__(256) void k_dispatch_few(DispatchArgs a) {
   __shared__ int shared[1024];
   __shared__ int sums[4];
@@ -709,7 +709,7 @@ __global__ __launch_bounds__(256) void k_dispatch_few(DispatchArgs a) {
 // atomics on integers: their order changes nothing), which gives its starts without a
 // word from the others, and ranks its own, 1024 at a time: a wave finds the lanes
 // of each expert bit by bit, and the waves' counts are summed in their order.  32768
-// choices: 8.0 us.
+// choices: 8.3 us.
 __global__ __launch_bounds__(1024) void k_slots(DispatchArgs a) {
   extern __shared__ int wave_counts[];  // [16][E]
   __shared__ int counts[2048], sums[16];  // choices before its own by expert, and the others
@@ -785,8 +785,8 @@ __global__ __launch_bounds__(1024) void k_slots(DispatchArgs a) {
   }
 }
 
-// TPT threads per token.  4096 tokens of 8 x 4096 bytes: 28.9 us, 151 MB at the 5.2 TB/s
-// of a large copy.
+// TPT threads per token.  4096 tokens of 8 x 4096 bytes: 30.4 us, 151 MB at 5.0 TB/s
+// (a large copy: 5.2).
 template <int TPT>
 __global__ __launch_bounds__(256) void k_move(DispatchArgs a) {
   __shared__ int shared[256 / TPT][64];
@@ -802,8 +802,8 @@ __global__ __launch_bounds__(256) void k_move(DispatchArgs a) {
 // ---------------------------------------------------------------------------
 // Back into token order: a thread sums 16 bytes' worth of a token's columns, the
 // loads of up to kRows rows in flight together.  A token's slots and weights are in
-// scalar registers.  4096 tokens of 8 x 4096 bf16 with a base: 62.5 us, 336 MB at 5.4
-// TB/s (one row after the other 82); 64 tokens 3.4, latency.
+// scalar registers.  4096 tokens of 8 x 4096 bf16 with a base: 64.2 us, 336 MB at 5.2
+// TB/s (one row after the other 82); 64 tokens 3.6, latency.
 // ---------------------------------------------------------------------------
 template <typename T, int VE>
 __device__ __forceinline__ void load_floats(const void* p, int64_t at, int n, float (&v)[VE]) {
@@ -917,7 +917,8 @@ hipError_t launch_dispatch(DispatchArgs a) {
     return hipGetLastError();
   }
   a.own = ((int64_t)a.n + 256 * 1024 - 1) / (256 * 1024) * 1024;  // at most a workgroup per compute unit
-  hipLaunchKernelGGL(k_slots, dim3((unsigned)((a.n + a.own - 1) / a.own)), dim3(1024), 16 * a.E * sizeof(int), a.stream, a);
+  hipLaunchKernelGGL(k_slots, dim3((unsigned)((a.n + a.own - 1) / a.own)), dim3(1024), 16 * a.E * sizeof(int), a.stream,
+                     a);
   // A wave per token for short rows, else four.  16384 tokens of 6 experts, us of the two
   // kernels with one and with four: 256 bytes 23.9 and 28.9, 1024 39.4 and 45.3, 2048 62.8
   // and 63.2, 4096 113 and 103; 1001 tokens: 1024 bytes 8.7 and 8.8, 2048 10.4 and 9.9.
