@@ -43,8 +43,8 @@ enum { FBG_GROUP_MAX = 0, FBG_GROUP_TOP2 = 1 };
  * bias [E] fp32 or NULL; mask [T] bytes or NULL: a token whose byte is not zero
  * gets experts -1 and weights 0.  A row that holds a NaN or +infinity (or with
  * a bias that does), or a softmax of nothing but -infinity, has no routing: its
- * weights are NaN and its experts 0 .. topk-1.  An infinity of -1 in
- * a logit or a bias otherwise leaves its expert to be chosen last.
+ * weights are NaN and its experts 0 .. topk-1.  A -infinity in a logit without a
+ * bias, or in a bias, otherwise leaves its expert to be chosen last.
  *
  * weights [T,topk] fp32 and experts [T,topk] int32, contiguous, 4-byte aligned,
  * overlapping nothing.  E <= 1024, topk <= 64, topk <= topk_groups * E / groups,
@@ -102,11 +102,11 @@ int fbg_combine_experts(const void *rows, int64_t ldrows, int dtype, int64_t R, 
  * x [M,K], A [L,R,K] and B [L,N,R] contiguous, of `dtype` (bf16 or fp16); y and
  * out [M,N] of out_dtype; adapters [M] int32; scales [L] fp32, or NULL for ones.
  * Adapters of a lower rank than R are padded with zeros.  Sums are fp32, the R
- * values between the two products stay fp32, and out is rounded once.  out may be y itself (same
- * address and pitch: rows without an adapter are then not touched), and
- * otherwise overlaps nothing.  R <= 256, K <= 2^24 - 128.  x, A, B, y and out aligned to their
- * elements.  K, R or L of 0: out is y.  workspace: 16-byte aligned device memory of
- * at least fbg_add_adapters_workspace_size(M, N, K, R) bytes, of any content; too
+ * values between the two products stay fp32, and out is rounded once.  out may be
+ * y itself (same address and pitch: rows without an adapter are then not touched),
+ * and otherwise overlaps nothing.  R <= 256, K <= 2^24 - 128.  x, A, B, y and out
+ * aligned to their elements.  K, R or L of 0: out is y.  workspace: 16-byte aligned
+ * device memory of at least fbg_add_adapters_workspace_size(M, N, K, R) bytes, of any content; too
  * small -> OUT_OF_MEMORY.  Calls that overlap in time must not share one.
  */
 int fbg_add_adapters(const void *y, int64_t ldy, const void *x, int64_t ldx, const void *A, const void *B,
