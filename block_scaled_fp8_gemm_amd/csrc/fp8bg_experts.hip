@@ -582,7 +582,7 @@ struct Mover {
       : x(a.x + token * a.x_pitch), bytes(a.row_bytes), t(t_) {
     if ((int64_t)t * 16 < bytes && bytes >= 16) head = *reinterpret_cast<const U4*>(x + start(t * 16));
   }
-  // The last 16 bytes of a row overlap those before them (one by one they took 4 us).
+  // The last 16 bytes of a row overlap those before them.
   __device__ __forceinline__ int64_t start(int64_t at) const { return at + 16 <= bytes ? at : bytes - 16; }
   __device__ __forceinline__ void put(const DispatchArgs& a, int64_t token, const int* slots) const {
     for (int64_t at = (int64_t)t * 16; at < bytes; at += TPT * 16) {
@@ -906,13 +906,14 @@ hipError_t launch_route(const RouteArgs& a) {
   }
 }
 
-// Up to this many comparisons of a token's choices with all of them the kernel
-// that makes them is the faster one (64 tokens of 8 choices 5.1 us against 7.3,
-// 256 of 8 8.3 against 8.6, 512 of 8 13.4 against 10.9, 2048 of 2 17 against 8.1).
-constexpr int64_t kFewComparisons = (int64_t)1 << 19;
+// Up to this many pairs of a token and a choice the kernel that compares them all is the
+// faster one.  us with it and without, rows of 4096 bytes: 64 tokens of 8 choices 5.1 and
+// 7.3, 256 of 8 8.1 and 8.6, 320 of 8 9.4 and 9.1, 512 of 8 12.8 and 10.3; 512 of 4 7.4
+// and 8.3, 1024 of 1 5.9 and 7.2, 2048 of 1 12.2 and 8.7.
+constexpr int64_t few_comparisons(int topk) { return (int64_t)1 << (topk <= 4 ? 20 : 19); }
 
 hipError_t launch_dispatch(DispatchArgs a) {
-  if ((int64_t)a.T * a.n <= kFewComparisons) {
+  if ((int64_t)a.T * a.n <= few_comparisons(a.topk)) {
     hipLaunchKernelGGL(k_dispatch_few, dim3(a.n > 0 ? a.T + 1 : 1), dim3(256), 0, a.stream, a);
     return hipGetLastError();
   }

@@ -61,6 +61,14 @@ def test_order(gpu, tokens, topk, E, kind):
     _check(gpu, ids, E, _x(tokens, 40, torch.int8, 1), torch.rand(tokens))
 
 
+@pytest.mark.parametrize("tokens,topk", [(1024, 1), (1025, 1), (724, 2), (725, 2), (512, 4), (513, 4), (323, 5), (324, 5),
+                                         (256, 8), (257, 8), (90, 64), (91, 64)])
+@pytest.mark.parametrize("E", [16, 1000])
+@pytest.mark.parametrize("kind", ["even", "some", "one"])
+def test_both_sides_of_few_choices(gpu, tokens, topk, E, kind):
+    _check(gpu, _ids(tokens, topk, E, tokens, kind), E, _x(tokens, 515, torch.bfloat16, 2), torch.rand(tokens, 3))
+
+
 @pytest.mark.parametrize("tokens,topk,E", [(40000, 8, 256), (20001, 3, 1000), (131072, 1, 16), (4096, 8, 128)])
 @pytest.mark.parametrize("kind", ["even", "some", "one"])
 def test_many_tokens(gpu, tokens, topk, E, kind):
