@@ -455,6 +455,9 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
     // What the others behind lane topk's are at most: the key's value and all that the
     // place took from another's.
     const float rest = other_key == kNone ? -kInf : unordered(other_key | kPlace);
+    // And how far above it one of them may be: the sum's rounding grows with the value, so
+    // a lower one stays below the same line.  (A -infinity is exact.)
+    const float rest_off = off > 0.0f && rest > -kInf ? off + 0x1p-24f * __builtin_fabsf(rest) : 0.0f;
     const bool there = l <= a.topk && rank_key != kNone;
     float v = z, most = 0.0f;
     if (a.bias && there) {
@@ -465,7 +468,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
     const bool next_there = __shfl((int)there, lane + 1, 64) != 0;
     bool clear = true;
     if (l < a.topk && next_there) clear = v - next > lim;
-    if (l == a.topk - 1 && other_key != kNone) clear = clear && v - rest > most + off;
+    if (l == a.topk - 1 && other_key != kNone) clear = clear && v - rest > most + rest_off;
     const bool again = !clear && !(softmax && a.bias);
     sure = sure && (clear || again);
     if (__ballot(again)) {
@@ -489,8 +492,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
       expert = __shfl(expert, from, 64);
       z = __shfl(z, from, 64);
       d = __shfl(d, from, 64);
-      const float lim = off > 0.0f ? off + 0x1p-24f * __builtin_fabsf(rest) : 0.0f;
-      if (l == a.topk - 1 && other_key != kNone) sure = sure && d - (double)rest > (double)lim;
+      if (l == a.topk - 1 && other_key != kNone) sure = sure && d - (double)rest > (double)rest_off;
     }
   }
   float weight = 0.0f;
