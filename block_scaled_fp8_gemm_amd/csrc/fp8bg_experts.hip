@@ -242,8 +242,8 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // compared in 64 bits, the first topk + 1 of them alone; where that does not settle a row
 // (three in a heap, the line between groups, a softmax with a bias), it is done again by
 // the whole wave, which takes 5 us.  A group's two best are taken in 32
-// bits, by its lanes where it is 2^p of them, else by one lane from LDS, and the line
-// between the kept and the others is checked like the rest (scores without a bias
+// bits, by its lanes where it is 2^p of them, else by one lane from LDS, and the kept
+// and the others are checked against each group's own bound (scores without a bias
 // are off by 1.5 |z| U < 2^-16.9 of themselves, or by 2^-126).
 //
 // 16384 tokens of 256 fp32 logits, sigmoid, bias, 4 of 8 groups, 8 experts: 15.6 us (18
@@ -381,12 +381,19 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
         for (int i = 0; i < size; ++i) take(values[l * size + i]);
       }
     }
-    float value = best;
-    if (two) {
-      const bool scored = EXACT || !a.bias;
-      value = scored ? score_of(best) : best;
-      if (a.E > a.groups) value += scored ? score_of(second) : second;
+    // A group's value and how far it may be off: each sum by its score and its own
+    // rounding, whatever is left of the two when they cancel.  (Half of both, so that no
+    // sum passes the largest number; a -infinity is exact.)
+    const auto plus_off = [&](float u) { return off + 0x1p-23f * __builtin_fabsf(u); };
+    float value = best, value_off = 2.0f * plus_off(best);
+    if (two && (EXACT || !a.bias)) {
+      value = score_of(best) + (a.E > a.groups ? score_of(second) : 0.0f);
+      value_off = 0x1p-16f * value + 0x1p-120f;
+    } else if (two && a.E > a.groups) {
+      value = 0.5f * best + 0.5f * second;
+      value_off = plus_off(best) + plus_off(second) + 0x1p-120f;
     }
+    if (value == -kInf) value_off = 0.0f;
     const int lanes = aligned ? a.group_lanes : 1, last = aligned ? L : a.groups;
     const bool real = aligned ? e0 < a.E : l < a.groups;
     if (!real) value = -kInf;
@@ -398,14 +405,12 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
     }
     const bool stays = real && better < a.topk_groups;
     if (two || off > 0.0f) {
-      // The last that stays and the first that does not.
-      const auto value_at = [&](int rank) {
-        const uint64_t at = __ballot(better == rank) >> (L == 64 ? 0 : lane & 48);
-        return __shfl(value, (int)__builtin_ctzll(at | 1ull << 63) + base, 64);
-      };
-      const float low = value_at(a.topk_groups - 1), high = value_at(a.topk_groups);
-      const float relative = off > 0.0f ? 0x1p-22f : 0x1p-16f;
-      sure = low - high > relative * (__builtin_fabsf(low) + __builtin_fabsf(high)) + 4.0f * off + 0x1p-120f || high == -kInf;
+      // The least that one that stays may be, and the most that another may be: not only
+      // the two next to the line, since each group has a bound of its own.
+      const auto smaller = [](float x, float y) { return x < y ? x : y; };
+      const float low = over_lanes<L>(stays ? value - value_off : kInf, smaller);
+      const float high = over_lanes<L>(real && !stays ? value + value_off : -kInf, larger);
+      sure = low > high || high == -kInf;
     }
     if (aligned) {
       kept = stays ? ~0u : 0;

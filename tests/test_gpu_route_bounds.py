@@ -1,6 +1,6 @@
 """What routing may call settled in 32 bits, at sums of any size: the last chosen
-expert against all that is no candidate.  The choice is that of the sums in 64
-bits."""
+expert against all that is no candidate, and groups whose two best cancel.  The
+choice is that of the sums in 64 bits."""
 import numpy as np
 import pytest
 import torch
@@ -68,3 +68,65 @@ def test_the_last_chosen(gpu, centre, E, place, rows, score, width):
         z, bias = _near_one_border(rows, E, place, centre, width, above, score, seed)
         got = gpu.route_experts(z.to(DEV), above + 1, score=score, bias=bias.to(DEV))
         T.assert_route(got, T.route(z, above + 1, score=score, bias=bias), (centre, E, score, seed))
+
+def _cancelling(rows, E, groups, sizes, spread, seed):
+    """Logits and a bias by which each group's two best sum to about one half; group
+    g's biases are +sizes[g] and -sizes[g] and the rest of it far below."""
+    rng = np.random.default_rng(seed)
+    n = E // groups
+    size = np.asarray(sizes, np.float64)[np.arange(groups) % len(sizes)]
+    bias = np.empty((groups, n), np.float32)
+    bias[:] = -2 * size[:, None] - 3
+    bias[:, 0], bias[:, n - 1] = size, -size
+    for g in range(groups):
+        bias[g] = rng.permutation(bias[g])
+    best, second = bias.argmax(axis=1), np.empty(groups, int)
+    for g in range(groups):
+        second[g] = np.argsort(-bias[g], kind="stable")[1]
+    z = rng.standard_normal((rows, groups, n))
+    s = 0.3 + 0.2 * rng.random((rows, groups))
+    at = np.arange(groups)
+    total = 0.9 + spread * rng.standard_normal((rows, groups))
+    z[:, at, best] = np.log(s / (1 - s))
+    z[:, at, second] = np.log((total - s) / (1 - total + s))
+    z = z.reshape(rows, E).astype(np.float32)
+    bias = bias.reshape(E)
+    c = 1 / (1 + np.exp(-z.astype(np.float64))) + bias.astype(np.float64)
+    v = np.sort(np.sort(c.reshape(rows, groups, n), axis=2)[:, :, -2:].sum(axis=2), axis=1)
+    clear = np.diff(v, axis=1).min(axis=1) > 1e-15 * max(sizes) + 1e-14
+    assert clear.mean() > 0.9
+    return torch.from_numpy(z[clear]), torch.from_numpy(bias)
+
+
+@pytest.mark.parametrize("sizes,spread", [((0.3,), 2e-7), ((8.0,), 1e-6), ((100.0,), 3e-6), ((30.0, 90.0), 3e-6),
+                                          ((0.1, 1e3, 0.1, 1e5), 3e-3), ((1e5, 0.2), 3e-3), ((1e5, 1e5, 0.2, 0.2), 1e-3)])
+@pytest.mark.parametrize("E,groups,rows", [(8, 4, 4000), (64, 8, 1500), (64, 8, 3000), (256, 8, 3000), (256, 8, 5500),
+                                           (60, 5, 3000), (250, 10, 5500), (1000, 20, 2000)])
+def test_two_best_that_cancel(gpu, sizes, spread, E, groups, rows):
+    z, bias = _cancelling(rows, E, groups, sizes, spread, E + groups)
+    for keep in sorted({1, groups // 2, groups - 1}):
+        kw = dict(score="sigmoid", bias=bias, groups=groups, topk_groups=keep, group_score="top2")
+        got = gpu.route_experts(z.to(DEV), 1, **{**kw, "bias": bias.to(DEV)})
+        # One choice: of the kept groups' experts the largest, which need not tell the groups apart;
+        # as many as are kept, the largest of each.
+        T.assert_route(got, T.route(z, 1, **kw), (sizes, E, keep))
+        got = gpu.route_experts(z.to(DEV), 2 * keep, **{**kw, "bias": bias.to(DEV)})
+        T.assert_route(got, T.route(z, 2 * keep, **kw), (sizes, E, keep))
+
+
+@pytest.mark.parametrize("rows", [5, 5000])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_two_best_past_the_largest_fp32(gpu, rows, score):
+    """Sums of two that fp32 cannot hold, of either sign, next to groups of -infinity."""
+    z = torch.randn(rows, 32, generator=torch.Generator().manual_seed(rows))
+    for sign in (1.0, -1.0):
+        bias = torch.full((8, 4), -3.4e38)
+        for g, (best, second) in enumerate(((2.0, 1.9), (2.1, 1.9), (2.0, 1.8), (1.9, 1.9), (2.2, 1.7), (1.8, 1.8))):
+            bias[g, 1], bias[g, 3] = sign * best * 1e38, sign * second * 1e38
+        bias[6] = -float("inf")
+        bias[7, 1:] = -float("inf")
+        bias = bias.view(32)
+        for keep in (1, 2, 3, 5, 6, 7):
+            kw = dict(score=score, bias=bias, groups=8, topk_groups=keep, group_score="top2")
+            got = gpu.route_experts(z.to(DEV), 2, **{**kw, "bias": bias.to(DEV)})
+            T.assert_route(got, T.route(z, 2, **kw), (sign, keep))
