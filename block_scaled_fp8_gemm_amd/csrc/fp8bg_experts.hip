@@ -833,16 +833,16 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.z * kGridY + blockIdx.y;
   int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VE;
-  if (t >= a.T) return;
+  if (t >= a.T || at - lane * VE >= a.D) return;  // whole waves: any lane's slot is read below
   const int slot_of = lane < a.topk ? a.slots[t * a.topk + lane] : -1;
   const float weight_of = lane < a.topk ? a.weights[t * a.topk + lane] : 0.0f;
-  if (at >= a.D) return;
   // A last chunk that D cuts is taken from the row's end; its first columns are
-  // another thread's, and not stored.
+  // another thread's, and not stored.  A lane past it takes it too and stores none.
   const bool whole = a.D >= VE;
+  const int n = whole ? VE : at == 0 ? a.D : 0;
   int cut = 0;
-  if (whole && at + VE > a.D) cut = (int)(at + VE - a.D), at = a.D - VE;
-  const int n = whole ? VE : a.D;
+  if (whole && at + VE > a.D) cut = at < a.D ? (int)(at + VE - a.D) : VE, at = a.D - VE;
+  if (!whole) at = 0;
   float acc[VE] = {};
   if (a.base) {
     if (a.base_is_out) load_floats<O>(a.base, t * a.ldbase + at, n, acc);
