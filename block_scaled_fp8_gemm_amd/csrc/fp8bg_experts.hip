@@ -889,7 +889,7 @@ template <typename T, typename O>
 hipError_t combine(const CombineArgs& a) {
   constexpr int kCols = 256 * 16 / (int)sizeof(T);
   const unsigned y = a.T < kGridY ? a.T : kGridY;
-  const dim3 g((a.D + kCols - 1) / kCols, y, (a.T + y - 1) / y);
+  const dim3 g((unsigned)(((int64_t)a.D + kCols - 1) / kCols), y, (a.T + y - 1) / y);
   hipLaunchKernelGGL((k_combine<T, O>), g, dim3(256), 0, a.stream, a);
   return hipGetLastError();
 }
