@@ -252,8 +252,8 @@ __device__ __forceinline__ void add_products(const V (&w)[4], const V (&h)[TERMS
   }
 }
 
-// h's ranks r .. r + 7 of one token, summed over the parts of K, times scale.
-__device__ __forceinline__ void load_hidden(const AdapterArgs& a, const float* row, int r, float scale, float (&v)[8]) {
+// h's ranks r .. r + 7 of one token, summed over the parts of K.
+__device__ __forceinline__ void load_hidden(const AdapterArgs& a, const float* row, int r, float (&v)[8]) {
   v4f part[kMaxSplits][2];
   const int64_t next = (int64_t)a.M * a.pitch;
 #pragma unroll
@@ -265,7 +265,52 @@ __device__ __forceinline__ void load_hidden(const AdapterArgs& a, const float* r
     for (int s = 1; s < kMaxSplits; ++s)
       if (s < a.splits) part[0][k] += part[s][k];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * k + i] = r < a.pitch ? part[0][k][i] * scale : 0.0f;
+    for (int i = 0; i < 4; ++i) v[4 * k + i] = r < a.pitch ? part[0][k][i] : 0.0f;
+  }
+}
+
+// Whether one of a token's 32 ranks, eight in each of its four lanes, is a NaN.
+__device__ __forceinline__ bool holds_nan(const float (&v)[8], int j) {
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) nan |= v[i] != v[i];
+  const uint64_t b = __ballot(nan), c = b | b >> 32;
+  return (c | c >> 16) >> j & 1;
+}
+
+__device__ __forceinline__ bool holds_nan(const v4f (&acc)[4]) {
+  const v4f s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  const float t = (s[0] + s[1]) + (s[2] + s[3]);
+  return t != t;
+}
+
+// Results that are no number though the token's h, `row`, holds none that is not: the
+// terms are not h where that is infinite or next to the largest number, and cancel
+// times an infinite weight.  They are summed as the formula has them, rank by rank in
+// fp32, one after the other (eight at once took 30 registers of every call's, and 512
+// tokens of rank 64 51 us instead of 37).
+template <typename T>
+__device__ __forceinline__ void sum_again(const AdapterArgs& a, const T* B, const float* row, int64_t n0, int g,
+                                          v4f (&acc)[4]) {
+  asm volatile("" : "+v"(g), "+v"(row));  // nothing of this is computed ahead of the branch (5 registers)
+  const int64_t next = (int64_t)a.M * a.pitch;
+#pragma unroll 1
+  for (int k = 0; k < 16; ++k) {
+    const int64_t n = n0 + 32 * (k >> 3) + 8 * g + (k & 7);
+    const T* w = B + (n < a.N ? n : a.N - 1) * a.R;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int r = 0; r < a.R; ++r) {
+      float h = row[r];
+#pragma unroll 1
+      for (int p = 1; p < a.splits; ++p) h += row[p * next + r];
+      s = __builtin_fmaf((float)w[r], h, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float v = acc[i >> 2][i & 3];
+      acc[i >> 2][i & 3] = i == k && v != v ? s : v;
+    }
   }
 }
 
@@ -374,7 +419,8 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
     const float scale = a.scales ? a.scales[cur] : 1.0f;
     V h[NC][kTerms];
     float unit[NC];
-    const auto products = [&](const Weights& b, v4f (&acc)[4]) {
+    bool number = true;
+    const auto products = [&](const Weights& b, int64_t n0, v4f (&acc)[4]) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         V w[4];
@@ -382,6 +428,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
         for (int t = 0; t < 4; ++t) w[t] = weights_of<T, RANKS>(b.v[c][t], 32 * c + 8 * g, a.R);
         add_products<kTerms>(w, h[c], unit[c], acc);
       }
+      if (mine && number && holds_nan(acc)) sum_again(a, B, hrow, n0, g, acc);
     };
     Weights b = load_b(n_first);
     Outputs y;
@@ -390,7 +437,8 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float v[8];
-      load_hidden(a, hrow, 32 * c + 8 * g, scale, v);
+      load_hidden(a, hrow, 32 * c + 8 * g, v);
+      number = number && !holds_nan(v, j);
       unit[c] = split_terms<T, kTerms>(v, h[c]);
     }
     // A lane's results are of its own token: those of the others' adapters,
@@ -404,12 +452,12 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);  // on their way before the products
       v4f acc[4] = {};
-      products(b, acc);
+      products(b, n0, acc);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         O8 v = __builtin_bit_cast(O8, y.v[q]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (O)((float)v[i] + acc[2 * q + (i >> 2)][i & 3]);
+        for (int i = 0; i < 8; ++i) v[i] = (O)__builtin_fmaf(acc[2 * q + (i >> 2)][i & 3], scale, (float)v[i]);
         if (mine) __builtin_memcpy(orow + n0 + 32 * q + 8 * g, &v, sizeof(v));
       }
       b = b_next;
@@ -426,13 +474,13 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
         }
       if (n0 > n_first) b = load_b(n0);
       v4f acc[4] = {};
-      products(b, acc);
+      products(b, n0, acc);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int64_t n = n0 + 32 * q + 8 * g + i;
-          if (mine && n < a.N) orow[n] = (O)((float)v[q][i] + acc[2 * q + (i >> 2)][i & 3]);
+          if (mine && n < a.N) orow[n] = (O)__builtin_fmaf(acc[2 * q + (i >> 2)][i & 3], scale, (float)v[q][i]);
         }
     }
   });
@@ -454,17 +502,23 @@ __global__ __launch_bounds__(256) void k_expand(AdapterArgs a) {
   }
 }
 
+// Two waves to a SIMD where that costs few registers: in bf16 four tiles and ranks in parts
+// take 260 (16384 tokens of rank 60 136 us, 156 with one wave), fp16's terms 294.
+template <typename T>
+constexpr int kDeepWaves = std::is_same<T, __bf16>::value ? 2 : 1;
+
 // The same for any rank, in chunks of 32: h's terms are made once per pass, by all
 // waves, and stay in LDS.  Many tokens take 16 MT of them to a workgroup, so that a
 // block's weights come from L2 once for all (rank 64 and 16384 tokens by 4096 columns:
 // 16 tokens' workgroups read 537 MB of them, four times the outputs).
 template <typename T, typename O, int MT, Ranks RANKS>
-__global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
+__global__ __launch_bounds__(256, kDeepWaves<T>) void k_expand_deep(AdapterArgs a) {
   constexpr int YC = 2 * (int)sizeof(O) / 4, TM = 16 * MT, kTerms = kTermsOf<T, O>;
   typedef typename Vec8<T>::type V;
   typedef uint32_t U4 __attribute__((ext_vector_type(4)));
   typedef O O8 __attribute__((ext_vector_type(8)));
-  extern __shared__ v4f staged[];  // [tile of tokens][chunk][term][lane], then the units [tile][chunk][16]
+  // [tile of tokens][chunk][term][lane], then the units [tile][chunk][16], NaN where h is.
+  extern __shared__ v4f staged[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
   const int worker = worker_of(a.workers), chunks = (a.R + 31) / 32;
   float* units = reinterpret_cast<float*>(staged + MT * chunks * kTerms * 64);
@@ -484,16 +538,18 @@ __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
   };
   for_passes<MT>(id, worker, a.workers, [&](int cur, uint64_t meant) {
     bool some[MT], mine[MT];
-    int64_t row_of[MT];
+    int row_of[MT];  // in the workgroup's
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const uint32_t bits = (uint32_t)(meant >> (16 * t)) & 0xffff;
       some[t] = bits != 0;
       mine[t] = (bits >> j) & 1;
       // Lanes of other tokens read the row of one that is meant.
-      const int64_t m = m0 + 16 * t + (mine[t] ? j : __builtin_ctz(bits | 0x10000) & 15);
-      row_of[t] = m < a.M ? m : a.M - 1;
+      const int m = 16 * t + (mine[t] ? j : __builtin_ctz(bits | 0x10000) & 15);
+      row_of[t] = m0 + m < a.M ? m : (int)(a.M - 1 - m0);
     }
+    const O* y_first = reinterpret_cast<const O*>(a.y) + m0 * a.ldy;
+    O* out_first = reinterpret_cast<O*>(a.out) + m0 * a.ldout;
     const T* B = reinterpret_cast<const T*>(a.B) + (int64_t)cur * a.N * a.R;
     const float scale = a.scales ? a.scales[cur] : 1.0f;
     for (int q = w; q < MT * chunks; q += 4) {  // a wave: some of the chunks
@@ -503,11 +559,12 @@ __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
       const int64_t m = m0 + 16 * t + ((bits >> j) & 1 ? j : __builtin_ctz(bits));
       float v[8];
       V h[kTerms];
-      load_hidden(a, a.h + m * a.pitch, 32 * c + 8 * g, scale, v);
+      load_hidden(a, a.h + m * a.pitch, 32 * c + 8 * g, v);
+      const bool nan = holds_nan(v, j);
       const float unit = split_terms<T, kTerms>(v, h);
 #pragma unroll
       for (int i = 0; i < kTerms; ++i) __builtin_memcpy(&staged[(q * kTerms + i) * 64 + lane], &h[i], 16);
-      if (g == 0) units[q * 16 + j] = unit;
+      if (g == 0) units[q * 16 + j] = nan ? __builtin_nanf("") : unit;
     }
     __syncthreads();
     const auto products = [&](const L2 (&raw)[4], int c, v4f (&acc)[MT][4]) {
@@ -531,7 +588,7 @@ __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
     if (n0 + 64 <= n_last) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        if (some[t]) y[t] = load_y(reinterpret_cast<const O*>(a.y) + row_of[t] * a.ldy, n0);
+        if (some[t]) y[t] = load_y(y_first + row_of[t] * a.ldy, n0);
     }
     for (; n0 < n_last; n0 += 256) {
       const bool whole = n0 + 64 <= n_last, more = n0 + 256 < n_last, next_whole = n0 + 320 <= n_last;
@@ -547,7 +604,7 @@ __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
         if (c == 0 && next_whole) {
 #pragma unroll
           for (int t = 0; t < MT; ++t)
-            if (some[t]) y_next[t] = load_y(reinterpret_cast<const O*>(a.y) + row_of[t] * a.ldy, n0 + 256);
+            if (some[t]) y_next[t] = load_y(y_first + row_of[t] * a.ldy, n0 + 256);
         }
         __builtin_amdgcn_sched_barrier(0);  // on their way before the products
         products(b, c, acc);
@@ -557,17 +614,25 @@ __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         if (!some[t]) continue;
-        O* orow = reinterpret_cast<O*>(a.out) + row_of[t] * a.ldout;
+        if (mine[t] && holds_nan(acc[t])) {
+          bool number = true;
+          for (int c = 0; c < chunks; ++c) {
+            const float unit = units[(t * chunks + c) * 16 + j];
+            number = number && unit == unit;
+          }
+          if (number) sum_again(a, B, a.h + (m0 + row_of[t]) * a.pitch, n0, g, acc[t]);
+        }
+        O* orow = out_first + row_of[t] * a.ldout;
         if (whole) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             O8 v = __builtin_bit_cast(O8, y[t].v[q]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = (O)((float)v[i] + acc[t][2 * q + (i >> 2)][i & 3]);
+            for (int i = 0; i < 8; ++i) v[i] = (O)__builtin_fmaf(acc[t][2 * q + (i >> 2)][i & 3], scale, (float)v[i]);
             if (mine[t]) __builtin_memcpy(orow + n0 + 32 * q + 8 * g, &v, sizeof(v));
           }
         } else {
-          const O* yrow = reinterpret_cast<const O*>(a.y) + row_of[t] * a.ldy;
+          const O* yrow = y_first + row_of[t] * a.ldy;
           O v[2][8];
 #pragma unroll
           for (int q = 0; q < 2; ++q)
@@ -581,7 +646,7 @@ __global__ __launch_bounds__(256) void k_expand_deep(AdapterArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int64_t n = n0 + 32 * q + 8 * g + i;
-              if (mine[t] && n < a.N) orow[n] = (O)((float)v[q][i] + acc[t][2 * q + (i >> 2)][i & 3]);
+              if (mine[t] && n < a.N) orow[n] = (O)__builtin_fmaf(acc[t][2 * q + (i >> 2)][i & 3], scale, (float)v[q][i]);
             }
         }
       }
