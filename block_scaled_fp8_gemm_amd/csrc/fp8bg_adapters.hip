@@ -197,11 +197,13 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a) {
 }
 
 // h in the weights' type, as a sum that the MFMA takes term by term: each term
-// is what the ones before it leave, rounded.  bf16 has fp32's range: two terms are
-// off by 2^-18 of a value, which a 16-bit output does not see, three by 2^-26.  fp16
-// goes relative to the largest of a token's 32 ranks (a power of two, returned), the
-// second term times 2^11 to stay above its smallest steps, with sums of its own:
-// off by 2^-22.
+// is what the ones before it leave, rounded.  bf16 has fp32's range: a value in [1, 2)
+// leaves at most 2^-8, that at most 2^-17 and that, of fp32's 24 bits, nothing.  So
+// three terms are h, and two are off by 2^-17 of it: for 16-bit outputs, whose rounding is
+// 2^-8 or 2^-11 of theirs, which only a y that cancels the product goes below (the third term
+// would cost them 1 to 3% of a call up to rank 64, 6% at rank 256).  fp16 goes relative to the
+// largest of a token's 32 ranks (a power of two, returned), the second term times 2^11
+// to stay above its smallest steps, with sums of its own: off by 2^-22 of the largest.
 template <typename T, typename O>
 constexpr int kTermsOf = std::is_same<T, __bf16>::value && sizeof(O) == 4 ? 3 : 2;
 

@@ -101,8 +101,12 @@ int fbg_combine_experts(const void *rows, int64_t ldrows, int dtype, int64_t R, 
  *
  * x [M,K], A [L,R,K] and B [L,N,R] contiguous, of `dtype` (bf16 or fp16); y and
  * out [M,N] of out_dtype; adapters [M] int32; scales [L] fp32, or NULL for ones.
- * Adapters of a lower rank than R are padded with zeros.  Sums are fp32, the R
- * values between the two products stay fp32, and out is rounded once.  out may be
+ * Adapters of a lower rank than R are padded with zeros.  Sums are fp32 and out is
+ * rounded once.  Between the two products the R values are summed and kept in fp32;
+ * the second takes each as a sum of 16-bit terms, which is the value itself for bf16
+ * weights and an fp32 out, off by at most 2^-17 of it for bf16 weights and a 16-bit out, and
+ * for fp16 weights by 2^-22 of the largest of its token's ranks 32 i .. 32 i + 31.
+ * Infinities and NaN go where the formula takes them.  out may be
  * y itself (same address and pitch: rows without an adapter are then not touched),
  * and otherwise overlaps nothing.  R <= 256, K <= 2^24 - 128.  x, A, B, y and out
  * aligned to their elements.  K, R or L of 0: out is y.  workspace: 16-byte aligned
