@@ -422,7 +422,9 @@ def block_norm(h: torch.Tensor, x: torch.Tensor = None, post_weight: torch.Tenso
 # ---------------------------------------------------------------------------
 # Every token picks its weights: experts, and low-rank adapters.  Declared in
 # include/fp8bg_tokens.h; checks and calls compiled as above.  Index tensors are
-# int32 and never read by the host.
+# int32 and never read by the host.  Forward only: outputs that a call makes hang on no
+# graph, and a tensor of the caller's is not written (ValueError) while gradients are
+# recorded and one of the call's tensors requires one.
 # ---------------------------------------------------------------------------
 def route_experts(logits: torch.Tensor, topk: int, score: str = "softmax", bias: torch.Tensor = None, groups: int = 1,
                   topk_groups: int = 1, group_score: str = "max", renormalize: bool = True, scale: float = 1.0,
@@ -464,7 +466,8 @@ def combine_experts(rows: torch.Tensor, slots: torch.Tensor, weights: torch.Tens
     once: rows [R,D] (bf16, fp16 or fp32) as the grouped products leave them, slots
     [T,topk] int32 from dispatch_tokens (outside 0 .. R-1: left out), weights
     [T,topk] float32, base [T,D] of the rows' or the output's type, or None.
-    out_dtype: that of `out`, or else the rows'.  `out` may be base.  See
+    out_dtype: that of `out`, or else the rows'.  `out` may be base.  No backward: with
+    `out`, under torch.no_grad() only where one of the tensors requires a gradient.  See
     fbg_combine_experts in include/fp8bg_tokens.h."""
     return (_native or _load_native()).combine_experts(rows, slots, weights, base, out_dtype, out, stream)
 
@@ -478,6 +481,7 @@ def add_adapters(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Ten
 
     x, A [L,R,K] and B [L,N,R] bf16 or fp16, y of any output type, adapters [M]
     int32, scales [L] float32 or None; rows of x, y and `out` any distance apart.
-    In place where out is None; returns the tensor written.  See
+    In place where out is None; returns the tensor written.  No backward: under
+    torch.no_grad() only, where one of the tensors requires a gradient.  See
     fbg_add_adapters in include/fp8bg_tokens.h."""
     return (_native or _load_native()).add_adapters(y, x, A, B, adapters, scales, out, stream)

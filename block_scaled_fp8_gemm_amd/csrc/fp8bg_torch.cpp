@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -16,6 +17,7 @@
 #include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <optional>
 #include <string>
 #include <utility>
@@ -312,6 +314,29 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+// Forward only.  A tensor of the caller's that is written (None: the call makes its own)
+// would stand in a graph that leaves this step out, with gradients that miss it: as
+// torch refuses `out=` there, so is that here.
+void check_forward_only(std::initializer_list<PyObject*> written, std::initializer_list<PyObject*> read) {
+  bool writes = false;
+  for (PyObject* o : written) writes |= o != Py_None;
+  if (!writes || !at::GradMode::is_enabled()) return;
+  for (const auto& list : {written, read})
+    for (PyObject* o : list)
+      if (o != Py_None && THPVariable_Unpack(o).requires_grad())
+        value_error("the operator has no backward: it does not write into a tensor of the caller's while one of its "
+                    "tensors requires a gradient (use torch.no_grad())");
+}
+
+// What was saved of them for a backward pass is out of date.
+void count_writes(std::initializer_list<PyObject*> written) {
+  for (PyObject* o : written) {
+    if (o == Py_None) continue;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+}
+
 // Which of two words `o` is.
 int one_of(PyObject* o, const char* name, const char* zero, const char* one) {
   const char* s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : "";
@@ -351,9 +376,11 @@ PyObject* route_experts(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const at::Tensor e = v[11] == Py_None ? make({T, topk}, at::kInt, dev) : tensor(v[11], "experts");
   auto* weights = static_cast<float*>(whole(w, "weights", at::kFloat, {T, topk}, dev));
   auto* experts = static_cast<int32_t*>(whole(e, "experts", at::kInt, {T, topk}, dev));
+  check_forward_only({v[10], v[11]}, {v[0], v[3]});
   check_status(fbg_route_experts(logits.data_ptr(), ld, in_code, T, E, topk, score, bias, groups, topk_groups,
                                  group_score, renormalize, (float)scale, mask, weights, experts, launch.get()),
                "fbg_route_experts");
+  count_writes({v[10], v[11]});
   return Py_BuildValue("(NN)", THPVariable_Wrap(w), THPVariable_Wrap(e));
   END_HANDLE_TH_ERRORS
 }
@@ -398,6 +425,7 @@ PyObject* dispatch_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
   } else if (v[6] != Py_None) {
     value_error("row_scale needs x_scale");
   }
+  check_forward_only({v[5], v[6]}, {v[2], v[3]});
   const auto [offsets, slots] = make_two({E + 1}, {T, topk}, dev);
   check_status(fbg_dispatch_tokens(ids, T, topk, first, E, x.data_ptr(), ldx, K, (int)size, x_scale, S,
                                    rows.data_ptr(), ldrows,
@@ -405,6 +433,7 @@ PyObject* dispatch_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                    static_cast<int32_t*>(offsets.data_ptr()), static_cast<int32_t*>(slots.data_ptr()),
                                    launch.get()),
                "fbg_dispatch_tokens");
+  count_writes({v[5], v[6]});
   PyObject* so = row_scale.defined() ? THPVariable_Wrap(row_scale) : Py_NewRef(Py_None);
   return Py_BuildValue("(NNNN)", THPVariable_Wrap(rows), so, THPVariable_Wrap(offsets), THPVariable_Wrap(slots));
   END_HANDLE_TH_ERRORS
@@ -441,9 +470,11 @@ PyObject* combine_experts(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const Launch launch(v[6], dev);
   const at::Tensor out = v[5] == Py_None ? make({T, D}, out_type, dev) : tensor(v[5], "out");
   const int64_t ldout = pitch(out, "out", out_type, T, D, dev);
+  check_forward_only({v[5]}, {v[0], v[2], v[3]});
   check_status(fbg_combine_experts(rows.data_ptr(), ldrows, in_code, R, at_slots, weights, base, ldbase, base_code,
                                    out.data_ptr(), ldout, out_code, T, topk, D, launch.get()),
                "fbg_combine_experts");
+  count_writes({v[5]});
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
@@ -471,10 +502,13 @@ PyObject* add_adapters(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const Launch launch(v[7], dev);
   const at::Tensor out = v[6] == Py_None ? y : tensor(v[6], "out");
   const int64_t ldout = pitch(out, "out", out_type, M, N, dev);
+  PyObject* const written = v[6] == Py_None ? v[0] : v[6];
+  check_forward_only({written}, {v[0], v[1], v[2], v[3], v[5]});
   const at::Tensor work = need ? make({(int64_t)need}, at::kByte, dev) : at::Tensor();
   check_status(fbg_add_adapters(y.data_ptr(), ldy, x.data_ptr(), ldx, pa, pb, ids, scales, out.data_ptr(), ldout, M, N,
                                 K, R, L, in_code, out_code, need ? work.data_ptr() : nullptr, need, launch.get()),
                "fbg_add_adapters");
+  count_writes({written});
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
