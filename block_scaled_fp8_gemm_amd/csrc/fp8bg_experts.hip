@@ -382,17 +382,19 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
       }
     }
     // A group's value and how far it may be off: each sum by its score and its own
-    // rounding, whatever is left of the two when they cancel.  (Half of both, so that no
-    // sum passes the largest number; a -infinity is exact.)
-    const auto plus_off = [&](float u) { return off + 0x1p-23f * __builtin_fabsf(u); };
-    float value = best, value_off = 2.0f * plus_off(best);
+    // rounding (U of it), whatever is left of the two when they cancel.  With the mean
+    // for the sum of two, so that none passes the largest number, that is at most off and
+    // U (|best| + |second|) / 2; the mean's rounding and that of a bound added to it are no more
+    // than the latter each.  (A -infinity is exact.)
+    float value = best, magnitude = __builtin_fabsf(best);
     if (two && (EXACT || !a.bias)) {
       value = score_of(best) + (a.E > a.groups ? score_of(second) : 0.0f);
-      value_off = 0x1p-16f * value + 0x1p-120f;
     } else if (two && a.E > a.groups) {
       value = 0.5f * best + 0.5f * second;
-      value_off = plus_off(best) + plus_off(second) + 0x1p-120f;
+      magnitude = 0.5f * magnitude + 0.5f * __builtin_fabsf(second);
     }
+    float value_off = off > 0.0f ? off + 0x1.8p-23f * magnitude : 0x1p-16f * value;
+    value_off += 0x1p-120f;
     if (value == -kInf) value_off = 0.0f;
     const int lanes = aligned ? a.group_lanes : 1, last = aligned ? L : a.groups;
     const bool real = aligned ? e0 < a.E : l < a.groups;
