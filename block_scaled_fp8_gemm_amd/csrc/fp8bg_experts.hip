@@ -874,6 +874,7 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
       for (int i = 0; i < VE; ++i) acc[i] = __builtin_fmaf(w, (float)raw[j][i], acc[i]);
     }
   }
+  if (cut == VE || n == 0) return;  // a lane past the last column
   O* out = reinterpret_cast<O*>(a.out) + t * a.ldout + at;
   O o[VE];
 #pragma unroll
