@@ -8,10 +8,12 @@
 // reads wherever they stand, and a run of one adapter is one pass.
 //
 // 16384 tokens of 16 adapters of rank 16, 4096 to 4096 columns, bf16: 39 us for the
-// first product (136 MB read by the counters, 3.5 TB/s) and 63 for the second (146 read
-// and 134 written, 4.5 TB/s); a large copy reaches 5.2.  64 tokens of a request each: 4.6
-// and 5.0 us, bound by latency.  One kernel for both, a workgroup per 16 tokens with h in
-// LDS, took 11.4 us there against 8.9 in a graph, and was no faster for many (104 both).
+// first product (136 MB read by the counters, 3.5 TB/s) and 64 for the second (146 read
+// and 134 written, 4.4 TB/s); a large copy reaches 5.2.  Neither computes for long (vector
+// and matrix instructions take 3% and 2% of the first's time, 32% and 6% of the second's).
+// 64 tokens of a request each: 4.6 and 5.1 us, bound by latency.  One kernel for both, a
+// workgroup per 16 tokens with h in LDS, took 11.4 us there against 8.9 in a graph, and
+// was no faster for many (104 both).
 #include <type_traits>
 
 #include "fp8bg_device.hpp"
@@ -648,7 +650,8 @@ __global__ __launch_bounds__(256, kDeepWaves<T>) void k_expand_deep(AdapterArgs 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int64_t n = n0 + 32 * q + 8 * g + i;
-              if (mine[t] && n < a.N) orow[n] = (O)__builtin_fmaf(acc[t][2 * q + (i >> 2)][i & 3], scale, (float)v[q][i]);
+              const float sum = acc[t][2 * q + (i >> 2)][i & 3];
+              if (mine[t] && n < a.N) orow[n] = (O)__builtin_fmaf(sum, scale, (float)v[q][i]);
             }
         }
       }
@@ -701,7 +704,12 @@ void expand_deep(const AdapterArgs& a, int64_t tiles, int64_t ranges) {
   else hipLaunchKernelGGL((k_expand_deep<T, O, MT, kPart>), g, b, lds, a.stream, a);
 }
 
-// Blocks of columns one after the other where there are many tokens.
+// Blocks of columns one after the other where there are many tokens: up to four, as long
+// as 1024 workgroups are left.  A batch of 12 prompts, us, one, two, four and eight blocks
+// at most: rank 16, 4096 tokens 37.4, 29.2, 26.8 and 28.3, 16384 114, 102, 101 and 106; rank 64,
+// 16384 tokens 147, 138, 134 and 134.  512, 1024 and 2048 workgroups left: rank 64, 64 tokens 14.8,
+// 13.4 and 13.4, 16384 134, 134 and 138; rank 128, 301 tokens 29.3, 24.9 and 24.8, 4096 68.4, 68.5
+// and 74.3.
 template <typename T, typename O>
 void second(AdapterArgs a, int64_t tiles) {
   constexpr int MT = sizeof(O) == 4 ? 2 : 4;
@@ -733,10 +741,14 @@ template <typename T>
 hipError_t add(AdapterArgs a) {
   const int64_t tiles = ((int64_t)a.M + 15) / 16;
   // Few tokens: a worker for each adapter that a tile may hold.  Many: the
-  // tiles cover the device, and their tokens come in runs.  Rank 16, us with 16 workers, 4
-  // and 1, prompts / requests of one token: 400 tokens 11.5 and 10.2 / 21.7 and 24.8 with 16
-  // and 4, 1024 15.8, 13.8, 15.4 / 40.1, 41.0, 51.0, 4096 36.3, 26.8, 29.4 / 101, 91, 125,
-  // 16384 149, 106, 102 / 403, 350, 355.
+  // tiles cover the device, and their tokens come in runs.  us with 16 workers, 4 and 1, 8
+  // prompts / requests of one token over 16 adapters:
+  //   tokens  rank 16                       rank 64                       rank 128
+  //       64   7.7  7.7 15.0 / 8.6 13.5 34.6  12.8 12.8 28.7 / 16.7 31.0 87  14.8 15.0 34.2 / 21.8 32.2 94
+  //      512  12.2 10.3 12.8 / 25.3 23.8 43   25.0 22.0 35.9 / 38.2 55.4 174 30.5 26.3 41.8 / 57.4 66.5 207
+  //     1024  15.5 14.7 15.8 / 39.6 37.6 50   32.0 23.9 36.9 / 62.9 79.5 176 40.5 31.2 49.6 / 95.8 111 208
+  //     8192  72.8 52.5 53.1 / 215 190 205    84.6 82.4 77.4 / 423 408 439   113 101 107 / 680 668 708
+  //    16384  144 106 101 / 403 351 361       134 123 124 / 788 763 750      189 178 180 / 1262 1254 1238
   a.workers = tiles <= 32 ? 16 : tiles <= 512 ? 4 : 1;
   while (a.workers / 2 >= a.M) a.workers /= 2;
   if (a.R > 0 && a.L > 0 && a.K > 0) {
@@ -756,10 +768,13 @@ hipError_t add(AdapterArgs a) {
 
 }  // namespace
 
-// How many workgroups split K: enough that few tokens still cover the device (64
-// tokens of rank 16: one 12.1 us, four 8.4).  Many tokens take fewer, which
-// halves h, and the second product reads all parts of it: 16384 tokens of rank 16, two
-// and four, the kernels 38.8 + 62.6 and 35.5 + 65.9, a call 97.9 and 99.6.
+// How many workgroups split K: enough that few tokens still cover the device, up to four
+// and 2048 in all.  us with one and with four: one token of rank 16 7.5 and 5.6, 64 12.0 and 7.8,
+// 1024 18.6 and 15.5, 2048 20.3 and 19.1; 256 of rank 64 31.0 and 19.1 (512 in all measures
+// the same in each of these).  Tokens that go 64 to a workgroup take 512 in all, 16384
+// of them two where more would double h, which the second product reads: one, two and four, rank 16
+// 106, 101 and 100, rank 64 140, 134 and 134, rank 128 191, 175 and 177; 4096 tokens one and four, rank 16 37.5
+// and 26.7, rank 128 81.2 and 68.6.
 int adapter_splits(int64_t M, int64_t K, int64_t R) {
   const int64_t tiles = (M + 15) / 16;
   const bool many = many_tokens(tiles, R);

@@ -246,10 +246,12 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // and the others are checked against each group's own bound (scores without a bias
 // are off by 1.5 |z| U < 2^-16.9 of themselves, or by 2^-126).
 //
-// 16384 tokens of 256 fp32 logits, sigmoid, bias, 4 of 8 groups, 8 experts: 15.6 us (18
-// MB, whose copy takes 3.4; every score in 64 bits took 54).  The comparisons bound it:
-// 16-bit logits without bias or groups take 7.1.  Few tokens are bound by latency: 64 of
-// them 6.1 us, one of bf16 logits 2.9.
+// 16384 tokens of 256 fp32 logits, sigmoid, bias, 4 of 8 groups, 8 experts: 16.1 us (18
+// MB, whose copy takes 3.4; every score in 64 bits took 54).  Vector instructions bind it,
+// most of them comparisons: 1552 a wave of four cycles each, four waves to a SIMD, are 24.8
+// thousand of the 25.5 thousand cycles that a wave lives.  About one row a call is done again by its whole wave
+// (the trace's maximum is 21.7 us).  16-bit logits without bias or groups take 7.1 us.  Few
+// tokens are bound by latency: 64 of them 6.2 us, one of bf16 logits 3.0.
 template <typename T, int L, int VPL, bool EXACT>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
   constexpr int kExact = L == 16 ? VPL < 4 ? 1 : VPL / 4 : VPL;  // experts per lane of a whole wave
@@ -551,7 +553,8 @@ hipError_t route(RouteArgs a) {
   // Many tokens: four to a wave.  Few: a wave each, for its shorter way to an answer.
   // 256 experts with bias and groups, us with 16 lanes and with 64: 2048 tokens 8.8 and
   // 6.8, 4096 8.9 and 8.4, 6000 8.9 and 10.0, 16384 16.4 and 21.2; 64 experts: 2048 6.1
-  // and 5.7, 4096 6.2 and 6.4, 16384 8.9 and 15.2.
+  // and 5.7, 4096 6.2 and 6.4, 16384 8.9 and 15.2.  More than 256 experts take a wave a
+  // token always: 16384 of 384 50 us, of 1024 47 (bf16 without bias and groups 26 and 24).
   if (a.T > 2048 && fits(16, 4)) return route<T, 16, 4>(a);
   if (a.T > 4096 && fits(16, 16)) return route<T, 16, 16>(a);
   if (fits(64, 1)) return route<T, 64, 1>(a);
@@ -650,7 +653,7 @@ __device__ __forceinline__ void exclusive_sums(int (&v)[1024 / THREADS], int* su
 // by counting, over all choices, those of lower experts and the earlier ones of
 // the same: the lanes' comparisons are masks in scalar registers, whose bits
 // the scalar unit counts.  The first workgroup makes the offsets.  64 tokens of 8
-// choices and 4096 bytes: 5.4 us, bound by latency.
+// choices and 4096 bytes: 5.3 us, bound by latency.
 __global__ __launch_bounds__(256) void k_dispatch_few(DispatchArgs a) {
   __shared__ int shared[1024];
   __shared__ int sums[4];
@@ -718,7 +721,8 @@ __global__ __launch_bounds__(256) void k_dispatch_few(DispatchArgs a) {
 // atomics on integers: their order changes nothing), which gives its starts without a
 // word from the others, and ranks its own, 1024 at a time: a wave finds the lanes
 // of each expert bit by bit, and the waves' counts are summed in their order.  32768
-// choices: 8.3 us.
+// choices: 8.3 us.  (The counting is by all workgroups of all choices, so past some hundred
+// thousand of them it grows with their number.)
 __global__ __launch_bounds__(1024) void k_slots(DispatchArgs a) {
   extern __shared__ int wave_counts[];  // [16][E]
   __shared__ int counts[2048], sums[16];  // choices before its own by expert, and the others
