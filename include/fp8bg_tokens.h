@@ -40,7 +40,8 @@ enum { FBG_GROUP_MAX = 0, FBG_GROUP_TOP2 = 1 };
  * Of equal values the lowest index comes first.  What is compared is exact for
  * logits and in 64 bits where a bias is added or scores are summed, so the
  * choice does not hang on a rounding of the scores.  Weights are fp32, off by at most
- * 2^-24 (|largest logit - logit| + topk + 48) of themselves (sigmoid: |logit|).
+ * 2^-24 (|largest logit - logit| + topk + 48) of themselves (sigmoid: |logit|) where the
+ * scores are normal numbers.
  * bias [E] fp32 or NULL; mask [T] bytes or NULL: a token whose byte is not zero
  * gets experts -1 and weights 0.  A row that holds a NaN or +infinity (or with
  * a bias that does), or a softmax of nothing but -infinity, has no routing: its
