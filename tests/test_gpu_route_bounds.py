@@ -20,6 +20,27 @@ def _value(k):
     return float(np.int32(k ^ ((k >> 31) & 0x7fffffff)).view(np.float32))
 
 
+def _check(gpu, z, bias, topk, what, score="sigmoid", groups=1, topk_groups=1):
+    """All rows' experts against the sums in 64 bits, some rows' weights too."""
+    kw = dict(score=score, groups=groups, topk_groups=topk_groups, group_score="top2")
+    weights, experts = gpu.route_experts(z.to(DEV), topk, bias=bias.to(DEV), **kw)
+    zd = z.double().numpy()
+    with np.errstate(over="ignore"):
+        e = np.exp(zd - zd.max(axis=1, keepdims=True))
+        s = e / e.sum(axis=1, keepdims=True) if score == "softmax" else 1 / (1 + np.exp(-zd))
+    c = s + bias.double().numpy()
+    order = np.argsort(-c, axis=1, kind="stable")
+    if groups > 1:
+        best = np.sort(c.reshape(len(c), groups, -1), axis=2)[:, :, -2:].sum(axis=2)
+        dropped = np.ones((len(c), groups), bool)
+        np.put_along_axis(dropped, np.argsort(-best, axis=1, kind="stable")[:, :topk_groups], False, axis=1)
+        out = np.take_along_axis(dropped, order // (c.shape[1] // groups), axis=1)
+        order = np.take_along_axis(order, np.argsort(out, axis=1, kind="stable"), axis=1)
+    wrong = (experts.cpu().numpy() != order[:, :topk]).any(axis=1)
+    assert not wrong.any(), (what, int(wrong.sum()), experts.cpu().numpy()[wrong][:2], order[wrong, :topk][:2])
+    T.assert_route((weights[:20], experts[:20]), T.route(z[:20], topk, bias=bias, **kw), what)
+
+
 def _near_one_border(rows, E, place, centre, width, above, score, seed):
     """(logits, bias, c): per row, `above` experts far above; then, of fp32's numbers
     in runs of `place` (what a comparison that keeps an expert's place in the last
@@ -66,8 +87,7 @@ def _near_one_border(rows, E, place, centre, width, above, score, seed):
 def test_the_last_chosen(gpu, centre, E, place, rows, score, width):
     for seed, above in ((1, 0), (2, 0), (3, 5)):
         z, bias = _near_one_border(rows, E, place, centre, width, above, score, seed)
-        got = gpu.route_experts(z.to(DEV), above + 1, score=score, bias=bias.to(DEV))
-        T.assert_route(got, T.route(z, above + 1, score=score, bias=bias), (centre, E, score, seed))
+        _check(gpu, z, bias, above + 1, (centre, E, score, seed), score)
 
 def _cancelling(rows, E, groups, sizes, spread, seed):
     """Logits and a bias by which each group's two best sum to about one half; group
@@ -105,13 +125,9 @@ def _cancelling(rows, E, groups, sizes, spread, seed):
 def test_two_best_that_cancel(gpu, sizes, spread, E, groups, rows):
     z, bias = _cancelling(rows, E, groups, sizes, spread, E + groups)
     for keep in sorted({1, groups // 2, groups - 1}):
-        kw = dict(score="sigmoid", bias=bias, groups=groups, topk_groups=keep, group_score="top2")
-        got = gpu.route_experts(z.to(DEV), 1, **{**kw, "bias": bias.to(DEV)})
-        # One choice: of the kept groups' experts the largest, which need not tell the groups apart;
-        # as many as are kept, the largest of each.
-        T.assert_route(got, T.route(z, 1, **kw), (sizes, E, keep))
-        got = gpu.route_experts(z.to(DEV), 2 * keep, **{**kw, "bias": bias.to(DEV)})
-        T.assert_route(got, T.route(z, 2 * keep, **kw), (sizes, E, keep))
+        # One choice need not tell the groups apart; as many as two of each kept group do.
+        for topk in (1, 2 * keep):
+            _check(gpu, z, bias, topk, (sizes, E, keep, topk), groups=groups, topk_groups=keep)
 
 
 @pytest.mark.parametrize("rows", [5, 5000])
@@ -127,6 +143,4 @@ def test_two_best_past_the_largest_fp32(gpu, rows, score):
         bias[7, 1:] = -float("inf")
         bias = bias.view(32)
         for keep in (1, 2, 3, 5, 6, 7):
-            kw = dict(score=score, bias=bias, groups=8, topk_groups=keep, group_score="top2")
-            got = gpu.route_experts(z.to(DEV), 2, **{**kw, "bias": bias.to(DEV)})
-            T.assert_route(got, T.route(z, 2, **kw), (sign, keep))
+            _check(gpu, z, bias, 2, (sign, keep), score, 8, keep)
